@@ -40,7 +40,8 @@
  * Ownership and execution: every pointer is device memory owned by the
  * caller.  The library allocates nothing, frees nothing and never
  * synchronizes; every call validates its arguments on the host, enqueues one
- * kernel on the calling thread's stream (mx_set_stream) and returns.  Calls
+ * kernel (mx_cache_attention: one or two) on the calling thread's stream
+ * (mx_set_stream) and returns.  Calls
  * are therefore safe to capture in a HIP graph.  dst == src (an exact alias)
  * is allowed for mx_qdq; any other overlap between inputs and outputs is
  * undefined.  Faults inside a kernel surface at the caller's next
@@ -91,7 +92,10 @@ extern "C" {
 #define MX_ENULL (-5)   /* a required pointer is NULL                       */
 #define MX_EALIGN (-6)  /* a pointer breaks the alignment stated above      */
 #define MX_ELAUNCH (-7) /* the kernel launch failed (hipGetLastError)       */
-#define MX_ELAYOUT (-8) /* scale_layout is not one of MX_SCALES_*           */
+#define MX_ELAYOUT (-8) /* scale_layout is not one of MX_SCALES_*, or a
+                           rotary layout not one of MX_ROTARY_*             */
+#define MX_EARG (-9)    /* a rotary, cache or attention argument is outside
+                           the range stated at its call                     */
 
 /* Scale layouts. */
 #define MX_SCALES_ROWMAJOR 0 /* [M x K/32] bytes, row-major, unpadded      */
@@ -245,6 +249,119 @@ MX_API int mx_nvfp4_dequantize(const uint8_t *codes, const uint8_t *scales,
                                int64_t M, int64_t K,
                                const float *global_scale, int dst_dtype,
                                void *dst);
+
+/*
+ * Rotary positions.  On the first `rot` dimensions of every head, pair p of
+ * rot/2 is turned by the angle positions[token] * inv_freq[p]:
+ *   a' = a c - b s,  b' = b c + a s,  c, s = scale * cos, scale * sin;
+ * the other dimensions are copied.  With inverse != 0 s is negated: the
+ * transposed rotation, which takes the gradient of y to that of x.
+ *   src, dst   [tokens x heads x dim] in dtype, dimensions contiguous; token
+ *              and head strides in elements, so that a head range of a wider
+ *              row can be passed.  dst == src is allowed with equal strides;
+ *              any other overlap is undefined.  Any alignment; 16-byte
+ *              pointers, strides and halves are fastest.
+ *   positions  [tokens] int64; inv_freq [rot/2] fp64 (scaled for long contexts
+ *              by the caller).  Angles are formed and reduced in fp64 (accurate
+ *              below 2^50 rad) and rounded once to fp32.
+ *   rot        even, 0 <= rot <= dim <= 4096 (MX_EARG).
+ *   layout     MX_ROTARY_HALF: pair p is dimensions p and p + rot/2;
+ *              MX_ROTARY_INTERLEAVED: dimensions 2p and 2p + 1.
+ */
+#define MX_ROTARY_HALF 0
+#define MX_ROTARY_INTERLEAVED 1
+
+MX_API int mx_rope(const void *src, int64_t src_token_stride,
+                   int64_t src_head_stride, int dtype, int64_t tokens,
+                   int64_t heads, int64_t dim, const int64_t *positions,
+                   const double *inv_freq, int64_t rot, int layout,
+                   double scale, int inverse, void *dst,
+                   int64_t dst_token_stride, int64_t dst_head_stride);
+
+/*
+ * Paged MX cache of keys and values.  A plain description: the caller owns
+ * the memory and may keep the struct where it likes (it is read during the
+ * call only).
+ *   page       tokens of a page: a power of two, 16 to 65536.
+ *   dim        a multiple of 32, 32 to 256; pages * heads * page * dim <= 2^46.
+ *   codes      [pages x heads x page x dim] bytes (E4M3) or
+ *              [pages x heads x page x dim/2] (E2M1, the even dimension in
+ *              bits 3:0); 16-byte aligned.
+ *   scales     [pages x heads x dim/32 x page] E8M0 bytes, one for each 32
+ *              dimensions of a token; 16-byte aligned.
+ * Token slots are page number * page + row.
+ */
+typedef struct mx_cache {
+  int32_t fmt, heads, page, dim;
+  int64_t pages;
+  uint8_t *k_codes, *k_scales, *v_codes, *v_scales;
+} mx_cache;
+
+/*
+ * Quantise new keys and values into their slots (the scale and element rules
+ * of mx_quantize).  With rot > 0 the keys are rotated first (as by mx_rope, in
+ * fp64) and rounded to bf16.
+ *   k, v       [tokens x heads x dim] bf16, strides in elements as above.
+ *   slots      [tokens] int64; a slot outside the cache (a negative one, say)
+ *              is skipped.  Two tokens with one slot leave either's bytes.
+ */
+MX_API int mx_cache_write(const mx_cache *cache, const void *k,
+                          int64_t k_token_stride, int64_t k_head_stride,
+                          const void *v, int64_t v_token_stride,
+                          int64_t v_head_stride, const int64_t *slots,
+                          int64_t tokens, const int64_t *positions,
+                          const double *inv_freq, int64_t rot, int layout,
+                          double scale);
+
+/*
+ * Read slots back: k, v [tokens x heads x dim] bf16, contiguous, 16-byte
+ * aligned; values rounded to nearest-even.  A slot outside the cache gives
+ * zeros.
+ */
+MX_API int mx_cache_read(const mx_cache *cache, const int64_t *slots,
+                         int64_t tokens, void *k, void *v);
+
+/*
+ * Attention over the cache: out[i] = softmax_j(scale * q[i] . k[j]) v[j].
+ * Query head h reads key/value head h / (q_heads / cache->heads).
+ * Sequence b has the queries q_starts[b] .. q_starts[b+1] - 1 and
+ * kv_lens[b] tokens in the cache, of which its new ones (one for each query)
+ * are the last; token t is in page block_table[b][t / page], row t % page.
+ * A query sees every token before the new ones, and of these
+ *   tree == NULL  the ones up to its own;
+ *   otherwise     the ones whose bits are set in its row: new token j is bit
+ *                 j % 64 of word j / 64 of tree[query * tree_words ..].
+ * A query that sees nothing gives zeros; what it does not see has no part in
+ * its result, NaN included.  Tokens of a page that is not in the cache count
+ * as not seen.
+ *   q          [total_q x q_heads x dim] bf16, 16-byte aligned, strides (in
+ *              elements) multiples of 8; out the same, contiguous.
+ *   q_starts   [batch + 1] int32, ascending from 0; kv_lens [batch] int32;
+ *              block_table [batch x table_stride] int32, of which the first
+ *              table_pages of a row may be read; tree [total_q x tree_words].
+ *   max_q, max_kv  at least the most queries and tokens of a sequence: what is
+ *              beyond them is not computed.
+ *   workspace  mx_cache_attention_workspace bytes, 16-byte aligned, contents
+ *              free; it may be NULL where that is 0.
+ * dim is 64, 96, 128, 192 or 256 and scale is positive and finite (MX_EARG);
+ * scores, weights' sums and output sums are fp32, weights are rounded to bf16
+ * for their products with the values.  Enqueues one kernel, or two where the
+ * tokens are split over workgroups.
+ */
+MX_API int64_t mx_cache_attention_workspace(const mx_cache *cache,
+                                            int64_t q_heads, int64_t batch,
+                                            int64_t total_q, int64_t max_q,
+                                            int64_t max_kv);
+MX_API int mx_cache_attention(const mx_cache *cache, const void *q,
+                              int64_t q_token_stride, int64_t q_head_stride,
+                              int64_t q_heads, const int32_t *q_starts,
+                              const int32_t *kv_lens, int64_t batch,
+                              const int32_t *block_table, int64_t table_stride,
+                              int64_t table_pages, int64_t total_q,
+                              int64_t max_q, int64_t max_kv,
+                              const int64_t *tree, int64_t tree_words,
+                              float scale, void *out, void *workspace,
+                              int64_t workspace_bytes);
 
 /* Stream used by the calling thread's subsequent calls (a hipStream_t;
  * NULL = the default stream).  The setting is thread-local. */

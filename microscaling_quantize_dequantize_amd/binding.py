@@ -32,6 +32,7 @@ _lib = ctypes.CDLL(LIB_PATH)
 E2M1, E4M3 = 0, 1
 BF16, F32 = 0, 1
 ROWMAJOR, BLOCKED = 0, 1
+HALF, INTERLEAVED = 0, 1
 _DTYPE = {torch.bfloat16: BF16, torch.float32: F32}
 
 _vp, _i64, _int = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int
@@ -47,13 +48,22 @@ _lib.mx_quantize_blocked.argtypes = [_int, _vp, _i64, _i64, _vp, _int, _vp, _vp]
 _lib.mx_nvfp4_quantize.argtypes = [_vp, _i64, _i64, _vp, _int, _vp, _vp, _vp]
 _lib.mx_nvfp4_qdq.argtypes = [_vp, _i64, _i64, _vp, _int, _vp, _vp]
 _lib.mx_nvfp4_dequantize.argtypes = [_vp, _vp, _i64, _i64, _vp, _int, _vp]
+_dbl = ctypes.c_double
+_lib.mx_rope.argtypes = [_vp, _i64, _i64, _int, _i64, _i64, _i64, _vp, _vp, _i64, _int, _dbl, _int, _vp, _i64, _i64]
+_lib.mx_cache_write.argtypes = [_vp, _vp, _i64, _i64, _vp, _i64, _i64, _vp, _i64, _vp, _vp, _i64, _int, _dbl]
+_lib.mx_cache_read.argtypes = [_vp, _vp, _i64, _vp, _vp]
+_lib.mx_cache_attention_workspace.argtypes = [_vp, _i64, _i64, _i64, _i64, _i64]
+_lib.mx_cache_attention_workspace.restype = _i64
+_lib.mx_cache_attention.argtypes = [_vp, _vp, _i64, _i64, _i64, _vp, _vp, _i64, _vp, _i64, _i64, _i64, _i64, _i64, _vp,
+                                    _i64, ctypes.c_float, _vp, _vp, _i64]
 _lib.mx_set_stream.argtypes = [_vp]
 _lib.mx_get_stream.restype = _vp
 _lib.mx_status_string.argtypes = [_int]
 _lib.mx_status_string.restype = ctypes.c_char_p
 for _f in (_lib.mx_qdq, _lib.mx_quantize, _lib.mx_dequantize, _lib.mx_rotate, _lib.mx_matmul,
            _lib.mx_scales_to_blocked, _lib.mx_quantize_blocked, _lib.mx_nvfp4_quantize, _lib.mx_nvfp4_qdq,
-           _lib.mx_nvfp4_dequantize):
+           _lib.mx_nvfp4_dequantize, _lib.mx_rope, _lib.mx_cache_write, _lib.mx_cache_read,
+           _lib.mx_cache_attention):
     _f.restype = _int
 
 
@@ -344,6 +354,208 @@ def mx_nvfp4_dequantize(codes: torch.Tensor, scales: torch.Tensor, K: int, globa
     _stream()
     _call(_lib.mx_nvfp4_dequantize(pc, pq, M, K, pg, _DTYPE[dst.dtype], pd))
     return dst
+
+
+# ---- rotary positions, the paged MX cache and attention over it ---------------
+
+
+def _heads(t, name: str, dtypes, shape=None):
+    """t must be [tokens, heads, dim] with contiguous dimensions (any token and head strides) on the current
+    device."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch tensor")
+    if t.dtype not in dtypes:
+        raise ValueError(f"{name} must be {' or '.join(str(d) for d in dtypes)}, got {t.dtype}")
+    if t.dim() != 3 or (shape is not None and tuple(t.shape) != tuple(shape)):
+        raise ValueError(f"{name} must have shape {'[tokens, heads, dim]' if shape is None else tuple(shape)}, "
+                         f"got {tuple(t.shape)}")
+    if t.shape[2] > 1 and t.stride(2) != 1:
+        raise ValueError(f"the dimensions of {name} must be contiguous")
+    _place(t, name)
+    return t.data_ptr(), t.stride(0), t.stride(1)
+
+
+def _place(t: torch.Tensor, name: str) -> None:
+    if not t.is_cuda:
+        raise TypeError(f"{name} must be a GPU tensor")
+    if t.device.index != torch.cuda.current_device():
+        raise ValueError(f"{name} is on {t.device}, the current device is cuda:{torch.cuda.current_device()}")
+
+
+def _vector(t, name: str, dtype: torch.dtype, n: int) -> int:
+    _want(t, name, dtype, (n,))
+    return _dev(t, name)
+
+
+def _rotary(positions, inv_freq, tokens: int):
+    """Pointers of the positions and frequencies, and the number of rotated dimensions."""
+    if not isinstance(inv_freq, torch.Tensor) or inv_freq.dtype != torch.float64 or inv_freq.dim() != 1:
+        raise ValueError("inv_freq must be a one-dimensional float64 tensor (angle per position of each pair)")
+    return _vector(positions, "positions", torch.int64, tokens), _dev(inv_freq, "inv_freq"), 2 * inv_freq.numel()
+
+
+def mx_rope(x: torch.Tensor, positions: torch.Tensor, inv_freq: torch.Tensor, layout: int = HALF, scale: float = 1.0,
+            inverse: bool = False, dst: torch.Tensor | None = None) -> torch.Tensor:
+    """Rotary positions on the first 2 * len(inv_freq) dimensions of x [tokens, heads, dim] (bf16 or fp32, any token
+    and head strides), the others copied.
+
+    positions int64 [tokens]; inv_freq float64 [pairs]; layout HALF (dimension p with p + pairs) or INTERLEAVED
+    (2p with 2p + 1); scale multiplies the rotated dimensions.  inverse: the transposed rotation, which takes the
+    gradient of the output to that of x.  dst may be x itself."""
+    ps, st, sh = _heads(x, "x", (torch.bfloat16, torch.float32))
+    if dst is None:
+        dst = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    pd, dt, dh = _heads(dst, "dst", (x.dtype,), x.shape)
+    pp, pf, rot = _rotary(positions, inv_freq, x.shape[0])
+    _stream()
+    _call(_lib.mx_rope(ps, st, sh, _DTYPE[x.dtype], *x.shape, pp, pf, rot, layout, scale, 1 if inverse else 0, pd, dt,
+                       dh))
+    return dst
+
+
+class _CacheStruct(ctypes.Structure):
+    _fields_ = [("fmt", ctypes.c_int32), ("heads", ctypes.c_int32), ("page", ctypes.c_int32), ("dim", ctypes.c_int32),
+                ("pages", _i64), ("k_codes", _vp), ("k_scales", _vp), ("v_codes", _vp), ("v_scales", _vp)]
+
+
+class MXCache:
+    """A paged cache of keys and values in MX codes over the caller's tensors.
+
+    fmt E2M1 or E4M3; codes uint8 [pages, heads, page, dim/2 or dim]; scales uint8 [pages, heads, dim/32, page].
+    Token slots are page number * page + row.  The handle keeps the four tensors; it may be used on any stream."""
+
+    def __init__(self, fmt: int, k_codes: torch.Tensor, k_scales: torch.Tensor, v_codes: torch.Tensor,
+                 v_scales: torch.Tensor):
+        if fmt not in (E2M1, E4M3):
+            raise ValueError("fmt must be E2M1 or E4M3")
+        if not isinstance(k_codes, torch.Tensor) or k_codes.dim() != 4:
+            raise ValueError("k_codes must be a 4-D uint8 tensor [pages, heads, page, dim/2 or dim]")
+        pages, heads, page, cols = k_codes.shape
+        dim = 2 * cols if fmt == E2M1 else cols
+        if dim % 32 or not 32 <= dim <= 256:
+            raise ValueError(f"the head's dimension must be a multiple of 32 up to 256, got {dim}")
+        if page < 16 or page > 65536 or page & (page - 1):
+            raise ValueError(f"a page must hold a power of two of tokens, 16 at least, got {page}")
+        _want(k_codes, "k_codes", torch.uint8, (pages, heads, page, cols))
+        _want(v_codes, "v_codes", torch.uint8, (pages, heads, page, cols))
+        _want(k_scales, "k_scales", torch.uint8, (pages, heads, dim // 32, page))
+        _want(v_scales, "v_scales", torch.uint8, (pages, heads, dim // 32, page))
+        ptrs = [_dev(t, n) for t, n in ((k_codes, "k_codes"), (k_scales, "k_scales"), (v_codes, "v_codes"),
+                                        (v_scales, "v_scales"))]
+        self.fmt, self.pages, self.heads, self.page, self.dim = fmt, pages, heads, page, dim
+        self.k_codes, self.k_scales, self.v_codes, self.v_scales = k_codes, k_scales, v_codes, v_scales
+        self.device = k_codes.device
+        self._struct = _CacheStruct(fmt, heads, page, dim, pages, *ptrs)
+        self._ref = ctypes.addressof(self._struct)
+
+    @classmethod
+    def allocate(cls, fmt: int, pages: int, heads: int, page: int, dim: int, device="cuda") -> "MXCache":
+        """A cache of new tensors, all values zero."""
+        cols = _code_cols(fmt, dim)
+
+        def zeros(*shape):
+            return torch.zeros(shape, dtype=torch.uint8, device=device)
+
+        return cls(fmt, zeros(pages, heads, page, cols), zeros(pages, heads, dim // 32, page),
+                   zeros(pages, heads, page, cols), zeros(pages, heads, dim // 32, page))
+
+
+def _cache(cache) -> int:
+    if not isinstance(cache, MXCache):
+        raise TypeError("cache must be an MXCache")
+    _place(cache.k_codes, "cache")
+    return cache._ref
+
+
+def mx_cache_write(cache: MXCache, k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor,
+                   positions: torch.Tensor | None = None, inv_freq: torch.Tensor | None = None, layout: int = HALF,
+                   scale: float = 1.0) -> None:
+    """Quantise keys and values [tokens, heads, dim] (bf16, any token and head strides) into the cache's slots
+    (int64 [tokens]; slots outside the cache are skipped).  With positions and inv_freq the keys are rotated first, as
+    by mx_rope, and rounded to bf16."""
+    pc = _cache(cache)
+    pk, kt, kh = _heads(k, "k", (torch.bfloat16,))
+    shape = (k.shape[0], cache.heads, cache.dim)
+    if tuple(k.shape) != shape:
+        raise ValueError(f"k must have shape {shape}, got {tuple(k.shape)}")
+    pv, vt, vh = _heads(v, "v", (torch.bfloat16,), shape)
+    ps = _vector(slots, "slots", torch.int64, shape[0])
+    if (positions is None) != (inv_freq is None):
+        raise ValueError("positions and inv_freq go together")
+    pp, pf, rot = (None, None, 0) if positions is None else _rotary(positions, inv_freq, shape[0])
+    _stream()
+    _call(_lib.mx_cache_write(pc, pk, kt, kh, pv, vt, vh, ps, shape[0], pp, pf, rot, layout, scale))
+
+
+def mx_cache_read(cache: MXCache, slots: torch.Tensor, k: torch.Tensor | None = None, v: torch.Tensor | None = None):
+    """Keys and values of slots (int64 [tokens]) as bf16 [tokens, heads, dim]; zeros for slots outside the cache."""
+    pc = _cache(cache)
+    if not isinstance(slots, torch.Tensor) or slots.dim() != 1:
+        raise ValueError("slots must be a one-dimensional int64 tensor")
+    shape = (slots.shape[0], cache.heads, cache.dim)
+    if k is None:
+        k = torch.empty(shape, dtype=torch.bfloat16, device=slots.device)
+    if v is None:
+        v = torch.empty(shape, dtype=torch.bfloat16, device=slots.device)
+    _want(k, "k", torch.bfloat16, shape)
+    _want(v, "v", torch.bfloat16, shape)
+    ps, pk, pv = _vector(slots, "slots", torch.int64, shape[0]), _dev(k, "k"), _dev(v, "v")
+    _stream()
+    _call(_lib.mx_cache_read(pc, ps, shape[0], pk, pv))
+    return k, v
+
+
+def mx_cache_attention(cache: MXCache, q: torch.Tensor, q_starts: torch.Tensor, kv_lens: torch.Tensor,
+                       block_table: torch.Tensor, max_q: int, max_kv: int, tree: torch.Tensor | None = None,
+                       scale: float | None = None, out: torch.Tensor | None = None) -> torch.Tensor:
+    """Attention of new tokens over the cache: q [total_q, q_heads, dim] (bf16, any token and head strides that are
+    multiples of 8) -> bf16 [total_q, q_heads, dim].
+
+    Sequence b has the queries q_starts[b] .. q_starts[b + 1] (int32 [batch + 1]), and kv_lens[b] tokens (int32
+    [batch]), of which the last are its new ones, one for each query; token t is in page block_table[b, t // page]
+    (int32 [batch, pages of the longest], rows contiguous).  A query sees all tokens before the new ones, and of the
+    new ones those up to its own, or with tree (int64 [total_q, words]) new token j where bit j % 64 of word j // 64 of
+    its row is set.  A query that sees nothing gives zeros.  max_q, max_kv: at least the most queries and tokens of a
+    sequence (what is beyond is not computed).  scale: dim ** -0.5 if not given."""
+    pc = _cache(cache)
+    pq, qt, qh = _heads(q, "q", (torch.bfloat16,))
+    total, heads, dim = q.shape
+    if dim != cache.dim or heads % cache.heads:
+        raise ValueError(f"q must have {cache.dim} dimensions and a multiple of {cache.heads} heads, got "
+                         f"{tuple(q.shape)}")
+    if not isinstance(kv_lens, torch.Tensor) or kv_lens.dim() != 1:
+        raise ValueError("kv_lens must be a one-dimensional int32 tensor")
+    batch = kv_lens.shape[0]
+    pl = _vector(kv_lens, "kv_lens", torch.int32, batch)
+    pst = _vector(q_starts, "q_starts", torch.int32, batch + 1)
+    if not isinstance(block_table, torch.Tensor) or block_table.dtype != torch.int32 or block_table.dim() != 2 \
+            or block_table.shape[0] != batch or (block_table.shape[1] > 1 and block_table.stride(1) != 1):
+        raise ValueError("block_table must be an int32 tensor [batch, pages] with contiguous rows")
+    _place(block_table, "block_table")
+    pages = block_table.shape[1]
+    stride = block_table.stride(0) if batch > 1 else pages
+    pt, words = None, 0
+    if tree is not None:
+        if not isinstance(tree, torch.Tensor) or tree.dim() != 2:
+            raise ValueError("tree must be an int64 tensor [total_q, words]")
+        words = tree.shape[1]
+        _want(tree, "tree", torch.int64, (total, words))
+        if 64 * words < max_q:
+            raise ValueError(f"tree has {words} words a row, max_q = {max_q} new tokens need {-(-max_q // 64)}")
+        pt = _dev(tree, "tree")
+    if out is None:
+        out = torch.empty((total, heads, dim), dtype=torch.bfloat16, device=q.device)
+    _want(out, "out", torch.bfloat16, (total, heads, dim))
+    po = _dev(out, "out")
+    need = _lib.mx_cache_attention_workspace(pc, heads, batch, total, max_q, max_kv)
+    if need < 0:
+        raise MXError(need)
+    space = torch.empty(need, dtype=torch.uint8, device=q.device) if need else None
+    _stream()
+    _call(_lib.mx_cache_attention(pc, pq, qt, qh, heads, pst, pl, batch, block_table.data_ptr(), stride, pages, total,
+                                  max_q, max_kv, pt, words, dim ** -0.5 if scale is None else scale, po,
+                                  space.data_ptr() if need else None, need))
+    return out
 
 
 def raw():

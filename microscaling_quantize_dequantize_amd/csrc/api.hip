@@ -217,6 +217,137 @@ MX_API int mx_nvfp4_dequantize(const uint8_t *codes, const uint8_t *scales, int6
   return launched(mx::launch_nv_dequant(dst_dtype, codes, scales, global_scale, dst, M * K, tl_stream));
 }
 
+namespace {
+
+bool fits(int64_t v, int64_t most) { return v >= 0 && v <= most; }
+
+int check_rotary(int64_t dim, const int64_t *positions, const double *inv_freq, int64_t rot, int layout) {
+  if (rot < 0 || rot % 2 != 0 || rot > dim) return MX_EARG;
+  if (layout != MX_ROTARY_HALF && layout != MX_ROTARY_INTERLEAVED) return MX_ELAYOUT;
+  if (rot > 0 && (!aligned(positions, 8) || !aligned(inv_freq, 8))) return MX_EALIGN;
+  return MX_OK;
+}
+
+int check_cache(const mx_cache *c) {
+  if (!c) return MX_ENULL;
+  int st = check_fmt(c->fmt);
+  if (st) return st;
+  if (c->dim < 32 || c->dim > 256 || c->dim % 32 != 0 || c->heads < 1 || c->heads > 65535 || c->page < 16 ||
+      c->page > 65536 || (c->page & (c->page - 1)) != 0 || c->pages < 0 || c->pages > INT32_MAX ||
+      c->pages > MAX_ELEMS / ((int64_t)c->heads * c->page * c->dim))
+    return MX_ESHAPE;
+  if (!aligned(c->k_codes, 16) || !aligned(c->k_scales, 16) || !aligned(c->v_codes, 16) || !aligned(c->v_scales, 16))
+    return MX_EALIGN;
+  return MX_OK;
+}
+
+bool empty_cache(const mx_cache *c) { return !c->k_codes || !c->k_scales || !c->v_codes || !c->v_scales; }
+
+mx::CacheView view(const mx_cache *c) {
+  return mx::CacheView{{c->k_codes, c->v_codes}, {c->k_scales, c->v_scales}, c->pages, c->fmt, c->heads, c->dim,
+                       __builtin_ctz((unsigned)c->page)};
+}
+
+int check_attention(const mx_cache *c, int64_t q_heads, int64_t batch, int64_t total_q, int64_t max_q,
+                    int64_t max_kv) {
+  int st = check_cache(c);
+  if (st) return st;
+  if (c->dim != 64 && c->dim != 96 && c->dim != 128 && c->dim != 192 && c->dim != 256) return MX_EARG;
+  if (q_heads < 1 || q_heads % c->heads != 0 || q_heads > 65535) return MX_ESHAPE;
+  if (!fits(batch, 1 << 24) || !fits(total_q, INT32_MAX / q_heads) || !fits(max_q, INT32_MAX / q_heads) ||
+      !fits(max_kv, INT32_MAX - 65536))
+    return MX_ESHAPE;
+  return MX_OK;
+}
+
+}  // namespace
+
+MX_API int mx_rope(const void *src, int64_t src_token_stride, int64_t src_head_stride, int dtype, int64_t tokens,
+                   int64_t heads, int64_t dim, const int64_t *positions, const double *inv_freq, int64_t rot,
+                   int layout, double scale, int inverse, void *dst, int64_t dst_token_stride,
+                   int64_t dst_head_stride) {
+  int st;
+  if ((st = check_dtype(dtype))) return st;
+  if (tokens < 0 || !fits(heads, 65535) || !fits(dim, 4096) || tokens > INT32_MAX) return MX_ESHAPE;
+  if ((st = check_rotary(dim, positions, inv_freq, rot, layout))) return st;
+  if (tokens == 0 || heads == 0 || dim == 0) return MX_OK;
+  if (!src || !dst || (rot > 0 && (!positions || !inv_freq))) return MX_ENULL;
+  const uintptr_t size = dtype == MX_DTYPE_F32 ? 4 : 2;
+  if (!aligned(src, size) || !aligned(dst, size)) return MX_EALIGN;
+  if (src == dst) {
+    if (src_token_stride != dst_token_stride || src_head_stride != dst_head_stride) return MX_EARG;
+    if (rot == 0) return MX_OK;
+  }
+  const int64_t strides[4] = {src_token_stride, src_head_stride, dst_token_stride, dst_head_stride};
+  return launched(mx::launch_rope(dtype, src, dst, tokens, heads, dim, strides, positions, inv_freq, rot, layout, scale,
+                                  inverse, tl_stream));
+}
+
+MX_API int mx_cache_write(const mx_cache *cache, const void *k, int64_t k_token_stride, int64_t k_head_stride,
+                          const void *v, int64_t v_token_stride, int64_t v_head_stride, const int64_t *slots,
+                          int64_t tokens, const int64_t *positions, const double *inv_freq, int64_t rot, int layout,
+                          double scale) {
+  int st;
+  if ((st = check_cache(cache))) return st;
+  if (!fits(tokens, INT32_MAX)) return MX_ESHAPE;
+  if ((st = check_rotary(cache->dim, positions, inv_freq, rot, layout))) return st;
+  if (tokens == 0 || cache->pages == 0) return MX_OK;
+  if (empty_cache(cache) || !k || !v || !slots || (rot > 0 && (!positions || !inv_freq))) return MX_ENULL;
+  if (!aligned(k, 2) || !aligned(v, 2) || !aligned(slots, 8)) return MX_EALIGN;
+  const int64_t ks[2] = {k_token_stride, k_head_stride}, vs[2] = {v_token_stride, v_head_stride};
+  return launched(mx::launch_cache_write(view(cache), k, ks, v, vs, slots, tokens, positions, inv_freq, rot, layout,
+                                         scale, tl_stream));
+}
+
+MX_API int mx_cache_read(const mx_cache *cache, const int64_t *slots, int64_t tokens, void *k, void *v) {
+  int st;
+  if ((st = check_cache(cache))) return st;
+  if (!fits(tokens, INT32_MAX)) return MX_ESHAPE;
+  if (tokens == 0) return MX_OK;
+  if ((cache->pages > 0 && empty_cache(cache)) || !slots || !k || !v) return MX_ENULL;
+  if (!aligned(slots, 8) || !aligned(k, 16) || !aligned(v, 16)) return MX_EALIGN;
+  return launched(mx::launch_cache_read(view(cache), slots, tokens, k, v, tl_stream));
+}
+
+MX_API int64_t mx_cache_attention_workspace(const mx_cache *cache, int64_t q_heads, int64_t batch, int64_t total_q,
+                                            int64_t max_q, int64_t max_kv) {
+  const int st = check_attention(cache, q_heads, batch, total_q, max_q, max_kv);
+  if (st) return st;
+  if (max_q > total_q) max_q = total_q;
+  return mx::attention_workspace(cache->fmt, cache->dim, cache->heads, (int)(q_heads / cache->heads), (int)batch,
+                                 total_q, max_q, max_kv);
+}
+
+MX_API int mx_cache_attention(const mx_cache *cache, const void *q, int64_t q_token_stride, int64_t q_head_stride,
+                              int64_t q_heads, const int32_t *q_starts, const int32_t *kv_lens, int64_t batch,
+                              const int32_t *block_table, int64_t table_stride, int64_t table_pages, int64_t total_q,
+                              int64_t max_q, int64_t max_kv, const int64_t *tree, int64_t tree_words, float scale,
+                              void *out, void *workspace, int64_t workspace_bytes) {
+  int st;
+  if ((st = check_attention(cache, q_heads, batch, total_q, max_q, max_kv))) return st;
+  if (!fits(table_pages, INT32_MAX / cache->page) || table_stride < table_pages || !fits(tree_words, INT32_MAX))
+    return MX_ESHAPE;
+  if (!(scale > 0.0f && scale <= 3.402823466e38f)) return MX_EARG;
+  if (batch == 0 || total_q == 0 || max_q == 0) return MX_OK;
+  if (!q || !q_starts || !kv_lens || !out) return MX_ENULL;
+  if (max_kv > 0 && table_pages > 0 && (!block_table || cache->pages == 0 || empty_cache(cache))) return MX_ENULL;
+  if (!aligned(q, 16) || !aligned(out, 16) || q_token_stride % 8 != 0 || q_head_stride % 8 != 0 ||
+      !aligned(q_starts, 4) || !aligned(kv_lens, 4) || !aligned(block_table, 4) || !aligned(tree, 8))
+    return MX_EALIGN;
+  const int group = (int)(q_heads / cache->heads);
+  if (max_q > total_q) max_q = total_q;
+  const int64_t need = mx::attention_workspace(cache->fmt, cache->dim, cache->heads, group, (int)batch, total_q, max_q,
+                                               max_kv);
+  if (need > 0 && !workspace) return MX_ENULL;
+  if (workspace_bytes < need) return MX_EARG;
+  if (need > 0 && !aligned(workspace, 16)) return MX_EALIGN;
+  const mx::AttentionArgs a{view(cache), (const unsigned short *)q, (unsigned short *)out, q_token_stride,
+                            q_head_stride, q_starts, kv_lens, block_table, tree, table_stride, (float *)workspace,
+                            (int)batch, group, (int)table_pages, (int)total_q, (int)max_q, (int)max_kv,
+                            (int)tree_words, scale};
+  return launched(mx::launch_cache_attention(a, tl_stream));
+}
+
 MX_API void mx_set_stream(void *stream) { tl_stream = (hipStream_t)stream; }
 
 MX_API void *mx_get_stream(void) { return (void *)tl_stream; }
@@ -231,7 +362,10 @@ MX_API const char *mx_status_string(int status) {
     case MX_ENULL: return "a required pointer is NULL";
     case MX_EALIGN: return "misaligned pointer (16 bytes; scales 4 bytes)";
     case MX_ELAUNCH: return "kernel launch failed";
-    case MX_ELAYOUT: return "invalid scale layout (expected MX_SCALES_ROWMAJOR or MX_SCALES_BLOCKED)";
+    case MX_ELAYOUT:
+      return "invalid layout (expected MX_SCALES_ROWMAJOR or MX_SCALES_BLOCKED; rotary: MX_ROTARY_HALF or "
+             "MX_ROTARY_INTERLEAVED)";
+    case MX_EARG: return "invalid rotary, cache or attention argument";
     default: return "unknown status";
   }
 }

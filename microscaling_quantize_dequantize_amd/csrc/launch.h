@@ -50,4 +50,41 @@ hipError_t launch_gemm(int fmt, const uint8_t *a, const uint8_t *as, const uint8
                        int scale_layout, int64_t M, int64_t N, int64_t K, float alpha, int out_dtype, void *c,
                        hipStream_t stream);
 
+// Rotary positions (strides: src token, src head, dst token, dst head, in elements).
+hipError_t launch_rope(int dtype, const void *src, void *dst, int64_t tokens, int64_t heads, int64_t dim,
+                       const int64_t strides[4], const int64_t *positions, const double *inv_freq, int64_t rot,
+                       int layout, double scale, int inverse, hipStream_t stream);
+
+// The paged cache as the kernels take it: [0] keys, [1] values.
+struct CacheView {
+  uint8_t *codes[2], *scales[2];
+  int64_t pages;
+  int fmt, heads, dim, page_log2;
+};
+
+// Strides: token, head, in elements.
+hipError_t launch_cache_write(const CacheView &cache, const void *k, const int64_t k_strides[2], const void *v,
+                              const int64_t v_strides[2], const int64_t *slots, int64_t tokens,
+                              const int64_t *positions, const double *inv_freq, int64_t rot, int layout, double scale,
+                              hipStream_t stream);
+hipError_t launch_cache_read(const CacheView &cache, const int64_t *slots, int64_t tokens, void *k, void *v,
+                             hipStream_t stream);
+
+struct AttentionArgs {
+  CacheView cache;
+  const unsigned short *q;
+  unsigned short *out;
+  int64_t q_token, q_head;  // strides in elements
+  const int *q_starts, *kv_lens, *table;
+  const int64_t *tree;  // nullptr: causal
+  int64_t table_stride;
+  float *partial;  // workspace
+  int batch, group, table_pages, total_q, max_q, max_kv, tree_words;
+  float scale;
+};
+
+int64_t attention_workspace(int fmt, int dim, int heads, int group, int batch, int64_t total_q, int64_t max_q,
+                            int64_t max_kv);
+hipError_t launch_cache_attention(const AttentionArgs &a, hipStream_t stream);
+
 }  // namespace mx

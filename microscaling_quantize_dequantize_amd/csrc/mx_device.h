@@ -331,6 +331,16 @@ __device__ __forceinline__ unsigned dpp(unsigned v) {
 
 __device__ __forceinline__ unsigned umax(unsigned a, unsigned b) { return a > b ? a : b; }
 
+// Sign-cleared u16 maximum of the 8 bf16 values in a piece.
+__device__ __forceinline__ unsigned piece_amax_bf16(u32x4 w) {
+  u16x2 a = __builtin_bit_cast(u16x2, w.x & 0x7FFF7FFFu);
+  u16x2 b = __builtin_bit_cast(u16x2, w.y & 0x7FFF7FFFu);
+  u16x2 c = __builtin_bit_cast(u16x2, w.z & 0x7FFF7FFFu);
+  u16x2 d = __builtin_bit_cast(u16x2, w.w & 0x7FFF7FFFu);
+  u16x2 m = __builtin_elementwise_max(__builtin_elementwise_max(a, b), __builtin_elementwise_max(c, d));
+  return umax(m[0], m[1]);
+}
+
 // Max of v over lanes l and l^32 (v_permlane32_swap exchanges the upper
 // half-wave of its first operand with the lower half-wave of its second).
 __device__ __forceinline__ unsigned max_across_halves(unsigned v) {

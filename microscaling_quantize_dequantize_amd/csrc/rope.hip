@@ -1,0 +1,156 @@
+// Rotary positions: y = R(position) x on the first `rot` dimensions of every
+// head, the rest copied, and the inverse rotation for gradients.
+//
+//   pair p of rot/2:  a' = a c - b s,  b' = b c + a s,
+//   c, s = scale cos, scale sin of position * inv_freq[p];  the inverse takes
+//   -s, which is the transposed rotation, so it gives the gradient of x from
+//   that of y.
+//
+// Bound: HBM, one read and one write of x (3 flops a rotated element).  The
+// angles are formed once for each (token, pair) in fp64, rounded once to fp32
+// and kept in LDS for all heads of the token, whose pairs are rotated in fp32
+// whatever the type of x.
+//
+// Split: a workgroup owns whole tokens (one, or several while their heads are
+// few), a thread VEC neighbouring pairs of one head, so that both elements of
+// a pair are read before either is written and dst may be src.
+#include "launch.h"
+#include "rotary.h"
+
+namespace mx {
+
+constexpr int ROPE_THREADS = 256;
+constexpr int ROPE_TABLE = 2048;  // (token, pair) entries of a workgroup's table: 16 KiB of LDS
+
+struct RopeArgs {
+  int64_t tokens, src_token, src_head, dst_token, dst_head;  // strides in elements
+  const int64_t *positions;
+  const double *inv_freq;
+  double scale;
+  int heads, dim, half, per_wg, inverse, copy;  // half: pairs; copy: the rest is copied too (dst is not src)
+};
+
+template <typename T, int N> struct Piece {
+  T v[N];
+} __attribute__((aligned(sizeof(T) * N)));
+
+__device__ __forceinline__ float to_f32(unsigned short b) { return __uint_as_float((unsigned)b << 16); }
+__device__ __forceinline__ float to_f32(float f) { return f; }
+__device__ __forceinline__ void from_f32(unsigned short &d, float f) { d = (unsigned short)bf16x2_rne(f, 0.0f); }
+__device__ __forceinline__ void from_f32(float &d, float f) { d = f; }
+
+template <typename T, int VEC, int LAYOUT>
+__global__ __launch_bounds__(ROPE_THREADS) void k_rope(const T *__restrict__ src, T *__restrict__ dst, RopeArgs a) {
+  __shared__ float tc[ROPE_TABLE], ts[ROPE_TABLE];
+  // items of a head: pieces of VEC pairs (HALF and single pairs) or of VEC elements, then the pieces that are copied
+  constexpr bool PAIRS = LAYOUT == ROTARY_HALF || VEC == 1;
+  constexpr int V = VEC;
+  const int turned = PAIRS ? a.half / V : (2 * a.half + V - 1) / V;
+  const int rest0 = PAIRS ? 2 * a.half : turned * V;  // first element that is copied
+  const int items = turned + (a.copy ? (a.dim - rest0) / V : 0);
+  const int64_t t0 = (int64_t)blockIdx.x * a.per_wg;
+  const int nt = (int)(a.tokens - t0 < a.per_wg ? a.tokens - t0 : a.per_wg);
+  for (int i = threadIdx.x; i < nt * a.half; i += ROPE_THREADS) {
+    const int t = i / a.half, p = i - t * a.half;
+    double s, c;
+    sine_cosine((double)a.positions[t0 + t] * a.inv_freq[p], s, c);
+    tc[i] = (float)(c * a.scale);
+    ts[i] = (float)(a.inverse ? -s * a.scale : s * a.scale);
+  }
+  __syncthreads();
+  const int total = nt * a.heads;
+  // a thread keeps its place in the head while the heads fit a pass of the workgroup
+  for (int item = threadIdx.x % (items < ROPE_THREADS ? items : ROPE_THREADS); item < items; item += ROPE_THREADS) {
+    const int step = items < ROPE_THREADS ? ROPE_THREADS / items : 1;
+    const int first = items < ROPE_THREADS ? threadIdx.x / items : 0;
+    if (first >= step) break;  // the threads past the last whole head
+    for (int row = first; row < total; row += step) {
+      const int t = row / a.heads, h = row - t * a.heads;
+      const T *x = src + (t0 + t) * a.src_token + h * a.src_head;
+      T *y = dst + (t0 + t) * a.dst_token + h * a.dst_head;
+      if (item >= turned) {
+        const int d = rest0 + (item - turned) * V;
+        *(Piece<T, V> *)(y + d) = *(const Piece<T, V> *)(x + d);
+        continue;
+      }
+      if (PAIRS) {
+        const int p = item * V;
+        const int da = LAYOUT == ROTARY_HALF ? p : 2 * p, db = LAYOUT == ROTARY_HALF ? p + a.half : 2 * p + 1;
+        Piece<T, V> u = *(const Piece<T, V> *)(x + da), w = *(const Piece<T, V> *)(x + db);
+        const float *c = tc + t * a.half + p, *s = ts + t * a.half + p;
+#pragma unroll
+        for (int e = 0; e < V; ++e) {
+          const float f = to_f32(u.v[e]), g = to_f32(w.v[e]);
+          from_f32(u.v[e], f * c[e] - g * s[e]);
+          from_f32(w.v[e], g * c[e] + f * s[e]);
+        }
+        *(Piece<T, V> *)(y + da) = u;
+        *(Piece<T, V> *)(y + db) = w;
+      } else {
+        const int d = item * V, p = d / 2;
+        Piece<T, V> u = *(const Piece<T, V> *)(x + d);
+        const float *c = tc + t * a.half, *s = ts + t * a.half;
+#pragma unroll
+        for (int e = 0; e < V / 2; ++e) {
+          if (p + e < a.half) {  // the last piece may hold elements that are not rotated
+            const float f = to_f32(u.v[2 * e]), g = to_f32(u.v[2 * e + 1]);
+            from_f32(u.v[2 * e], f * c[p + e] - g * s[p + e]);
+            from_f32(u.v[2 * e + 1], g * c[p + e] + f * s[p + e]);
+          }
+        }
+        *(Piece<T, V> *)(y + d) = u;
+      }
+    }
+  }
+}
+
+template <typename T, int VEC, int LAYOUT>
+static void rope_start(const void *src, void *dst, const RopeArgs &a, hipStream_t stream) {
+  const unsigned grid = (unsigned)((a.tokens + a.per_wg - 1) / a.per_wg);
+  k_rope<T, VEC, LAYOUT><<<grid, ROPE_THREADS, 0, stream>>>((const T *)src, (T *)dst, a);
+}
+
+template <typename T, int LAYOUT>
+static void rope_vec(int vec, const void *src, void *dst, const RopeArgs &a, hipStream_t stream) {
+  switch (vec) {
+    case 8:
+      if constexpr (sizeof(T) == 2) return rope_start<T, 8, LAYOUT>(src, dst, a, stream);
+    case 4: return rope_start<T, 4, LAYOUT>(src, dst, a, stream);
+    case 2: return rope_start<T, 2, LAYOUT>(src, dst, a, stream);
+    default: return rope_start<T, 1, LAYOUT>(src, dst, a, stream);
+  }
+}
+
+hipError_t launch_rope(int dtype, const void *src, void *dst, int64_t tokens, int64_t heads, int64_t dim,
+                       const int64_t strides[4], const int64_t *positions, const double *inv_freq, int64_t rot,
+                       int layout, double scale, int inverse, hipStream_t stream) {
+  const int size = dtype == 1 ? 4 : 2;
+  RopeArgs a{tokens, strides[0], strides[1], strides[2], strides[3], positions, inv_freq, scale,
+             (int)heads, (int)dim, (int)(rot / 2), 1, inverse, src != dst};
+  // the widest piece, up to 16 bytes, at which every access is aligned and no piece is cut
+  int vec = 16 / size;
+  for (; vec > 1; vec /= 2) {
+    bool ok = dim % vec == 0 && (layout == ROTARY_INTERLEAVED || a.half % vec == 0) &&
+              (uintptr_t)src % (vec * size) == 0 && (uintptr_t)dst % (vec * size) == 0;
+    for (int i = 0; i < 4; ++i) ok = ok && strides[i] % vec == 0;
+    if (ok) break;
+  }
+  // tokens of a workgroup: about four 16-byte pieces for each of its threads, as long as the table holds them and
+  // there are four workgroups for every CU
+  const int64_t row = heads * dim * size;
+  int64_t per = 4 * 16 * ROPE_THREADS / row;
+  if (a.half && per > ROPE_TABLE / a.half) per = ROPE_TABLE / a.half;
+  const int64_t spread = tokens / (4 * device_cu_count());
+  if (per > spread) per = spread;
+  a.per_wg = per < 1 ? 1 : (int)per;
+  if (dtype == 1) {
+    if (layout == ROTARY_HALF) rope_vec<float, ROTARY_HALF>(vec, src, dst, a, stream);
+    else rope_vec<float, ROTARY_INTERLEAVED>(vec, src, dst, a, stream);
+  } else {
+    if (layout == ROTARY_HALF) rope_vec<unsigned short, ROTARY_HALF>(vec, src, dst, a, stream);
+    else rope_vec<unsigned short, ROTARY_INTERLEAVED>(vec, src, dst, a, stream);
+  }
+  return hipGetLastError();
+}
+
+}  // namespace mx

@@ -25,16 +25,6 @@ constexpr int64_t MAX_BLOCKS = (int64_t)1 << 22;
 
 __device__ __forceinline__ u32x4 load_piece(const u32x4 *p) { return __builtin_nontemporal_load(p); }
 
-// Sign-cleared u16 maximum of the 8 bf16 values in a piece.
-__device__ __forceinline__ unsigned piece_amax_bf16(u32x4 w) {
-  u16x2 a = __builtin_bit_cast(u16x2, w.x & 0x7FFF7FFFu);
-  u16x2 b = __builtin_bit_cast(u16x2, w.y & 0x7FFF7FFFu);
-  u16x2 c = __builtin_bit_cast(u16x2, w.z & 0x7FFF7FFFu);
-  u16x2 d = __builtin_bit_cast(u16x2, w.w & 0x7FFF7FFFu);
-  u16x2 m = __builtin_elementwise_max(__builtin_elementwise_max(a, b), __builtin_elementwise_max(c, d));
-  return umax(m[0], m[1]);
-}
-
 // OP_QDQ: dst (bf16) = dequantized values.  OP_QUANT: codes + scales.
 // SL (OP_QUANT only): 0 = row-major scales, 1 = the blocked layout `bl`.
 template <int FMT, int OP, int THREADS, int UNROLL, int SL>
