@@ -1,0 +1,306 @@
+// What the attention kernels share: sequences and the division of their work,
+// conversions, row statistics.
+#pragma once
+
+#include "launch.h"
+
+namespace mx {
+
+constexpr int TILE = 64;  // tokens of a tile, the unit of the division
+
+// How the work is divided.  An item is a block of rows of one key/value head of one sequence, its work the tiles of
+// 64 tokens that it reads; items follow one another by sequence, head and block.  `workers` workgroups take equal
+// runs of tiles (not less than min_tiles), so that ragged sequences need no host copy of their lengths to be spread
+// evenly.  A run that covers an item whole writes the result; pieces of an item go to the worker's slots of the
+// workspace (slot 0: a piece that continues its item, which only the run's first can; slot 1: one that begins it, which then is
+// the run's last) and are
+// joined by k_join.  workers == 0: one workgroup for each item, nothing to join.
+struct Division {
+  int workers, min_tiles, rows;  // rows: of a block
+  int blocks, tiles;             // host's bounds on an item's blocks and tiles
+};
+
+struct Sequence {
+  int q0, nq, len;
+};
+
+__device__ __forceinline__ Sequence sequence_of(const AttentionArgs &a, int b) {
+  Sequence s;
+  const int q0 = a.q_starts[b], q1 = a.q_starts[b + 1];
+  s.q0 = q0 < 0 ? 0 : q0;
+  s.nq = (q1 > a.total_q ? a.total_q : q1) - s.q0;
+  s.nq = s.nq < 0 ? 0 : s.nq > a.max_q ? a.max_q : s.nq;
+  const int64_t cap = (int64_t)a.table_pages << a.cache.page_log2;
+  int len = a.kv_lens[b];
+  len = len < 0 ? 0 : len > a.max_kv ? a.max_kv : len;
+  s.len = len > cap ? (int)cap : len;
+  return s;
+}
+
+// Tiles of an item (one at least: rows without tokens get their zeros) and blocks of a head.
+__device__ __forceinline__ int item_tiles(const Sequence &s) { return s.len > 0 ? (s.len + TILE - 1) / TILE : 1; }
+__device__ __forceinline__ int item_blocks(const AttentionArgs &a, const Sequence &s, int rows) {
+  return (s.nq * a.group + rows - 1) / rows;
+}
+__device__ __forceinline__ int64_t sequence_work(const AttentionArgs &a, int b, int rows) {
+  const Sequence s = sequence_of(a, b);
+  return (int64_t)item_blocks(a, s, rows) * a.cache.heads * item_tiles(s);
+}
+
+// All of these are computed by a whole wave, with the same result in every lane.
+__device__ __forceinline__ int64_t wave_sum(int64_t v) {
+#pragma unroll
+  for (int d = 32; d > 0; d /= 2) v += __shfl_xor(v, d);
+  return v;
+}
+__device__ __forceinline__ int64_t wave_prefix(int64_t v, int lane) {  // inclusive
+#pragma unroll
+  for (int d = 1; d < 64; d *= 2) {
+    const int64_t u = __shfl_up(v, d);
+    if (lane >= d) v += u;
+  }
+  return v;
+}
+
+struct Place {
+  int b;          // sequence
+  int64_t first;  // where its work starts
+};
+
+// Total work, and the tiles of a worker's run.
+__device__ __forceinline__ int64_t total_work(const AttentionArgs &a, int rows) {
+  const int lane = threadIdx.x % 64;
+  int64_t t = 0;
+  for (int b = lane; b < a.batch; b += 64) t += sequence_work(a, b, rows);
+  return wave_sum(t);
+}
+__device__ __forceinline__ int64_t run_tiles(const Division &d, int64_t total) {
+  const int64_t per = (total + d.workers - 1) / d.workers;
+  return per < d.min_tiles ? d.min_tiles : per;
+}
+// The sequence in which tile `at` of the work lies (at < total), or (find_b >= 0) where sequence find_b starts.
+__device__ __forceinline__ Place find_place(const AttentionArgs &a, int rows, int64_t at, int find_b) {
+  const int lane = threadIdx.x % 64;
+  int64_t base = 0;
+  for (int b0 = 0; b0 < a.batch; b0 += 64) {
+    const int b = b0 + lane;
+    const int64_t w = b < a.batch ? sequence_work(a, b, rows) : 0;
+    const int64_t end = base + wave_prefix(w, lane);
+    const uint64_t hit = __builtin_amdgcn_ballot_w64(find_b >= 0 ? b == find_b : at < end && at >= end - w);
+    if (hit) {
+      const int l = __builtin_ctzll(hit);
+      return Place{b0 + l, __shfl(end - w, l)};
+    }
+    base = __shfl(end, 63);
+  }
+  return Place{a.batch, base};
+}
+
+__device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
+
+// Pairs of neighbouring dimensions of CNT codes as bf16.  The conversions take the scale from the exponent field of
+// an fp32; 0xFF there makes NaN of every code (checked on gfx950 for all of them).
+template <int FMT, int CNT>
+__device__ __forceinline__ void widen(unsigned *o, const unsigned *c, unsigned scale_byte) {
+  const float sc = scale_operand(scale_byte);
+#pragma unroll
+  for (int p = 0; p < CNT / 2; ++p) {
+    if constexpr (FMT == 0) {
+      const unsigned w = c[p / 4];
+      bf16x2 r;
+      switch (p & 3) {
+        case 0: r = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, sc, 0); break;
+        case 1: r = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, sc, 1); break;
+        case 2: r = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, sc, 2); break;
+        default: r = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, sc, 3); break;
+      }
+      o[p] = __builtin_bit_cast(unsigned, r);
+    } else {
+      const unsigned w = c[p / 2];
+      o[p] = __builtin_bit_cast(unsigned, (p & 1) ? __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, sc, true)
+                                                  : __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, sc, false));
+    }
+  }
+}
+
+// N bytes at p (aligned to the largest power of two up to 16 that divides N) into words
+template <int N>
+__device__ __forceinline__ void load_bytes(unsigned *w, const uint8_t *p) {
+  if constexpr (N % 16 == 0) {
+#pragma unroll
+    for (int i = 0; i < N / 16; ++i) {
+      const u32x4 v = ((const u32x4 *)p)[i];
+      w[4 * i] = v.x, w[4 * i + 1] = v.y, w[4 * i + 2] = v.z, w[4 * i + 3] = v.w;
+    }
+  } else if constexpr (N % 8 == 0) {
+#pragma unroll
+    for (int i = 0; i < N / 8; ++i) {
+      const u32x2 v = ((const u32x2 *)p)[i];
+      w[2 * i] = v.x, w[2 * i + 1] = v.y;
+    }
+  } else if constexpr (N % 4 == 0) {
+#pragma unroll
+    for (int i = 0; i < N / 4; ++i) w[i] = ((const unsigned *)p)[i];
+  } else if constexpr (N == 2) {
+    w[0] = *(const unsigned short *)p;
+  } else if constexpr (N == 1) {
+    w[0] = *p;
+  }
+}
+
+// Sum of a packed bf16 pair onto c.
+__device__ __forceinline__ float add_pair(unsigned pair, float c) {
+  return __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2, pair), __builtin_bit_cast(bf16x2, 0x3F803F80u), c,
+                                         false);
+}
+
+// Maximum and sum with lane ^ 32, and with lane ^ 16.
+__device__ __forceinline__ float max_halves(float v) {
+  auto a = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return fmaxf(__uint_as_float(a[0]), __uint_as_float(a[1]));
+}
+__device__ __forceinline__ float sum_halves(float v) {
+  auto a = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return __uint_as_float(a[0]) + __uint_as_float(a[1]);
+}
+__device__ __forceinline__ float max_rows16(float v) {
+  auto a = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return fmaxf(__uint_as_float(a[0]), __uint_as_float(a[1]));
+}
+__device__ __forceinline__ float sum_rows16(float v) {
+  auto a = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return __uint_as_float(a[0]) + __uint_as_float(a[1]);
+}
+
+// Which of N (up to 32) tokens from j0 (the first one's place among the sequence's new tokens, negative before them)
+// a new token sees: bit i for place j0 + i.
+template <int N>
+__device__ __forceinline__ unsigned seen_bits(const AttentionArgs &a, int query, int node, int j0) {
+  constexpr unsigned ALL = N == 32 ? 0xFFFFFFFFu : (1u << N) - 1u;
+  if (a.tree == nullptr) {
+    const int count = node + 1 - j0;
+    return count >= N ? ALL : count <= 0 ? 0u : (1u << count) - 1u;
+  }
+  if (j0 <= -N) return ALL;
+  const int64_t *words = a.tree + (int64_t)query * a.tree_words;
+  const int at = j0 < 0 ? 0 : j0;
+  const uint64_t w0 = at / 64 < a.tree_words ? (uint64_t)words[at / 64] : 0;
+  const uint64_t w1 = at / 64 + 1 < a.tree_words ? (uint64_t)words[at / 64 + 1] : 0;
+  uint64_t bits = w0 >> (at % 64);
+  if (at % 64) bits |= w1 << (64 - at % 64);
+  return (j0 < 0 ? ((unsigned)(bits << -j0) | ((1u << -j0) - 1u)) : (unsigned)bits) & ALL;
+}
+
+// Bits of the first n of N tokens.
+template <int N>
+__device__ __forceinline__ unsigned first_bits(int n) {
+  constexpr unsigned ALL = N == 32 ? 0xFFFFFFFFu : (1u << N) - 1u;
+  return n >= N ? ALL : n <= 0 ? 0u : (1u << n) - 1u;
+}
+
+// The maximum that weights refer to may lag behind the scores' by this many powers of two before the sums are
+// rescaled: weights stay below 2^8, and most tiles need no rescaling.
+constexpr float LAG = 8.0f;
+
+// Which sums of exponentials give a result (none: the row saw nothing) and its reciprocal; NaN stays NaN.
+__device__ __forceinline__ float reciprocal(float l) { return l == 0.0f ? 0.0f : 1.0f / l; }
+
+// A worker's run, piece by piece.
+struct Pieces {
+  // the piece: tiles t0 .. t1 of the item's `tiles`, and the slot for a part
+  Sequence s;
+  int b, head, block, t0, t1, tiles, slot;
+  // the run
+  int64_t at, end, in;  // of the work; in: of the sequence
+
+  __device__ __forceinline__ Pieces(const AttentionArgs &a, const Division &d) {
+    if (d.workers == 0) {  // one item: the run is found without the others' work
+      const int item = blockIdx.x;
+      const int heads = a.cache.heads;
+      b = item / d.blocks / heads;
+      s = sequence_of(a, b);
+      const int blocks = item_blocks(a, s, d.rows), tiles = item_tiles(s);
+      in = ((int64_t)(item / d.blocks % heads) * blocks + item % d.blocks) * tiles;
+      at = 0;
+      end = item % d.blocks < blocks ? tiles : 0;
+    } else {
+      const int64_t total = total_work(a, d.rows), per = run_tiles(d, total);
+      at = blockIdx.x * per;
+      end = at + per < total ? at + per : total;
+      if (at >= end) return;
+      const Place p = find_place(a, d.rows, at, -1);
+      b = uniform(p.b);
+      in = at - p.first;
+    }
+  }
+  __device__ __forceinline__ bool next(const AttentionArgs &a, const Division &d) {
+    if (at >= end) return false;
+    int item, blocks;
+    for (;; ++b, in = 0) {  // to the next sequence that has rows
+      s = sequence_of(a, b);
+      tiles = item_tiles(s);
+      blocks = item_blocks(a, s, d.rows);
+      item = uniform((int)(in / tiles));
+      if (item < blocks * a.cache.heads) break;
+    }
+    head = item / blocks;
+    block = item % blocks;
+    t0 = uniform((int)(in - (int64_t)item * tiles));
+    t1 = uniform(end - at < tiles - t0 ? t0 + (int)(end - at) : tiles);
+    slot = t0 > 0 ? 0 : 1;
+    at += t1 - t0;
+    in += t1 - t0;
+    return true;
+  }
+};
+
+// Values that are not finite, of tokens that some rows see and others do not, are left out of the products; afterwards
+// their dimensions are made NaN in the rows that see them.  For a row (query `query`, place `node` among the new
+// tokens) and the tokens from .. to of its sequence: not_finite(codes, scales, row of the head's page) is asked for
+// every token that the row sees.
+template <typename Ask>
+__device__ __forceinline__ void seen_tokens(const AttentionArgs &a, const int *table, int head, int query, int node,
+                                            int first_new, int from, int to, Ask ask) {
+  const CacheView &cv = a.cache;
+#pragma unroll 1
+  for (int tok = from; tok < to; ++tok) {
+    const unsigned page = (unsigned)table[tok >> cv.page_log2];
+    if (page >= (uint64_t)cv.pages || !(seen_bits<1>(a, query, node, tok - first_new) & 1u)) continue;
+    ask((int64_t)page * cv.heads + head, tok & ((1 << cv.page_log2) - 1));
+  }
+}
+
+// 1 in bit 0 and bit 16 for the values of a packed pair that are not finite (all ones in the exponent carry into the
+// sign's place).
+__device__ __forceinline__ unsigned not_finite(unsigned pair) {
+  return (((pair & 0x7F807F80u) + 0x00800080u) >> 15) & 0x00010001u;
+}
+
+// Takes values that are not finite out of N packed pairs; non-zero if there were any.
+template <int N>
+__device__ __forceinline__ unsigned clear_not_finite(unsigned *w) {
+  unsigned any = 0u;
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const unsigned bad = not_finite(w[i]);
+    w[i] &= ~((bad << 16) - bad);
+    any |= bad;
+  }
+  return any;
+}
+
+// Parts of the workspace: D sums for each row of a slot, then the slots' maxima and sums.
+__device__ __forceinline__ float *part_sums(const AttentionArgs &a, const Division &d, int64_t slot, int dim) {
+  return a.partial + slot * d.rows * dim;
+}
+__device__ __forceinline__ float *part_stats(const AttentionArgs &a, const Division &d, int64_t slot, int dim) {
+  return a.partial + 2 * (int64_t)d.workers * d.rows * dim + slot * d.rows * 2;
+}
+
+// ---- host ----
+Division attention_division_rows(int dim, int heads, int group, int batch, int64_t max_q, int64_t max_kv);
+Division attention_division_tiles(int dim, int heads, int group, int batch, int64_t max_q, int64_t max_kv);
+hipError_t launch_attention_rows(const AttentionArgs &a, const Division &d, hipStream_t stream);
+hipError_t launch_attention_tiles(const AttentionArgs &a, const Division &d, hipStream_t stream);
+
+}  // namespace mx

@@ -99,6 +99,17 @@ def test_splits(mx, fmt, dim, group):
     c.check(c.run(mx))
 
 
+@pytest.mark.parametrize("group,nq", [(2, 1), (4, 10)])
+def test_many_sequences(mx, group, nq):
+    """More sequences than a wave has lanes, most of them short, some without tokens or queries: the division of the
+    work passes over them."""
+    kv = [(37 * b) % 91 for b in range(150)]
+    kv[3], kv[77], kv[149] = 1500, 900, 700
+    new = [0 if b % 11 == 5 else 1 + b % nq for b in range(150)]
+    c = Case(mx, 1, 1, group, 64, 16, kv, new, seed=150)
+    c.check(c.run(mx))
+
+
 @pytest.mark.parametrize("fmt", [0, 1])
 @pytest.mark.parametrize("nodes,kv", [(2, 2), (13, 400), (16, 16), (64, 300), (65, 65), (100, 731), (130, 700)])
 def test_trees(mx, fmt, nodes, kv):
