@@ -330,7 +330,8 @@ MX_API int mx_cache_read(const mx_cache *cache, const int64_t *slots,
  * A query sees every token before the new ones, and of these
  *   tree == NULL  the ones up to its own;
  *   otherwise     the ones whose bits are set in its row: new token j is bit
- *                 j % 64 of word j / 64 of tree[query * tree_words ..].
+ *                 j % 64 of word j / 64 of tree[query * tree_words ..]
+ *                 (64 * tree_words >= max_q, MX_EARG).
  * A query that sees nothing gives zeros; what it does not see has no part in
  * its result, NaN included.  Tokens of a page that is not in the cache count
  * as not seen.

@@ -328,6 +328,7 @@ MX_API int mx_cache_attention(const mx_cache *cache, const void *q, int64_t q_to
   if (!fits(table_pages, INT32_MAX / cache->page) || table_stride < table_pages || !fits(tree_words, INT32_MAX))
     return MX_ESHAPE;
   if (!(scale > 0.0f && scale <= 3.402823466e38f)) return MX_EARG;
+  if (tree && (max_q < total_q ? max_q : total_q) > 64 * tree_words) return MX_EARG;
   if (batch == 0 || total_q == 0 || max_q == 0) return MX_OK;
   if (!q || !q_starts || !kv_lens || !out) return MX_ENULL;
   if (max_kv > 0 && table_pages > 0 && (!block_table || cache->pages == 0 || empty_cache(cache))) return MX_ENULL;

@@ -24,6 +24,16 @@ struct Sequence {
   int q0, nq, len;
 };
 
+// Values that are the same in every lane of a wave, told to the compiler: they stay in scalar registers, and branches
+// on them cost no exec mask.
+__device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
+__device__ __forceinline__ int64_t uniform(int64_t v) {
+  return (int64_t)(((uint64_t)(unsigned)uniform((int)(v >> 32)) << 32) | (unsigned)uniform((int)v));
+}
+__device__ __forceinline__ Sequence uniform(const Sequence &s) {
+  return Sequence{uniform(s.q0), uniform(s.nq), uniform(s.len)};
+}
+
 __device__ __forceinline__ Sequence sequence_of(const AttentionArgs &a, int b) {
   Sequence s;
   const int q0 = a.q_starts[b], q1 = a.q_starts[b + 1];
@@ -61,42 +71,6 @@ __device__ __forceinline__ int64_t wave_prefix(int64_t v, int lane) {  // inclus
   }
   return v;
 }
-
-struct Place {
-  int b;          // sequence
-  int64_t first;  // where its work starts
-};
-
-// Total work, and the tiles of a worker's run.
-__device__ __forceinline__ int64_t total_work(const AttentionArgs &a, int rows) {
-  const int lane = threadIdx.x % 64;
-  int64_t t = 0;
-  for (int b = lane; b < a.batch; b += 64) t += sequence_work(a, b, rows);
-  return wave_sum(t);
-}
-__device__ __forceinline__ int64_t run_tiles(const Division &d, int64_t total) {
-  const int64_t per = (total + d.workers - 1) / d.workers;
-  return per < d.min_tiles ? d.min_tiles : per;
-}
-// The sequence in which tile `at` of the work lies (at < total), or (find_b >= 0) where sequence find_b starts.
-__device__ __forceinline__ Place find_place(const AttentionArgs &a, int rows, int64_t at, int find_b) {
-  const int lane = threadIdx.x % 64;
-  int64_t base = 0;
-  for (int b0 = 0; b0 < a.batch; b0 += 64) {
-    const int b = b0 + lane;
-    const int64_t w = b < a.batch ? sequence_work(a, b, rows) : 0;
-    const int64_t end = base + wave_prefix(w, lane);
-    const uint64_t hit = __builtin_amdgcn_ballot_w64(find_b >= 0 ? b == find_b : at < end && at >= end - w);
-    if (hit) {
-      const int l = __builtin_ctzll(hit);
-      return Place{b0 + l, __shfl(end - w, l)};
-    }
-    base = __shfl(end, 63);
-  }
-  return Place{a.batch, base};
-}
-
-__device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
 
 // Pairs of neighbouring dimensions of CNT codes as bf16.  The conversions take the scale from the exponent field of
 // an fp32; 0xFF there makes NaN of every code (checked on gfx950 for all of them).
@@ -176,16 +150,17 @@ __device__ __forceinline__ float sum_rows16(float v) {
 // a new token sees: bit i for place j0 + i.
 template <int N>
 __device__ __forceinline__ unsigned seen_bits(const AttentionArgs &a, int query, int node, int j0) {
-  constexpr unsigned ALL = N == 32 ? 0xFFFFFFFFu : (1u << N) - 1u;
+  constexpr unsigned ALL = 0xFFFFFFFFu >> (32 - N);
   if (a.tree == nullptr) {
     const int count = node + 1 - j0;
     return count >= N ? ALL : count <= 0 ? 0u : (1u << count) - 1u;
   }
   if (j0 <= -N) return ALL;
   const int64_t *words = a.tree + (int64_t)query * a.tree_words;
-  const int at = j0 < 0 ? 0 : j0;
-  const uint64_t w0 = at / 64 < a.tree_words ? (uint64_t)words[at / 64] : 0;
-  const uint64_t w1 = at / 64 + 1 < a.tree_words ? (uint64_t)words[at / 64 + 1] : 0;
+  const int at = j0 < 0 ? 0 : j0, i0 = at / 64, last = a.tree_words - 1;
+  uint64_t w0 = words[i0 < last ? i0 : last], w1 = words[i0 < last ? i0 + 1 : last];  // one wait for both
+  if (i0 > last) w0 = 0;
+  if (i0 + 1 > last) w1 = 0;
   uint64_t bits = w0 >> (at % 64);
   if (at % 64) bits |= w1 << (64 - at % 64);
   return (j0 < 0 ? ((unsigned)(bits << -j0) | ((1u << -j0) - 1u)) : (unsigned)bits) & ALL;
@@ -194,7 +169,7 @@ __device__ __forceinline__ unsigned seen_bits(const AttentionArgs &a, int query,
 // Bits of the first n of N tokens.
 template <int N>
 __device__ __forceinline__ unsigned first_bits(int n) {
-  constexpr unsigned ALL = N == 32 ? 0xFFFFFFFFu : (1u << N) - 1u;
+  constexpr unsigned ALL = 0xFFFFFFFFu >> (32 - N);
   return n >= N ? ALL : n <= 0 ? 0u : (1u << n) - 1u;
 }
 
@@ -205,39 +180,69 @@ constexpr float LAG = 8.0f;
 // Which sums of exponentials give a result (none: the row saw nothing) and its reciprocal; NaN stays NaN.
 __device__ __forceinline__ float reciprocal(float l) { return l == 0.0f ? 0.0f : 1.0f / l; }
 
+// The workspace: D sums for each row of a slot, the slots' maxima and sums, and the first and last worker of each item.
+__device__ __forceinline__ float *part_sums(const AttentionArgs &a, const Division &d, int64_t slot, int dim) {
+  return a.partial + slot * d.rows * dim;
+}
+__device__ __forceinline__ float *part_stats(const AttentionArgs &a, const Division &d, int64_t slot, int dim) {
+  return a.partial + 2 * (int64_t)d.workers * d.rows * dim + slot * d.rows * 2;
+}
+
+__device__ __forceinline__ int *item_workers(const AttentionArgs &a, const Division &d) {
+  return (int *)(a.partial + 2 * (int64_t)d.workers * d.rows * (a.cache.dim + 2));
+}
+
 // A worker's run, piece by piece.
 struct Pieces {
   // the piece: tiles t0 .. t1 of the item's `tiles`, and the slot for a part
   Sequence s;
   int b, head, block, t0, t1, tiles, slot;
   // the run
-  int64_t at, end, in;  // of the work; in: of the sequence
+  int64_t at, end, in, per;  // of the work; in: of the sequence
 
   __device__ __forceinline__ Pieces(const AttentionArgs &a, const Division &d) {
     if (d.workers == 0) {  // one item: the run is found without the others' work
       const int item = blockIdx.x;
       const int heads = a.cache.heads;
       b = item / d.blocks / heads;
-      s = sequence_of(a, b);
+      s = uniform(sequence_of(a, b));
       const int blocks = item_blocks(a, s, d.rows), tiles = item_tiles(s);
       in = ((int64_t)(item / d.blocks % heads) * blocks + item % d.blocks) * tiles;
       at = 0;
-      end = item % d.blocks < blocks ? tiles : 0;
+      end = per = item % d.blocks < blocks ? tiles : 0;
     } else {
-      const int64_t total = total_work(a, d.rows), per = run_tiles(d, total);
+      const int lane = threadIdx.x % 64;
+      int64_t work = lane < a.batch ? sequence_work(a, lane, d.rows) : 0;
+      const int64_t upto = wave_prefix(work, lane);
+      int64_t total = __shfl(upto, 63);
+      for (int b0 = 64; b0 < a.batch; b0 += 64) total += wave_sum(b0 + lane < a.batch ? sequence_work(a, b0 + lane, d.rows) : 0);
+      total = uniform(total);
+      per = (total + d.workers - 1) / d.workers;
+      per = per < d.min_tiles ? d.min_tiles : per;
       at = blockIdx.x * per;
       end = at + per < total ? at + per : total;
       if (at >= end) return;
-      const Place p = find_place(a, d.rows, at, -1);
-      b = uniform(p.b);
-      in = at - p.first;
+      // the sequence in which the run starts
+      int64_t base = 0, end_of = upto;
+      for (int b0 = 0;; b0 += 64) {
+        const uint64_t hit = __builtin_amdgcn_ballot_w64(at >= end_of - work && at < end_of);
+        if (hit) {
+          const int l = __builtin_ctzll(hit);
+          b = uniform(b0 + l);
+          in = at - uniform(__shfl(end_of - work, l));
+          break;
+        }
+        base = __shfl(end_of, 63);
+        work = b0 + 64 + lane < a.batch ? sequence_work(a, b0 + 64 + lane, d.rows) : 0;
+        end_of = base + wave_prefix(work, lane);
+      }
     }
   }
   __device__ __forceinline__ bool next(const AttentionArgs &a, const Division &d) {
     if (at >= end) return false;
     int item, blocks;
     for (;; ++b, in = 0) {  // to the next sequence that has rows
-      s = sequence_of(a, b);
+      s = uniform(sequence_of(a, b));
       tiles = item_tiles(s);
       blocks = item_blocks(a, s, d.rows);
       item = uniform((int)(in / tiles));
@@ -248,6 +253,12 @@ struct Pieces {
     t0 = uniform((int)(in - (int64_t)item * tiles));
     t1 = uniform(end - at < tiles - t0 ? t0 + (int)(end - at) : tiles);
     slot = t0 > 0 ? 0 : 1;
+    if (slot && d.workers && threadIdx.x == 0) {
+      // who has the rest: read by k_join
+      int *w = item_workers(a, d) + 2 * (((int64_t)b * a.cache.heads + head) * d.blocks + block);
+      w[0] = blockIdx.x;
+      w[1] = (int)((at + tiles - 1) / per);
+    }
     at += t1 - t0;
     in += t1 - t0;
     return true;
@@ -287,14 +298,6 @@ __device__ __forceinline__ unsigned clear_not_finite(unsigned *w) {
     any |= bad;
   }
   return any;
-}
-
-// Parts of the workspace: D sums for each row of a slot, then the slots' maxima and sums.
-__device__ __forceinline__ float *part_sums(const AttentionArgs &a, const Division &d, int64_t slot, int dim) {
-  return a.partial + slot * d.rows * dim;
-}
-__device__ __forceinline__ float *part_stats(const AttentionArgs &a, const Division &d, int64_t slot, int dim) {
-  return a.partial + 2 * (int64_t)d.workers * d.rows * dim + slot * d.rows * 2;
 }
 
 // ---- host ----

@@ -4,63 +4,70 @@
 
 namespace mx {
 
-// Joins the pieces of a row: out = sum_s 2^(m_s - m) o_s / sum_s 2^(m_s - m) l_s.  A workgroup of WAVES waves takes a
-// row (the waves take pieces in turn) and finds its pieces from the same division as the workers.
-template <int D, int WAVES>
-__global__ __launch_bounds__(64 * WAVES) void k_join(AttentionArgs a, Division dv) {
-  __shared__ float part[WAVES][D + 2];
-  const int wave = uniform(threadIdx.x / 64), lane = threadIdx.x % 64;
-  const int heads = a.cache.heads * a.group;
-  const int64_t at = blockIdx.x;
-  const int token = (int)(at / heads), qh = (int)(at - (int64_t)token * heads);
-  int b = 0, past = a.batch;  // the sequence of the token: the last that starts at or before it
-  while (past - b > 1) {
-    const int mid = (b + past) / 2;
-    if (a.q_starts[mid] <= token) b = mid; else past = mid;
-  }
-  const Sequence s = sequence_of(a, b);
-  const int node = token - s.q0;
-  if (node < 0 || node >= s.nq) return;
-  const int64_t per = run_tiles(dv, total_work(a, dv.rows));
-  const int tiles = item_tiles(s), blocks = item_blocks(a, s, dv.rows);
-  const int head = qh / a.group, row = node * a.group + qh - head * a.group;
-  const int64_t begin = find_place(a, dv.rows, 0, b).first + ((int64_t)head * blocks + row / dv.rows) * tiles;
-  const int w0 = (int)(begin / per), w1 = (int)((begin + tiles - 1) / per);
+// Joins the pieces of items: out = sum_s 2^(m_s - m) o_s / sum_s 2^(m_s - m) l_s.  A workgroup of four waves (sixteen
+// if WIDE) has ROWS rows of an item; WIDE: all waves share one row, as a row of few items has many pieces.
+constexpr int JOIN_ROWS = 4;
+
+template <int D, bool WIDE>
+__global__ __launch_bounds__(WIDE ? 1024 : 256) void k_join(AttentionArgs a, Division dv, int row_groups) {
+  constexpr int WAVES = WIDE ? 16 : 4;
+  __shared__ float part[WIDE ? WAVES : 1][D + 2];
+  const int wave = uniform((int)threadIdx.x / 64), lane = threadIdx.x % 64;
+  const int item = blockIdx.x / row_groups, row0 = (blockIdx.x - item * row_groups) * (WIDE ? 1 : JOIN_ROWS);
+  const int block = item % dv.blocks, head = item / dv.blocks % a.cache.heads, b = item / dv.blocks / a.cache.heads;
+  const int2 ws = *(const int2 *)(item_workers(a, dv) + 2 * (int64_t)item);
+  const Sequence s = uniform(sequence_of(a, b));
+  const int rows = s.nq * a.group - block * dv.rows;  // of this block, if not more than it holds
+  if (row0 >= rows) return;                           // (also for items that are not there, whose workers are not set)
+  const int w0 = uniform(ws.x), w1 = uniform(ws.y);
   if (w0 == w1) return;  // one worker had all of it and has written the result
-  const int r = row % dv.rows;
   constexpr int N = (D + 63) / 64;
-  float m = -__builtin_inff(), l = 0.0f, acc[N];
+  const int last = rows < dv.rows ? rows : dv.rows;
+  for (int r = row0 + (WIDE ? 0 : wave); r < last && r < row0 + (WIDE ? 1 : JOIN_ROWS); r += WIDE ? 1 : WAVES) {
+    float m = -__builtin_inff(), l = 0.0f, acc[N];
 #pragma unroll
-  for (int i = 0; i < N; ++i) acc[i] = 0.0f;
-  auto slot = [&](int w) { return 2 * (int64_t)w + (w == w0); };
-  for (int w = w0 + wave; w <= w1; w += WAVES) m = fmaxf(m, part_stats(a, dv, slot(w), D)[2 * r]);
-  const float base = m == -__builtin_inff() ? 0.0f : m;
+    for (int i = 0; i < N; ++i) acc[i] = 0.0f;
+    auto slot = [&](int w) { return 2 * (int64_t)w + (w == w0); };
+    const int step = WIDE ? WAVES : 1;
+    for (int w = w0 + (WIDE ? wave : 0); w <= w1; w += step) m = fmaxf(m, part_stats(a, dv, slot(w), D)[2 * r]);
+    const float base = m == -__builtin_inff() ? 0.0f : m;
 #pragma unroll 4
-  for (int w = w0 + wave; w <= w1; w += WAVES) {
-    const float *ml = part_stats(a, dv, slot(w), D) + 2 * r, *o = part_sums(a, dv, slot(w), D) + (int64_t)r * D;
-    const float f = __builtin_amdgcn_exp2f(ml[0] - base);
-    l += f * ml[1];
+    for (int w = w0 + (WIDE ? wave : 0); w <= w1; w += step) {
+      const float *ml = part_stats(a, dv, slot(w), D) + 2 * r, *o = part_sums(a, dv, slot(w), D) + (int64_t)r * D;
+      const float f = __builtin_amdgcn_exp2f(ml[0] - base);
+      l += f * ml[1];
+#pragma unroll
+      for (int i = 0; i < N; ++i)
+        if (D % 64 == 0 || 64 * i + lane < D) acc[i] += f * o[64 * i + lane];
+    }
+    const int row = block * dv.rows + r, node = row / a.group;
+    unsigned short *out = a.out + ((int64_t)(s.q0 + node) * a.cache.heads * a.group + head * a.group + row -
+                                   node * a.group) * D;
+    if (!WIDE) {
+      const float inv = reciprocal(l);
+#pragma unroll
+      for (int i = 0; i < N; ++i)
+        if (D % 64 == 0 || 64 * i + lane < D) out[64 * i + lane] = (unsigned short)bf16x2_rne(acc[i] * inv, 0.0f);
+      continue;
+    }
 #pragma unroll
     for (int i = 0; i < N; ++i)
-      if (D % 64 == 0 || 64 * i + lane < D) acc[i] += f * o[64 * i + lane];
-  }
+      if (D % 64 == 0 || 64 * i + lane < D) part[wave][64 * i + lane] = acc[i];
+    if (lane == 0) part[wave][D] = m, part[wave][D + 1] = l;
+    __syncthreads();
+    if (threadIdx.x < D) {
+      float top = -__builtin_inff(), sum = 0.0f, v = 0.0f;
 #pragma unroll
-  for (int i = 0; i < N; ++i)
-    if (D % 64 == 0 || 64 * i + lane < D) part[wave][64 * i + lane] = acc[i];
-  if (lane == 0) part[wave][D] = m, part[wave][D + 1] = l;
-  __syncthreads();
-  for (int d = threadIdx.x; d < D; d += 64 * WAVES) {
-    float top = -__builtin_inff(), sum = 0.0f, v = 0.0f;
+      for (int w = 0; w < WAVES; ++w) top = fmaxf(top, part[w][D]);
 #pragma unroll
-    for (int w = 0; w < WAVES; ++w) top = fmaxf(top, part[w][D]);
-#pragma unroll
-    for (int w = 0; w < WAVES; ++w) {
-      // a wave without a maximum has sums of zero, or NaN, which has to stay
-      const float f = part[w][D] == -__builtin_inff() ? 1.0f : __builtin_amdgcn_exp2f(part[w][D] - top);
-      sum += f * part[w][D + 1];
-      v += f * part[w][d];
+      for (int w = 0; w < WAVES; ++w) {
+        // a wave without a maximum has sums of zero, or NaN, which has to stay
+        const float f = part[w][D] == -__builtin_inff() ? 1.0f : __builtin_amdgcn_exp2f(part[w][D] - top);
+        sum += f * part[w][D + 1];
+        v += f * part[w][threadIdx.x];
+      }
+      out[threadIdx.x] = (unsigned short)bf16x2_rne(v * reciprocal(sum), 0.0f);
     }
-    a.out[at * D + d] = (unsigned short)bf16x2_rne(v * reciprocal(sum), 0.0f);
   }
 }
 
@@ -75,17 +82,21 @@ int64_t attention_workspace(int fmt, int dim, int heads, int group, int batch, i
   if (batch == 0 || total_q == 0 || max_q == 0) return 0;
   bool tiled;
   const Division d = division_of(dim, heads, group, batch, max_q, max_kv, &tiled);
-  return 2 * (int64_t)d.workers * d.rows * (dim + 2) * 4;
+  if (d.workers == 0) return 0;
+  return 2 * (int64_t)d.workers * d.rows * (dim + 2) * 4 + (int64_t)batch * heads * d.blocks * 8;
 }
 
 template <int D>
 static hipError_t join(const AttentionArgs &a, const Division &d, hipStream_t stream) {
-  const unsigned rows = (unsigned)((int64_t)a.total_q * a.cache.heads * a.group);
-  // the more pieces a row can have, the more waves share them
   const int64_t items = (int64_t)a.batch * a.cache.heads * d.blocks;
-  if (d.workers / items > 16) k_join<D, 16><<<rows, 1024, 0, stream>>>(a, d);
-  else if (d.workers / items > 4) k_join<D, 4><<<rows, 256, 0, stream>>>(a, d);
-  else k_join<D, 1><<<rows, 64, 0, stream>>>(a, d);
+  const int most = a.max_q * a.group < d.rows ? a.max_q * a.group : d.rows;  // rows of a block
+  // eight pieces or more of every item on the average and few rows: one row for sixteen waves
+  if (d.workers / items >= 8 && items * most <= 2 * device_cu_count()) {
+    k_join<D, true><<<(unsigned)(items * most), 1024, 0, stream>>>(a, d, most);
+  } else {
+    const int groups = (most + JOIN_ROWS - 1) / JOIN_ROWS;
+    k_join<D, false><<<(unsigned)(items * groups), 256, 0, stream>>>(a, d, groups);
+  }
   return hipGetLastError();
 }
 
@@ -124,8 +135,8 @@ Division attention_division_rows(int dim, int heads, int group, int batch, int64
 }
 
 Division attention_division_tiles(int dim, int heads, int group, int batch, int64_t max_q, int64_t max_kv) {
-  const int rows = max_q * group <= 128 ? 128 : 256;
-  return divide(rows, (int64_t)device_cu_count(), 2, heads, group, batch, max_q, max_kv);
+  const int rows = max_q * group <= 128 || dim > 128 ? 128 : 256;
+  return divide(rows, (rows == 128 && dim <= 128 ? 2 : 1) * (int64_t)device_cu_count(), 2, heads, group, batch, max_q, max_kv);
 }
 
 }  // namespace mx

@@ -137,14 +137,15 @@ __global__ __launch_bounds__(64 * ATT_WAVES, NT == 1 && D <= 128 ? 2 : 1) void k
   using A = Att<FMT, D>;
   extern __shared__ float lds[];
   const CacheView &cv = a.cache;
-  const int wave = uniform(threadIdx.x / 64), lane = threadIdx.x % 64, n16 = lane % 16, g = lane / 16;
+  const int wave = uniform((int)threadIdx.x / 64), lane = threadIdx.x % 64, n16 = lane % 16, g = lane / 16;
   const int page_mask = (1 << cv.page_log2) - 1;
   for (Pieces pc(a, dv); pc.next(a, dv);) {
-    const Sequence sq = pc.s;
-    const int b = pc.b, head = pc.head, rb = pc.block, t0 = pc.t0, t1 = pc.t1, tiles = pc.tiles, slot = pc.slot;
-  const int q0 = sq.q0, len = sq.len, rows = sq.nq * a.group;
+    const int nq = uniform(pc.s.nq), len = uniform(pc.s.len), q0 = uniform(pc.s.q0), b = uniform(pc.b);
+    const int head = uniform(pc.head), rb = uniform(pc.block);
+    const int t0 = uniform(pc.t0), t1 = uniform(pc.t1), tiles = uniform(pc.tiles), slot = uniform(pc.slot);
+  const int rows = nq * a.group;
   const int lo = t0 * TILE, hi = t1 * TILE < len ? t1 * TILE : len;
-  const int first_new = len - sq.nq;                                // may be negative
+  const int first_new = len - nq;                                // may be negative
   const int seen_by_all = a.tree ? first_new : first_new + 1;       // tokens before this need no mask
   const int *table = a.table + (int64_t)b * a.table_stride;
 

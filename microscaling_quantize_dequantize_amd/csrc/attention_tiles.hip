@@ -31,14 +31,15 @@ namespace mx {
 typedef short i16x4 __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) i16x4 lds_i16x4;
 typedef __attribute__((address_space(3))) uint8_t lds_u8;
+typedef __attribute__((address_space(3))) int lds_int;
 
 template <int FMT, int D, int RB, int WAVES> struct Tiled {
   static constexpr int THREADS = 64 * WAVES;
   static constexpr int ROWS = 32 * RB * WAVES;
   static constexpr int CODE = FMT == 0 ? 8 : 16;                       // bytes of 16 dimensions
   static constexpr int ROW = D / 16;                                   // such units of a row
-  static constexpr int ALL = 2 * TILE * ROW;                           // of a tile: keys, then values
-  static constexpr int UNITS = (ALL + THREADS - 1) / THREADS;          // of a thread
+  static constexpr int SHARE = THREADS / TILE;                         // threads of a token
+  static constexpr int UNITS = (ROW + SHARE - 1) / SHARE;              // units of a thread, of the key and of the value
   static constexpr int KS = 2 * D + 16;                                // bytes of an LDS row
   static constexpr int VS = 2 * D + (D == 96 ? 0 : 64);
   static constexpr int BUFFER = TILE * (KS + VS);
@@ -50,6 +51,14 @@ __device__ __forceinline__ f32x16 mma32(u32x4 a, u32x4 b, f32x16 c) {
                                                  0);
 }
 
+// Kinds of instructions for the order that the compiler is asked for.
+constexpr int SCHED_VALU = 0x2, SCHED_MFMA = 0x8, SCHED_LDS_READ = 0x100;
+template <int KIND, int N> __device__ __forceinline__ void order() { __builtin_amdgcn_sched_group_barrier(KIND, N, 0); }
+
+// Keeps what is computed of a loaded value behind this point: where a loop loads it for its next turn, the compiler
+// would compute it, and wait for it, at once.
+template <typename T> __device__ __forceinline__ void held(T &v) { asm volatile("" : "+v"(v)); }
+
 // Eight tokens of a dimension: two transposing reads, `far` bytes apart.
 __device__ __forceinline__ u32x4 read_v(const lds_u8 *p, int far) {
   const u32x2 a = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4 *)p));
@@ -58,20 +67,23 @@ __device__ __forceinline__ u32x4 read_v(const lds_u8 *p, int far) {
 }
 
 template <int FMT, int D, int RB, int WAVES>
-__global__ __launch_bounds__(64 * WAVES) void k_attention_tiles(AttentionArgs a, Division dv) {
+__global__ __launch_bounds__(64 * WAVES, D <= 128 ? 2 : 1) void k_attention_tiles(AttentionArgs a, Division dv) {
   using T = Tiled<FMT, D, RB, WAVES>;
   extern __shared__ __align__(16) uint8_t lds[];
   const CacheView &cv = a.cache;
-  const int wave = uniform(threadIdx.x / 64), lane = threadIdx.x % 64, n32 = lane % 32, h = lane / 32;
+  const int wave = uniform((int)threadIdx.x / 64), lane = threadIdx.x % 64, n32 = lane % 32, h = lane / 32;
   const int page_mask = (1 << cv.page_log2) - 1;
-  volatile int *flags = (volatile int *)(lds + 2 * T::BUFFER);  // [0]: a page outside the cache, [1]: values that are not finite in a masked tile
+  lds_int *flags = (lds_int *)(lds + 2 * T::BUFFER);  // [0]: a page outside the cache, [1]: values that are not finite in a masked tile
+  constexpr int VG = D % 128 == 0 ? 4 : D % 96 == 0 ? 3 : 2;  // V operands of a group
+  constexpr int PARTS = D / 32 / VG;                           // groups for 16 tokens
   const float to_log2 = a.scale * 1.4426950408889634f;
 
   for (Pieces pc(a, dv); pc.next(a, dv);) {
-    const Sequence sq = pc.s;
-    const int b = pc.b, head = pc.head, rb = pc.block, t0 = pc.t0, t1 = pc.t1, tiles = pc.tiles, slot = pc.slot;
-    const int q0 = sq.q0, len = sq.len, rows = sq.nq * a.group;
-    const int first_new = len - sq.nq;                           // may be negative
+    const int nq = uniform(pc.s.nq), len = uniform(pc.s.len), q0 = uniform(pc.s.q0), b = uniform(pc.b);
+    const int head = uniform(pc.head), rb = uniform(pc.block);
+    const int t0 = uniform(pc.t0), t1 = uniform(pc.t1), tiles = uniform(pc.tiles), slot = uniform(pc.slot);
+    const int rows = nq * a.group;
+    const int first_new = len - nq;                           // may be negative
     const int seen_by_all = a.tree ? first_new : first_new + 1;  // tokens before this need no mask
     const int tail0 = (seen_by_all < 0 ? 0 : seen_by_all) / TILE;  // the first tile that needs a mask
     const int *table = a.table + (int64_t)b * a.table_stride;
@@ -102,71 +114,70 @@ __global__ __launch_bounds__(64 * WAVES) void k_attention_tiles(AttentionArgs a,
         for (int r = 0; r < 16; ++r) o[n][i][r] = 0.0f;
     }
 
-    // codes on their way: the thread's units of a tile
-    unsigned code[T::UNITS][T::CODE / 4], scale[T::UNITS];
-    int page[T::UNITS];
-    auto unit_row = [&](int u, int &row, int &col) {  // which of keys (rows 0 ..) and values (TILE ..), 16 dimensions
-      const int i = threadIdx.x + u * T::THREADS;
-      row = i / T::ROW;
-      col = i - row * T::ROW;
-      return T::ALL % T::THREADS == 0 || i < T::ALL;
-    };
-    auto token_of = [&](int t, int row) {  // past the end: the last one again
-      const int tok = t * TILE + row % TILE;
+    // codes on their way: a thread has one token of a tile, and of its key and its value (index 0 and 1 below) every
+    // SHARE-th unit of 16 dimensions
+    const int my_row = threadIdx.x / T::SHARE, my_col = threadIdx.x % T::SHARE;
+    unsigned code[2][T::UNITS][T::CODE / 4], scale[2][T::UNITS];
+    int page = 0;
+    bool outside = false;  // the page is not in the cache
+    auto has = [&](int u) { return T::ROW % T::SHARE == 0 || my_col + u * T::SHARE < T::ROW; };
+    auto token_of = [&](int t) {  // past the end: the last one again
+      const int tok = t * TILE + my_row;
       return tok < len ? tok : len - 1;
     };
-    auto look_up = [&](int t) {
-#pragma unroll
-      for (int u = 0; u < T::UNITS; ++u) {
-        int row, col;
-        if (!unit_row(u, row, col)) break;
-        page[u] = table[token_of(t, row) >> cv.page_log2];
-      }
-    };
+    auto look_up = [&](int t) { page = table[token_of(t) >> cv.page_log2]; };
     auto fetch = [&](int t) {
+      held(page);
+      outside = (unsigned)page >= (uint64_t)cv.pages;
+      const int r = token_of(t) & page_mask;
+      const int64_t ph = (int64_t)(outside ? 0 : page) * cv.heads + head;
+      const int64_t c0 = ((ph << cv.page_log2) + r) * (T::ROW * T::CODE) + my_col * T::CODE;
+      const int64_t s0 = ((ph * (D / 32)) << cv.page_log2) + (r & ~3);
 #pragma unroll
-      for (int u = 0; u < T::UNITS; ++u) {
-        int row, col;
-        if (!unit_row(u, row, col)) break;
-        const int r = token_of(t, row) & page_mask;
-        const bool ok = (unsigned)page[u] < (uint64_t)cv.pages;
-        const int64_t ph = (int64_t)(ok ? page[u] : 0) * cv.heads + head;
-        const bool value = row >= TILE;
-        const uint8_t *c = value ? cv.codes[1] : cv.codes[0], *s = value ? cv.scales[1] : cv.scales[0];
-        load_bytes<T::CODE>(code[u], c + (((ph << cv.page_log2) + r) * T::ROW + col) * T::CODE);
-        scale[u] = s[((ph * (D / 32) + col / 2) << cv.page_log2) + r];
-        if (!ok) scale[u] |= 0x100u;
-      }
-    };
-    auto store = [&](int t) {
-      uint8_t *buf = lds + (t & 1) * T::BUFFER;
-      const bool tail = t >= tail0;
-      bool outside_any = false;
-      unsigned odd_any = 0u;
+      for (int v = 0; v < 2; ++v)
 #pragma unroll
-      for (int u = 0; u < T::UNITS; ++u) {
-        int row, col;
-        if (!unit_row(u, row, col)) break;
-        const bool value = row >= TILE, outside = scale[u] > 0xFFu;
-        unsigned w[8];
-        widen<FMT, 16>(w, code[u], scale[u] & 0xFFu);
-        outside_any |= outside;
-        if (tail) {
-          const unsigned keep = value && (outside || t * TILE + row - TILE >= len) ? 0u : 0xFFFFFFFFu;
-#pragma unroll
-          for (int i = 0; i < 8; ++i) w[i] &= keep;
-          if (value) odd_any |= clear_not_finite<8>(w);
-        } else if (outside) {
-#pragma unroll
-          for (int i = 0; i < 8; ++i) w[i] = 0u;
+        for (int u = 0; u < T::UNITS; ++u) {
+          if (!has(u)) break;
+          load_bytes<T::CODE>(code[v][u], cv.codes[v] + c0 + u * (T::SHARE * T::CODE));
+          // four tokens' bytes: a byte would be masked, and so waited for, where it is loaded
+          scale[v][u] = *(const unsigned *)(cv.scales[v] + s0 + ((my_col + u * T::SHARE) / 2 << cv.page_log2));
         }
-        u32x4 *d = (u32x4 *)(buf + (value ? TILE * T::KS + (row - TILE) * T::VS : row * T::KS) + 32 * col);
+    };
+    auto place = [&](int t, int v, int u) {
+      return (u32x4 *)(lds + (t & 1) * T::BUFFER + (v ? TILE * T::KS + my_row * T::VS : my_row * T::KS) + 32 * my_col +
+                       32 * T::SHARE * u);
+    };
+    auto scale_of = [&](int t, int v, int u) { return scale[v][u] >> (8 * (token_of(t) & 3)) & 0xFFu; };
+    auto store = [&](int t, int v, int u) {
+      if (!has(u)) return;
+      held(scale[v][u]);
+      unsigned w[8];
+      widen<FMT, 16>(w, code[v][u], scale_of(t, v, u));
+      u32x4 *d = place(t, v, u);
+      d[0] = u32x4{w[0], w[1], w[2], w[3]};
+      d[1] = u32x4{w[4], w[5], w[6], w[7]};
+    };
+    // The values of a tile that needs a mask, or has pages outside the cache, once more: tokens that are not there
+    // become zero, and so does what is not finite.
+    auto clean = [&](int t) {
+      unsigned odd = 0u;
+#pragma unroll
+      for (int u = 0; u < T::UNITS; ++u) {
+        if (!has(u)) break;
+        unsigned w[8];
+        widen<FMT, 16>(w, code[1][u], scale_of(t, 1, u));
+        const unsigned keep = outside || t * TILE + my_row >= len ? 0u : 0xFFFFFFFFu;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) w[i] &= keep;
+        if (t >= tail0) odd |= clear_not_finite<8>(w);
+        u32x4 *d = place(t, 1, u);
         d[0] = u32x4{w[0], w[1], w[2], w[3]};
         d[1] = u32x4{w[4], w[5], w[6], w[7]};
       }
-      if (outside_any) flags[0] = 1;
-      if (odd_any) flags[1] = 1;
+      if (outside) flags[0] = 1;
+      if (odd) flags[1] = 1;
     };
+    auto needs_clean = [&](int t) { return t >= tail0 || __builtin_amdgcn_ballot_w64(outside) != 0; };
 
     if (threadIdx.x < 2) flags[threadIdx.x] = 0;
     __syncthreads();
@@ -174,34 +185,70 @@ __global__ __launch_bounds__(64 * WAVES) void k_attention_tiles(AttentionArgs a,
       look_up(t0);
       fetch(t0);
       look_up(t0 + 1);
-      store(t0);
+#pragma unroll
+      for (int u = 0; u < T::UNITS; ++u) store(t0, 0, u), store(t0, 1, u);
+      if (needs_clean(t0)) clean(t0);
       fetch(t0 + 1);
       look_up(t0 + 2);
     }
+    __builtin_amdgcn_s_waitcnt(0);  // the queries' loads too: none is left for the loop to wait for
     __syncthreads();
     for (int t = t0; t < t1 && len > 0; ++t) {
       const lds_u8 *kb = (const lds_u8 *)(lds + (t & 1) * T::BUFFER + n32 * T::KS + 16 * h);
       const lds_u8 *vb = (const lds_u8 *)(lds + (t & 1) * T::BUFFER + TILE * T::KS + (4 * h + lane % 16 / 4) * T::VS +
                                           32 * (lane / 16 % 2) + 8 * (lane % 4));
-      f32x16 s[RB][2];
+      const int outside_seen = flags[0];
+      // operands are read one group ahead of the products that take them
+      u32x4 kf[2][4], vf[2][VG];
+      auto read_k = [&](int g) {
 #pragma unroll
-      for (int i = 0; i < D / 16; ++i)
+        for (int i = 0; i < 4; ++i)
+          kf[g & 1][i] = *(const __attribute__((address_space(3))) u32x4 *)(kb + (i & 1) * 32 * T::KS + 64 * g + 32 * (i / 2));
+      };
+      auto read_values = [&](int g) {
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          const u32x4 k = *(const __attribute__((address_space(3))) u32x4 *)(kb + u * 32 * T::KS + 32 * i);
-#pragma unroll
-          for (int n = 0; n < RB; ++n) s[n][u] = mma32(k, q[n][i], i == 0 ? f32x16{} : s[n][u]);
-          if (u == 1 && i % 2 == 1) __builtin_amdgcn_sched_barrier(0);
+        for (int i = 0; i < VG; ++i) {
+          const int k = (g * VG + i) / (D / 32), d = (g * VG + i) % (D / 32);
+          vf[g & 1][i] = read_v(vb + 16 * k * T::VS + 64 * d, 8 * T::VS);
         }
+      };
+      f32x16 s[RB][2];
+      read_k(0);
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int g = 0; g < D / 32; ++g) {
+        if (g + 1 < D / 32) read_k(g + 1);
+        else read_values(0);
+        // the next tile's conversion under the products
+        if (g < 2 * T::UNITS) store(t + 1, g % 2, g / 2);
+        if (g == D / 32 - 1)
+#pragma unroll
+          for (int k = D / 32; k < 2 * T::UNITS; ++k) store(t + 1, k % 2, k / 2);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int n = 0; n < RB; ++n)
+            s[n][i & 1] = mma32(kf[g & 1][i], q[n][2 * g + i / 2], g == 0 && i < 2 ? f32x16{} : s[n][i & 1]);
+        order<SCHED_LDS_READ, 4>();
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          order<SCHED_MFMA, RB>();
+          order<SCHED_VALU, 5>();
+        }
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      if (needs_clean(t + 1) && t + 1 < t1) clean(t + 1);
+      fetch(t + 2);  // not under a condition: its registers would be copied, which waits for the loads
+      look_up(t + 3);
 
-      const bool masked = t >= tail0 || flags[0];
+      const bool masked = t >= tail0 || uniform(outside_seen);
       unsigned vis[RB][2];
       if (masked) {
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
           const int tok = t * TILE + 32 * u;
           unsigned in = first_bits<32>(len - tok);
-          if (flags[0]) {
+          if (outside_seen) {
             // pages hold 16 tokens at least
             if (tok < len && (unsigned)table[tok >> cv.page_log2] >= (uint64_t)cv.pages) in &= 0xFFFF0000u;
             if (tok + 16 < len && (unsigned)table[(tok + 16) >> cv.page_log2] >= (uint64_t)cv.pages) in &= 0xFFFFu;
@@ -216,8 +263,7 @@ __global__ __launch_bounds__(64 * WAVES) void k_attention_tiles(AttentionArgs a,
         }
       }
 
-      // weights: registers 8 s .. of a half are the operand for its tokens 16 s ..
-      u32x4 p[RB][4];
+      float base[RB];
 #pragma unroll
       for (int n = 0; n < RB; ++n) {
         float top = s[n][0][0];
@@ -232,30 +278,42 @@ __global__ __launch_bounds__(64 * WAVES) void k_attention_tiles(AttentionArgs a,
 #pragma unroll
           for (int i = 0; i < D / 32; ++i) o[n][i] *= f;
         }
-        const float base = m[n] == -__builtin_inff() ? 0.0f : m[n];
-#pragma unroll
-        for (int k = 0; k < 16; ++k) {
-          const float w0 = __builtin_amdgcn_exp2f(__builtin_fmaf(s[n][k / 8][2 * k % 16], to_log2, -base));
-          const float w1 = __builtin_amdgcn_exp2f(__builtin_fmaf(s[n][k / 8][2 * k % 16 + 1], to_log2, -base));
-          p[n][k / 4][k % 4] = bf16x2_rne(w0, w1);
-          l[n] = add_pair(p[n][k / 4][k % 4], l[n]);
-        }
+        base[n] = m[n] == -__builtin_inff() ? 0.0f : m[n];
       }
 
+      // weights: registers 8 k .. of the scores are the operand for the tokens 16 k ..; those of the next 16 tokens
+      // are computed under the products of these
+      u32x4 p[RB][4];
+      auto weigh = [&](int k, int from, int to) {
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
+        for (int n = 0; n < RB; ++n)
 #pragma unroll
-          for (int i = 0; i < D / 32; ++i) {
-            const u32x4 v = read_v(vb + 16 * k * T::VS + 64 * i, 8 * T::VS);
-#pragma unroll
-            for (int n = 0; n < RB; ++n) o[n][i] = mma32(v, p[n][k], o[n][i]);
-            if (i % 2 == 1) __builtin_amdgcn_sched_barrier(0);
+          for (int i = from; i < to; ++i) {
+            const int r = 8 * (k & 1) + 2 * i;
+            const float w0 = __builtin_amdgcn_exp2f(__builtin_fmaf(s[n][k / 2][r], to_log2, -base[n]));
+            const float w1 = __builtin_amdgcn_exp2f(__builtin_fmaf(s[n][k / 2][r + 1], to_log2, -base[n]));
+            p[n][k][i] = bf16x2_rne(w0, w1);
+            l[n] = add_pair(p[n][k][i], l[n]);
           }
-
-      if (t + 1 < t1) {
-        store(t + 1);
-        fetch(t + 2);
-        look_up(t + 3);
+      };
+      weigh(0, 0, 4);
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int g = 0; g < D / 8 / VG; ++g) {
+        const int k = g / PARTS, part = g % PARTS;
+        if (g + 1 < D / 8 / VG) read_values(g + 1);
+        if (k < 3) weigh(k + 1, 4 * part / PARTS, 4 * (part + 1) / PARTS);
+#pragma unroll
+        for (int i = 0; i < VG; ++i)
+#pragma unroll
+          for (int n = 0; n < RB; ++n) o[n][part * VG + i] = mma32(vf[g & 1][i], p[n][k], o[n][part * VG + i]);
+#pragma unroll
+        for (int i = 0; i < VG; ++i) {
+          order<SCHED_LDS_READ, 2>();
+          order<SCHED_MFMA, RB>();
+          order<SCHED_VALU, (24 * RB / PARTS + VG - 1) / VG>();
+        }
+        __builtin_amdgcn_sched_barrier(0);
       }
       __syncthreads();
     }

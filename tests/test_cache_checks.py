@@ -127,6 +127,8 @@ def test_attention_refusals(b):
     for name, off in (("q", 8), ("out", 8), ("starts", 2), ("lens", 2), ("table", 2)):
         assert attend(**{name: A + off}) == EALIGN
     assert attend(tree=A + 4, words=1) == EALIGN
+    assert attend(tree=A, words=0) == EARG
+    assert attend(tree=A, words=1, total=100, max_q=65) == EARG
     assert attend(qt=252) == EALIGN
     assert attend(qh=68) == EALIGN
     need = lib.mx_cache_attention_workspace(c, 4, 2, 2, 1, 100000)
