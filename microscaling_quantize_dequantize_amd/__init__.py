@@ -17,5 +17,6 @@ __all__ = ["mx_qdq", "mx_quantize", "mx_dequantize", "mx_rotate", "mx_matmul",
 def __getattr__(name):
     if name in __all__:
         from . import binding
-        return getattr(binding, name)
+        value = globals()[name] = getattr(binding, name)  # found without this function from now on
+        return value
     raise AttributeError(name)

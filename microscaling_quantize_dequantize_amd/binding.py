@@ -57,6 +57,7 @@ _lib.mx_cache_attention_workspace.restype = _i64
 _lib.mx_cache_attention.argtypes = [_vp, _vp, _i64, _i64, _i64, _vp, _vp, _i64, _vp, _i64, _i64, _i64, _i64, _i64, _vp,
                                     _i64, ctypes.c_float, _vp, _vp, _i64]
 _lib.mx_set_stream.argtypes = [_vp]
+_lib.mx_set_stream.restype = None
 _lib.mx_get_stream.restype = _vp
 _lib.mx_status_string.argtypes = [_int]
 _lib.mx_status_string.restype = ctypes.c_char_p
@@ -142,7 +143,8 @@ def _call(status: int) -> None:
 
 
 def _stream() -> None:
-    _lib.mx_set_stream(ctypes.c_void_p(torch.cuda.current_stream().cuda_stream))
+    # the handle alone: torch.cuda.current_stream() builds a Stream object around it, 3 us of a call's 10
+    _lib.mx_set_stream(torch._C._cuda_getCurrentRawStream(torch.cuda.current_device()))
 
 
 def mx_qdq(fmt: int, src: torch.Tensor, rot: torch.Tensor | None = None,
@@ -359,39 +361,53 @@ def mx_nvfp4_dequantize(codes: torch.Tensor, scales: torch.Tensor, K: int, globa
 # ---- rotary positions, the paged MX cache and attention over it ---------------
 
 
+def _place(t: torch.Tensor, name: str) -> None:
+    if not t.is_cuda:
+        raise TypeError(f"{name} must be a GPU tensor")
+    if t.get_device() != torch.cuda.current_device():
+        raise ValueError(f"{name} is on {t.device}, the current device is cuda:{torch.cuda.current_device()}")
+
+
 def _heads(t, name: str, dtypes, shape=None):
     """t must be [tokens, heads, dim] with contiguous dimensions (any token and head strides) on the current
-    device."""
+    device.  Its pointer and the two strides."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch tensor")
     if t.dtype not in dtypes:
         raise ValueError(f"{name} must be {' or '.join(str(d) for d in dtypes)}, got {t.dtype}")
-    if t.dim() != 3 or (shape is not None and tuple(t.shape) != tuple(shape)):
+    if t.dim() != 3 or (shape is not None and t.shape != shape):
         raise ValueError(f"{name} must have shape {'[tokens, heads, dim]' if shape is None else tuple(shape)}, "
                          f"got {tuple(t.shape)}")
-    if t.shape[2] > 1 and t.stride(2) != 1:
+    token, head, one = t.stride()
+    if one != 1 and t.shape[2] > 1:
         raise ValueError(f"the dimensions of {name} must be contiguous")
     _place(t, name)
-    return t.data_ptr(), t.stride(0), t.stride(1)
-
-
-def _place(t: torch.Tensor, name: str) -> None:
-    if not t.is_cuda:
-        raise TypeError(f"{name} must be a GPU tensor")
-    if t.device.index != torch.cuda.current_device():
-        raise ValueError(f"{name} is on {t.device}, the current device is cuda:{torch.cuda.current_device()}")
+    return t.data_ptr(), token, head
 
 
 def _vector(t, name: str, dtype: torch.dtype, n: int) -> int:
-    _want(t, name, dtype, (n,))
-    return _dev(t, name)
+    """Pointer of a contiguous [n] tensor of this type on the current device."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch tensor")
+    if t.dtype != dtype or t.shape != (n,):
+        raise ValueError(f"{name} must be {dtype} [{n}], got {t.dtype} {tuple(t.shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    _place(t, name)
+    return t.data_ptr()
 
 
 def _rotary(positions, inv_freq, tokens: int):
     """Pointers of the positions and frequencies, and the number of rotated dimensions."""
     if not isinstance(inv_freq, torch.Tensor) or inv_freq.dtype != torch.float64 or inv_freq.dim() != 1:
         raise ValueError("inv_freq must be a one-dimensional float64 tensor (angle per position of each pair)")
-    return _vector(positions, "positions", torch.int64, tokens), _dev(inv_freq, "inv_freq"), 2 * inv_freq.numel()
+    pairs = inv_freq.shape[0]
+    return (_vector(positions, "positions", torch.int64, tokens), _vector(inv_freq, "inv_freq", torch.float64, pairs),
+            2 * pairs)
+
+
+def _like(t: torch.Tensor) -> torch.Tensor:
+    return torch.empty_like(t, memory_format=torch.contiguous_format)
 
 
 def mx_rope(x: torch.Tensor, positions: torch.Tensor, inv_freq: torch.Tensor, layout: int = HALF, scale: float = 1.0,
@@ -404,7 +420,7 @@ def mx_rope(x: torch.Tensor, positions: torch.Tensor, inv_freq: torch.Tensor, la
     gradient of the output to that of x.  dst may be x itself."""
     ps, st, sh = _heads(x, "x", (torch.bfloat16, torch.float32))
     if dst is None:
-        dst = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        dst = _like(x)
     pd, dt, dh = _heads(dst, "dst", (x.dtype,), x.shape)
     pp, pf, rot = _rotary(positions, inv_freq, x.shape[0])
     _stream()
@@ -544,13 +560,13 @@ def mx_cache_attention(cache: MXCache, q: torch.Tensor, q_starts: torch.Tensor, 
             raise ValueError(f"tree has {words} words a row, max_q = {max_q} new tokens need {-(-max_q // 64)}")
         pt = _dev(tree, "tree")
     if out is None:
-        out = torch.empty((total, heads, dim), dtype=torch.bfloat16, device=q.device)
+        out = _like(q)
     _want(out, "out", torch.bfloat16, (total, heads, dim))
     po = _dev(out, "out")
     need = _lib.mx_cache_attention_workspace(pc, heads, batch, total, max_q, max_kv)
     if need < 0:
         raise MXError(need)
-    space = torch.empty(need, dtype=torch.uint8, device=q.device) if need else None
+    space = kv_lens.new_empty(need // 4) if need else None  # int32: 4 bytes each
     _stream()
     _call(_lib.mx_cache_attention(pc, pq, qt, qh, heads, pst, pl, batch, block_table.data_ptr(), stride, pages, total,
                                   max_q, max_kv, pt, words, dim ** -0.5 if scale is None else scale, po,

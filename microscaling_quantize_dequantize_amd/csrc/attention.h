@@ -2,6 +2,8 @@
 // conversions, row statistics.
 #pragma once
 
+#include <atomic>
+
 #include "launch.h"
 
 namespace mx {
@@ -301,6 +303,19 @@ __device__ __forceinline__ unsigned clear_not_finite(unsigned *w) {
 }
 
 // ---- host ----
+
+// More than 64 KiB of LDS for a kernel, asked for once on each device (`done`: a bit for each).
+inline hipError_t allow_lds(const void *kernel, int bytes, std::atomic<uint64_t> &done) {
+  int dev = 0;
+  hipError_t e = hipGetDevice(&dev);
+  if (e != hipSuccess) return e;
+  const uint64_t bit = (uint64_t)1 << (dev & 63);
+  if (done.load(std::memory_order_relaxed) & bit) return hipSuccess;
+  e = hipFuncSetAttribute(kernel, hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == hipSuccess) done.fetch_or(bit, std::memory_order_relaxed);
+  return e;
+}
+
 Division attention_division_rows(int dim, int heads, int group, int batch, int64_t max_q, int64_t max_kv);
 Division attention_division_tiles(int dim, int heads, int group, int batch, int64_t max_q, int64_t max_kv);
 hipError_t launch_attention_rows(const AttentionArgs &a, const Division &d, hipStream_t stream);

@@ -407,11 +407,7 @@ template <int FMT, int D, int NT>
 static hipError_t start(const AttentionArgs &a, const Division &d, hipStream_t stream) {
   const int64_t grid = d.workers ? d.workers : (int64_t)a.batch * a.cache.heads * d.blocks;
   constexpr int bytes = 2 * NT * (D / 4 + 2) * 64 * 4;
-  if (bytes > 65536) {
-    const hipError_t e = hipFuncSetAttribute((const void *)k_attention_rows<FMT, D, NT>,
-                                             hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
-    if (e != hipSuccess) return e;
-  }
+  static_assert(bytes <= 65536, "more LDS than a kernel has without asking");
   k_attention_rows<FMT, D, NT><<<(unsigned)grid, 64 * ATT_WAVES, bytes, stream>>>(a, d);
   return hipGetLastError();
 }

@@ -377,8 +377,8 @@ template <int FMT, int D, int RB, int WAVES>
 static hipError_t start(const AttentionArgs &a, const Division &d, hipStream_t stream) {
   using T = Tiled<FMT, D, RB, WAVES>;
   const int64_t grid = d.workers ? d.workers : (int64_t)a.batch * a.cache.heads * d.blocks;
-  const hipError_t e = hipFuncSetAttribute((const void *)k_attention_tiles<FMT, D, RB, WAVES>,
-                                           hipFuncAttributeMaxDynamicSharedMemorySize, T::LDS);
+  static std::atomic<uint64_t> done{0};
+  const hipError_t e = allow_lds((const void *)k_attention_tiles<FMT, D, RB, WAVES>, T::LDS, done);
   if (e != hipSuccess) return e;
   k_attention_tiles<FMT, D, RB, WAVES><<<(unsigned)grid, T::THREADS, T::LDS, stream>>>(a, d);
   return hipGetLastError();

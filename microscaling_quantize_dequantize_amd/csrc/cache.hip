@@ -36,7 +36,6 @@ struct WriteArgs {
 
 __device__ __forceinline__ double bf16_f64(unsigned short b) { return (double)__uint_as_float((unsigned)b << 16); }
 
-// HEADVEC: 16-byte loads (strides and pointers allow them); otherwise 2-byte ones.
 template <bool VEC>
 __device__ __forceinline__ u32x4 load8(const unsigned short *p) {
   if (VEC) return *(const u32x4 *)p;
@@ -46,9 +45,13 @@ __device__ __forceinline__ u32x4 load8(const unsigned short *p) {
   return o;
 }
 
-// The 8 dimensions from d of a key x (a whole head), rotated; tab: cos and sin of the token's pairs.
-template <int LAYOUT, bool VEC>
-__device__ __forceinline__ u32x4 rotate8(const unsigned short *x, u32x4 w, int d, int half, const double *tc,
+// Where the partners of dimensions d .. d + 7 are, if they are one aligned piece (half layout, half a multiple of 8).
+__device__ __forceinline__ int partner_of(int d, int half) { return d < half ? d + half : d < 2 * half ? d - half : d; }
+
+// The 8 dimensions w from d of a key x (a whole head), rotated; q: their partners if ALIGNED; tc, ts: cosines and
+// sines of the token's pairs.
+template <int LAYOUT, bool ALIGNED>
+__device__ __forceinline__ u32x4 rotate8(const unsigned short *x, u32x4 w, u32x4 q, int d, int half, const double *tc,
                                          const double *ts) {
   if (d >= 2 * half) return w;
   double y[8];
@@ -65,11 +68,9 @@ __device__ __forceinline__ u32x4 rotate8(const unsigned short *x, u32x4 w, int d
       y[e] = in ? __builtin_fma(a, c, -(b * s)) : a;
       y[e + 1] = in ? __builtin_fma(b, c, a * s) : b;
     }
-  } else if (VEC && half % 8 == 0) {
-    // the partners are one aligned piece
+  } else if (ALIGNED) {
     const bool low = d < half;
     const int p = low ? d : d - half;
-    const u32x4 q = *(const u32x4 *)(x + (low ? d + half : d - half));
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
       const double a = bf16_f64(own[e]), b = bf16_f64((unsigned short)(q[e / 2] >> (16 * (e & 1))));
@@ -95,7 +96,12 @@ __device__ __forceinline__ u32x4 rotate8(const unsigned short *x, u32x4 w, int d
   return o;
 }
 
-template <int FMT, int LAYOUT, bool VEC>
+// A thread keeps its piece of 8 dimensions and takes (token, head) rows, WRITE_ROWS of them at a time so that their
+// loads are under way together.
+constexpr int WRITE_ROWS = 4;
+
+// VEC: 16-byte loads (strides and pointers allow them).  ALIGNED: half layout whose partners are whole pieces.
+template <int FMT, int LAYOUT, bool VEC, bool ALIGNED>
 __global__ __launch_bounds__(WRITE_THREADS) void k_cache_write(WriteArgs a) {
   __shared__ double tc[WRITE_TABLE], ts[WRITE_TABLE];
   const CacheView &cv = a.cache;
@@ -117,38 +123,53 @@ __global__ __launch_bounds__(WRITE_THREADS) void k_cache_write(WriteArgs a) {
   const int64_t st = value ? a.token_stride[1] : a.token_stride[0];
   const int64_t sh = value ? a.head_stride[1] : a.head_stride[0];
   uint8_t *codes = value ? cv.codes[1] : cv.codes[0], *scales = value ? cv.scales[1] : cv.scales[0];
-  const int pieces = cv.dim / 8, total = nh * nt * pieces;
-  // piece fastest, then token, then head: neighbouring tokens of a head are neighbours in their page.  total is a
-  // multiple of 4, so the four lanes of a scale are in the loop together.
-  for (int i = threadIdx.x; i < total; i += WRITE_THREADS) {
-    const int row = i / pieces, d = 8 * (i - row * pieces);
-    const int h = row / nt, t = row - h * nt;
-    const unsigned short *x = src + (t0 + t) * st + (h0 + h) * sh;
-    u32x4 w = load8<VEC>(x + d);
-    if (half) w = rotate8<LAYOUT, VEC>(x, w, d, half, tc + t * half, ts + t * half);
-    unsigned m = piece_amax_bf16(w);
-    m = umax(m, dpp<DPP_QUAD_1032>(m));
-    m = umax(m, dpp<DPP_QUAD_2301>(m));
-    const unsigned sb = scale_byte<FMT>(m << 16);
-    const float sc = scale_operand(sb);
-    const int64_t slot = a.slots[t0 + t];
-    if (slot < 0 || slot >= cv.pages << cv.page_log2) continue;  // padding: nothing is written
-    const int64_t pg = slot >> cv.page_log2;
-    const int r = (int)(slot & ((1 << cv.page_log2) - 1));
-    const int64_t ph = pg * cv.heads + h0 + h;
-    if (FMT == 0) {
-      unsigned c = fp4_from_bf16x8(w, sc);
-      if (sb == 255u) c = 0u;
-      *(unsigned *)(codes + ((ph << cv.page_log2) + r) * (cv.dim / 2) + d / 2) = c;
-    } else {
-      const unsigned c2 = e4m3_clamp_bf16x2(sb);
+  // rows: token fastest, then head, as neighbouring tokens of a head are neighbours in their page.  A row's pieces are
+  // a multiple of 4, so the four lanes of a scale are in the loop together; threads past the last whole row have none.
+  const int pieces = cv.dim / 8, pass = WRITE_THREADS / pieces;
+  const int d = 8 * ((int)threadIdx.x % pieces), first = threadIdx.x / pieces, rows = nh * nt;
+  if (first >= pass) return;
+  for (int row0 = first; row0 < rows; row0 += pass * WRITE_ROWS) {
+    u32x4 w[WRITE_ROWS], q[WRITE_ROWS];
+    int64_t slot[WRITE_ROWS];
+    const unsigned short *x[WRITE_ROWS];
 #pragma unroll
-      for (int k = 0; k < 4; ++k) w[k] = clamp_bf16x2(w[k], c2);
-      u32x2 c = fp8_from_bf16x8(w, sc);
-      if (sb == 255u) c = u32x2{0x7F7F7F7Fu, 0x7F7F7F7Fu};
-      *(u32x2 *)(codes + ((ph << cv.page_log2) + r) * cv.dim + d) = c;
+    for (int k = 0; k < WRITE_ROWS; ++k) {
+      int row = row0 + k * pass;
+      row = row < rows ? row : rows - 1;
+      const int h = row / nt, t = row - h * nt;
+      x[k] = src + (t0 + t) * st + (h0 + h) * sh;
+      w[k] = load8<VEC>(x[k] + d);
+      q[k] = ALIGNED ? load8<VEC>(x[k] + partner_of(d, half)) : w[k];
+      slot[k] = a.slots[t0 + t];
     }
-    if ((d & 31) == 0) scales[((ph * (cv.dim / 32) + d / 32) << cv.page_log2) + r] = (uint8_t)sb;
+#pragma unroll
+    for (int k = 0; k < WRITE_ROWS; ++k) {
+      const int row = row0 + k * pass;
+      const int h = (row < rows ? row : rows - 1) / nt, t = (row < rows ? row : rows - 1) - h * nt;
+      u32x4 v = w[k];
+      if (half) v = rotate8<LAYOUT, ALIGNED>(x[k], v, q[k], d, half, tc + t * half, ts + t * half);
+      unsigned m = piece_amax_bf16(v);
+      m = umax(m, dpp<DPP_QUAD_1032>(m));
+      m = umax(m, dpp<DPP_QUAD_2301>(m));
+      const unsigned sb = scale_byte<FMT>(m << 16);
+      const float sc = scale_operand(sb);
+      if (row >= rows || slot[k] < 0 || slot[k] >= cv.pages << cv.page_log2) continue;  // padding: nothing is written
+      const int64_t ph = (slot[k] >> cv.page_log2) * cv.heads + h0 + h;
+      const int r = (int)(slot[k] & ((1 << cv.page_log2) - 1));
+      if (FMT == 0) {
+        unsigned c = fp4_from_bf16x8(v, sc);
+        if (sb == 255u) c = 0u;
+        *(unsigned *)(codes + ((ph << cv.page_log2) + r) * (cv.dim / 2) + d / 2) = c;
+      } else {
+        const unsigned c2 = e4m3_clamp_bf16x2(sb);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] = clamp_bf16x2(v[i], c2);
+        u32x2 c = fp8_from_bf16x8(v, sc);
+        if (sb == 255u) c = u32x2{0x7F7F7F7Fu, 0x7F7F7F7Fu};
+        *(u32x2 *)(codes + ((ph << cv.page_log2) + r) * cv.dim + d) = c;
+      }
+      if ((d & 31) == 0) scales[((ph * (cv.dim / 32) + d / 32) << cv.page_log2) + r] = (uint8_t)sb;
+    }
   }
 }
 
@@ -168,14 +189,20 @@ hipError_t launch_cache_write(const CacheView &cache, const void *k, const int64
   const dim3 grid((unsigned)tiles, (unsigned)((cache.heads + a.heads_per_wg - 1) / a.heads_per_wg), 2);
   bool vec = ((uintptr_t)k | (uintptr_t)v) % 16 == 0;
   for (int i = 0; i < 2; ++i) vec = vec && k_strides[i] % 8 == 0 && v_strides[i] % 8 == 0;
-#define MX_WRITE(F, L, V) k_cache_write<F, L, V><<<grid, WRITE_THREADS, 0, stream>>>(a)
+#define MX_WRITE(F, L, V, A) k_cache_write<F, L, V, A><<<grid, WRITE_THREADS, 0, stream>>>(a)
+#define MX_FORMAT(F)                                                        \
+  if (layout == ROTARY_INTERLEAVED) {                                       \
+    if (vec) MX_WRITE(F, ROTARY_INTERLEAVED, true, false);                  \
+    else MX_WRITE(F, ROTARY_INTERLEAVED, false, false);                     \
+  } else if (vec && a.half % 8 == 0) MX_WRITE(F, ROTARY_HALF, true, true);  \
+  else if (vec) MX_WRITE(F, ROTARY_HALF, true, false);                      \
+  else MX_WRITE(F, ROTARY_HALF, false, false)
   if (cache.fmt == 0) {
-    if (layout == ROTARY_HALF) { if (vec) MX_WRITE(0, ROTARY_HALF, true); else MX_WRITE(0, ROTARY_HALF, false); }
-    else { if (vec) MX_WRITE(0, ROTARY_INTERLEAVED, true); else MX_WRITE(0, ROTARY_INTERLEAVED, false); }
+    MX_FORMAT(0);
   } else {
-    if (layout == ROTARY_HALF) { if (vec) MX_WRITE(1, ROTARY_HALF, true); else MX_WRITE(1, ROTARY_HALF, false); }
-    else { if (vec) MX_WRITE(1, ROTARY_INTERLEAVED, true); else MX_WRITE(1, ROTARY_INTERLEAVED, false); }
+    MX_FORMAT(1);
   }
+#undef MX_FORMAT
 #undef MX_WRITE
   return hipGetLastError();
 }
