@@ -179,6 +179,15 @@ __device__ __forceinline__ unsigned first_bits(int n) {
 // rescaled: weights stay below 2^8, and most tiles need no rescaling.
 constexpr float LAG = 8.0f;
 
+// Sums times f.  ACC: they are in accumulation registers, which the vector units do not reach, and are moved for this
+// here and nowhere else (left to itself the compiler moves them in every tile, for the branch's sake).
+template <bool ACC, typename V>
+__device__ __forceinline__ void rescale(V &o, float f) {
+  if (ACC) asm volatile("" : "+a"(o));
+  o *= f;
+  if (ACC) asm volatile("" : "+a"(o));
+}
+
 // Which sums of exponentials give a result (none: the row saw nothing) and its reciprocal; NaN stays NaN.
 __device__ __forceinline__ float reciprocal(float l) { return l == 0.0f ? 0.0f : 1.0f / l; }
 

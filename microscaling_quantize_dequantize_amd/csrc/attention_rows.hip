@@ -135,6 +135,7 @@ __device__ __forceinline__ void spoil(f32x4 (&acc)[W], int base, const uint8_t *
 template <int FMT, int D, int NT>
 __global__ __launch_bounds__(64 * ATT_WAVES, NT == 1 && D <= 128 ? 2 : 1) void k_attention_rows(AttentionArgs a, Division dv) {
   using A = Att<FMT, D>;
+  constexpr bool ACC = NT > 1 || D > 128;  // one wave a SIMD: the sums are in accumulation registers
   extern __shared__ float lds[];
   const CacheView &cv = a.cache;
   const int wave = uniform((int)threadIdx.x / 64), lane = threadIdx.x % 64, n16 = lane % 16, g = lane / 16;
@@ -284,7 +285,7 @@ __global__ __launch_bounds__(64 * ATT_WAVES, NT == 1 && D <= 128 ? 2 : 1) void k
         st.m[n] = m;
         st.l[n] *= f;
 #pragma unroll
-        for (int i = 0; i < D / 16; ++i) st.o[n][i] *= f;
+        for (int i = 0; i < D / 16; ++i) rescale<ACC>(st.o[n][i], f);
       }
       const float m = st.m[n] == -__builtin_inff() ? 0.0f : st.m[n];
       float w[16];  // by token

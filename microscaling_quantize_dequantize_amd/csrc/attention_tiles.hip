@@ -74,6 +74,7 @@ __global__ __launch_bounds__(64 * WAVES, D <= 128 ? 2 : 1) void k_attention_tile
   const int wave = uniform((int)threadIdx.x / 64), lane = threadIdx.x % 64, n32 = lane % 32, h = lane / 32;
   const int page_mask = (1 << cv.page_log2) - 1;
   lds_int *flags = (lds_int *)(lds + 2 * T::BUFFER);  // [0]: a page outside the cache, [1]: values that are not finite in a masked tile
+  constexpr bool ACC = D > 128 && WAVES == 4;  // one wave a SIMD: the sums are in accumulation registers
   constexpr int VG = D % 128 == 0 ? 4 : D % 96 == 0 ? 3 : 2;  // V operands of a group
   constexpr int PARTS = D / 32 / VG;                           // groups for 16 tokens
   const float to_log2 = a.scale * 1.4426950408889634f;
@@ -276,7 +277,7 @@ __global__ __launch_bounds__(64 * WAVES, D <= 128 ? 2 : 1) void k_attention_tile
           m[n] = big;
           l[n] *= f;
 #pragma unroll
-          for (int i = 0; i < D / 32; ++i) o[n][i] *= f;
+          for (int i = 0; i < D / 32; ++i) rescale<ACC>(o[n][i], f);
         }
         base[n] = m[n] == -__builtin_inff() ? 0.0f : m[n];
       }
