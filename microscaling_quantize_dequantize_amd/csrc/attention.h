@@ -311,6 +311,9 @@ __device__ __forceinline__ unsigned clear_not_finite(unsigned *w) {
   return any;
 }
 
+// Workgroups of the few-rows kernel that a CU holds at once (waves of a SIMD): what its registers allow.
+constexpr int rows_held(int dim, int nt) { return nt > 1 || dim > 128 ? 1 : dim <= 64 ? 3 : 2; }
+
 // ---- host ----
 
 // More than 64 KiB of LDS for a kernel, asked for once on each device (`done`: a bit for each).

@@ -132,10 +132,10 @@ static Division divide(int rows, int64_t workers, int min_tiles, int heads, int 
 
 Division attention_division_rows(int dim, int heads, int group, int batch, int64_t max_q, int64_t max_kv) {
   const int rows = max_q * group <= 16 ? 16 : 32;
-  // One run for every workgroup that the CUs hold at once (two where 256 registers are enough); of several sequences,
+  // One run for every workgroup that the CUs hold at once (rows_held); of several sequences,
   // whose lengths differ as a rule, two, so that a CU that has finished early takes another: 64 ragged sequences in
   // MXFP8 224 us against 235 with one run each, 64 equal ones 384 against 381, one of 500000 tokens 129 against 120.
-  const int64_t held = (rows == 16 && dim <= 128 ? 2 : 1) * (int64_t)device_cu_count();
+  const int64_t held = rows_held(dim, rows / 16) * (int64_t)device_cu_count();
   return divide(rows, batch > 1 ? 2 * held : held, 4, heads, group, batch, max_q, max_kv);
 }
 

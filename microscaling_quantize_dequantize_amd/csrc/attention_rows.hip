@@ -133,7 +133,7 @@ __device__ __forceinline__ void spoil(f32x4 (&acc)[W], int base, const uint8_t *
 }
 
 template <int FMT, int D, int NT>
-__global__ __launch_bounds__(64 * ATT_WAVES, NT == 1 && D <= 128 ? 2 : 1) void k_attention_rows(AttentionArgs a, Division dv) {
+__global__ __launch_bounds__(64 * ATT_WAVES, rows_held(D, NT)) void k_attention_rows(AttentionArgs a, Division dv) {
   using A = Att<FMT, D>;
   constexpr bool ACC = NT > 1 || D > 128;  // one wave a SIMD: the sums are in accumulation registers
   extern __shared__ float lds[];

@@ -104,10 +104,67 @@ __global__ __launch_bounds__(ROPE_THREADS) void k_rope(const T *__restrict__ src
   }
 }
 
+// Half layout whose halves are not whole pieces: a thread has a piece of the row as it lies in memory, and takes the
+// partners of its elements out of LDS, where the workgroup has put the rows' pieces.  (In pieces of single pairs the
+// same case, 62 of 128 dimensions rotated, took 140 us for the 8192 x 64 heads that take 42 with whole pieces.)
+// Every row is in LDS before any of it is written, so dst may be src.
+template <typename T, int VEC>
+__global__ __launch_bounds__(ROPE_THREADS) void k_rope_staged(const T *__restrict__ src, T *__restrict__ dst,
+                                                              RopeArgs a) {
+  __shared__ float tc[ROPE_TABLE], ts[ROPE_TABLE];
+  __shared__ Piece<T, VEC> rows[2][ROPE_THREADS];
+  const int64_t t0 = (int64_t)blockIdx.x * a.per_wg;
+  const int nt = (int)(a.tokens - t0 < a.per_wg ? a.tokens - t0 : a.per_wg);
+  for (int i = threadIdx.x; i < nt * a.half; i += ROPE_THREADS) {
+    const int t = i / a.half, p = i - t * a.half;
+    double s, c;
+    sine_cosine((double)a.positions[t0 + t] * a.inv_freq[p], s, c);
+    tc[i] = (float)(c * a.scale);
+    ts[i] = (float)(a.inverse ? -s * a.scale : s * a.scale);
+  }
+  const int items = a.dim / VEC, step = ROPE_THREADS / items;
+  const int first = threadIdx.x / items, d = (threadIdx.x - first * items) * VEC, total = nt * a.heads;
+  float c[VEC], s[VEC];
+  int with = -1;  // the token whose angles these are
+  for (int base = 0, turn = 0; base < total; base += step, turn ^= 1) {
+    const int row = base + first;
+    const bool in = first < step && row < total;
+    const int t = in ? row / a.heads : 0, h = row - t * a.heads;
+    Piece<T, VEC> u;
+    if (in) rows[turn][threadIdx.x] = u = *(const Piece<T, VEC> *)(src + (t0 + t) * a.src_token + h * a.src_head + d);
+    __syncthreads();  // (the other turn's rows are read until the barrier after this one)
+    if (!in) continue;
+    if (t != with) {
+      with = t;
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) {
+        const int p = d + e < a.half ? d + e : d + e - a.half;
+        const bool turned = d + e < 2 * a.half;
+        c[e] = turned ? tc[t * a.half + p] : 1.0f;
+        s[e] = turned ? (d + e < a.half ? -ts[t * a.half + p] : ts[t * a.half + p]) : 0.0f;
+      }
+    }
+    const T *mine = (const T *)&rows[turn][first * items];
+#pragma unroll
+    for (int e = 0; e < VEC; ++e)
+      if (d + e < 2 * a.half) {
+        const float f = to_f32(u.v[e]), g = to_f32(mine[d + e < a.half ? d + e + a.half : d + e - a.half]);
+        from_f32(u.v[e], f * c[e] + g * s[e]);
+      }
+    *(Piece<T, VEC> *)(dst + (t0 + t) * a.dst_token + h * a.dst_head + d) = u;
+  }
+}
+
 template <typename T, int VEC, int LAYOUT>
 static void rope_start(const void *src, void *dst, const RopeArgs &a, hipStream_t stream) {
   const unsigned grid = (unsigned)((a.tokens + a.per_wg - 1) / a.per_wg);
   k_rope<T, VEC, LAYOUT><<<grid, ROPE_THREADS, 0, stream>>>((const T *)src, (T *)dst, a);
+}
+
+template <typename T, int VEC>
+static void rope_staged(const void *src, void *dst, const RopeArgs &a, hipStream_t stream) {
+  const unsigned grid = (unsigned)((a.tokens + a.per_wg - 1) / a.per_wg);
+  k_rope_staged<T, VEC><<<grid, ROPE_THREADS, 0, stream>>>((const T *)src, (T *)dst, a);
 }
 
 template <typename T, int LAYOUT>
@@ -127,14 +184,17 @@ hipError_t launch_rope(int dtype, const void *src, void *dst, int64_t tokens, in
   const int size = dtype == 1 ? 4 : 2;
   RopeArgs a{tokens, strides[0], strides[1], strides[2], strides[3], positions, inv_freq, scale,
              (int)heads, (int)dim, (int)(rot / 2), 1, inverse, src != dst};
-  // the widest piece, up to 16 bytes, at which every access is aligned and no piece is cut
-  int vec = 16 / size;
-  for (; vec > 1; vec /= 2) {
-    bool ok = dim % vec == 0 && (layout == ROTARY_INTERLEAVED || a.half % vec == 0) &&
-              (uintptr_t)src % (vec * size) == 0 && (uintptr_t)dst % (vec * size) == 0;
-    for (int i = 0; i < 4; ++i) ok = ok && strides[i] % vec == 0;
+  // the widest piece, up to 16 bytes, at which every access is aligned and no head is cut; in the half layout the
+  // halves should not be cut either
+  int wide = 16 / size;
+  for (; wide > 1; wide /= 2) {
+    bool ok = dim % wide == 0 && (uintptr_t)src % (wide * size) == 0 && (uintptr_t)dst % (wide * size) == 0;
+    for (int i = 0; i < 4; ++i) ok = ok && strides[i] % wide == 0;
     if (ok) break;
   }
+  int vec = wide;
+  while (layout == ROTARY_HALF && a.half % vec != 0) vec /= 2;
+  const bool staged = vec < wide && wide >= 4 && dim / wide <= ROPE_THREADS;
   // tokens of a workgroup: about four 16-byte pieces for each of its threads, as long as the table holds them and
   // there are four workgroups for every CU
   const int64_t row = heads * dim * size;
@@ -143,7 +203,11 @@ hipError_t launch_rope(int dtype, const void *src, void *dst, int64_t tokens, in
   const int64_t spread = tokens / (4 * device_cu_count());
   if (per > spread) per = spread;
   a.per_wg = per < 1 ? 1 : (int)per;
-  if (dtype == 1) {
+  if (staged) {
+    if (dtype == 1) rope_staged<float, 4>(src, dst, a, stream);
+    else if (wide == 8) rope_staged<unsigned short, 8>(src, dst, a, stream);
+    else rope_staged<unsigned short, 4>(src, dst, a, stream);
+  } else if (dtype == 1) {
     if (layout == ROTARY_HALF) rope_vec<float, ROTARY_HALF>(vec, src, dst, a, stream);
     else rope_vec<float, ROTARY_INTERLEAVED>(vec, src, dst, a, stream);
   } else {

@@ -67,6 +67,19 @@ def test_strides_and_alignment(mx, layout, offset, pad):
     assert torch.equal(wide, whole)  # nothing outside the view was touched
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_halves_that_cut_pieces_in_place(mx, dtype):
+    """62 of 128 dimensions, many rows a workgroup, written over the input."""
+    g = torch.Generator(device="cuda").manual_seed(62)
+    x = torch.randn((37, 70, 128), generator=g, device="cuda").to(dtype)
+    pos = torch.randint(0, 1 << 17, (37,), generator=g, device="cuda")
+    f = frequencies(31)
+    y = mx.mx_rope(x, pos, f, scale=0.5)
+    check(y, x, pos, f, 0.5, HALF, False)
+    mx.mx_rope(x, pos, f, scale=0.5, dst=x)
+    assert torch.equal(x, y)
+
+
 def test_far_positions_keep_their_angle(mx):
     """Angles near 2^31 and beyond are reduced in 64 bits: the same bound holds."""
     x = torch.randn((4, 2, 8), device="cuda")
