@@ -21,7 +21,7 @@
 namespace mx {
 
 constexpr int WRITE_THREADS = 256;
-constexpr int WRITE_TABLE = 2048;  // (token, pair) entries: 32 KiB of LDS
+constexpr int WRITE_TABLE = 1024;  // (token, pair) entries: 16 KiB of LDS
 
 struct WriteArgs {
   CacheView cache;
@@ -179,7 +179,7 @@ hipError_t launch_cache_write(const CacheView &cache, const void *k, const int64
                               hipStream_t stream) {
   WriteArgs a{cache, {(const unsigned short *)k, (const unsigned short *)v}, {k_strides[0], v_strides[0]},
               {k_strides[1], v_strides[1]}, slots, positions, inv_freq, scale, tokens, (int)(rot / 2), 0, 0};
-  a.tile = 16;
+  a.tile = 8;
   while (a.half * a.tile > WRITE_TABLE) a.tile /= 2;
   // all heads of a tile share its angles, unless there are too few tiles to fill the CUs
   const int64_t tiles = (tokens + a.tile - 1) / a.tile;

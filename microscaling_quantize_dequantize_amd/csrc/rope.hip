@@ -39,6 +39,8 @@ __device__ __forceinline__ float to_f32(float f) { return f; }
 __device__ __forceinline__ void from_f32(unsigned short &d, float f) { d = (unsigned short)bf16x2_rne(f, 0.0f); }
 __device__ __forceinline__ void from_f32(float &d, float f) { d = f; }
 
+constexpr int ROPE_ROWS = 2;  // rows whose loads a thread has under way together, the first ones before the angles
+
 template <typename T, int VEC, int LAYOUT>
 __global__ __launch_bounds__(ROPE_THREADS) void k_rope(const T *__restrict__ src, T *__restrict__ dst, RopeArgs a) {
   __shared__ float tc[ROPE_TABLE], ts[ROPE_TABLE];
@@ -50,6 +52,69 @@ __global__ __launch_bounds__(ROPE_THREADS) void k_rope(const T *__restrict__ src
   const int items = turned + (a.copy ? (a.dim - rest0) / V : 0);
   const int64_t t0 = (int64_t)blockIdx.x * a.per_wg;
   const int nt = (int)(a.tokens - t0 < a.per_wg ? a.tokens - t0 : a.per_wg);
+  const int total = nt * a.heads;
+  // a thread keeps its place in the head while the heads fit a pass of the workgroup
+  const int step = items < ROPE_THREADS ? ROPE_THREADS / items : 1;
+  const int first = items < ROPE_THREADS ? threadIdx.x / items : 0;
+  const int item0 = threadIdx.x - first * items;
+  const bool active = first < step && item0 < items;  // not so: threads past the last whole head
+
+  Piece<T, V> u[ROPE_ROWS], w[ROPE_ROWS];
+  auto offsets = [&](int item, int &da, int &db) {  // of the piece, and of the pairs' second elements
+    const int p = item * V;
+    da = item >= turned ? rest0 + (item - turned) * V : !PAIRS || LAYOUT == ROTARY_HALF ? p : 2 * p;
+    db = LAYOUT == ROTARY_HALF ? p + a.half : 2 * p + 1;
+  };
+  auto load = [&](int item, int base) {
+    int da, db;
+    offsets(item, da, db);
+#pragma unroll
+    for (int k = 0; k < ROPE_ROWS; ++k) {
+      const int row = base + k * step;
+      if (row >= total) break;
+      const int t = row / a.heads, h = row - t * a.heads;
+      const T *x = src + (t0 + t) * a.src_token + h * a.src_head;
+      u[k] = *(const Piece<T, V> *)(x + da);
+      if (PAIRS && item < turned) w[k] = *(const Piece<T, V> *)(x + db);
+    }
+  };
+  auto finish = [&](int item, int base) {
+    int da, db;
+    offsets(item, da, db);
+#pragma unroll
+    for (int k = 0; k < ROPE_ROWS; ++k) {
+      const int row = base + k * step;
+      if (row >= total) break;
+      const int t = row / a.heads, h = row - t * a.heads;
+      T *y = dst + (t0 + t) * a.dst_token + h * a.dst_head;
+      if (item < turned) {
+        const float *c = tc + t * a.half, *s = ts + t * a.half;
+        if (PAIRS) {
+          const int p = item * V;
+#pragma unroll
+          for (int e = 0; e < V; ++e) {
+            const float f = to_f32(u[k].v[e]), g = to_f32(w[k].v[e]);
+            from_f32(u[k].v[e], f * c[p + e] - g * s[p + e]);
+            from_f32(w[k].v[e], g * c[p + e] + f * s[p + e]);
+          }
+          *(Piece<T, V> *)(y + db) = w[k];
+        } else {
+          const int p = da / 2;
+#pragma unroll
+          for (int e = 0; e < V / 2; ++e) {
+            if (p + e < a.half) {  // the last piece may hold elements that are not rotated
+              const float f = to_f32(u[k].v[2 * e]), g = to_f32(u[k].v[2 * e + 1]);
+              from_f32(u[k].v[2 * e], f * c[p + e] - g * s[p + e]);
+              from_f32(u[k].v[2 * e + 1], g * c[p + e] + f * s[p + e]);
+            }
+          }
+        }
+      }
+      *(Piece<T, V> *)(y + da) = u[k];
+    }
+  };
+
+  if (active) load(item0, first);
   for (int i = threadIdx.x; i < nt * a.half; i += ROPE_THREADS) {
     const int t = i / a.half, p = i - t * a.half;
     double s, c;
@@ -58,50 +123,12 @@ __global__ __launch_bounds__(ROPE_THREADS) void k_rope(const T *__restrict__ src
     ts[i] = (float)(a.inverse ? -s * a.scale : s * a.scale);
   }
   __syncthreads();
-  const int total = nt * a.heads;
-  // a thread keeps its place in the head while the heads fit a pass of the workgroup
-  for (int item = threadIdx.x % (items < ROPE_THREADS ? items : ROPE_THREADS); item < items; item += ROPE_THREADS) {
-    const int step = items < ROPE_THREADS ? ROPE_THREADS / items : 1;
-    const int first = items < ROPE_THREADS ? threadIdx.x / items : 0;
-    if (first >= step) break;  // the threads past the last whole head
-    for (int row = first; row < total; row += step) {
-      const int t = row / a.heads, h = row - t * a.heads;
-      const T *x = src + (t0 + t) * a.src_token + h * a.src_head;
-      T *y = dst + (t0 + t) * a.dst_token + h * a.dst_head;
-      if (item >= turned) {
-        const int d = rest0 + (item - turned) * V;
-        *(Piece<T, V> *)(y + d) = *(const Piece<T, V> *)(x + d);
-        continue;
-      }
-      if (PAIRS) {
-        const int p = item * V;
-        const int da = LAYOUT == ROTARY_HALF ? p : 2 * p, db = LAYOUT == ROTARY_HALF ? p + a.half : 2 * p + 1;
-        Piece<T, V> u = *(const Piece<T, V> *)(x + da), w = *(const Piece<T, V> *)(x + db);
-        const float *c = tc + t * a.half + p, *s = ts + t * a.half + p;
-#pragma unroll
-        for (int e = 0; e < V; ++e) {
-          const float f = to_f32(u.v[e]), g = to_f32(w.v[e]);
-          from_f32(u.v[e], f * c[e] - g * s[e]);
-          from_f32(w.v[e], g * c[e] + f * s[e]);
-        }
-        *(Piece<T, V> *)(y + da) = u;
-        *(Piece<T, V> *)(y + db) = w;
-      } else {
-        const int d = item * V, p = d / 2;
-        Piece<T, V> u = *(const Piece<T, V> *)(x + d);
-        const float *c = tc + t * a.half, *s = ts + t * a.half;
-#pragma unroll
-        for (int e = 0; e < V / 2; ++e) {
-          if (p + e < a.half) {  // the last piece may hold elements that are not rotated
-            const float f = to_f32(u.v[2 * e]), g = to_f32(u.v[2 * e + 1]);
-            from_f32(u.v[2 * e], f * c[p + e] - g * s[p + e]);
-            from_f32(u.v[2 * e + 1], g * c[p + e] + f * s[p + e]);
-          }
-        }
-        *(Piece<T, V> *)(y + d) = u;
-      }
+  if (!active) return;
+  for (int item = item0; item < items; item += ROPE_THREADS)
+    for (int base = first; base < total; base += ROPE_ROWS * step) {
+      if (item != item0 || base != first) load(item, base);
+      finish(item, base);
     }
-  }
 }
 
 // Half layout whose halves are not whole pieces: a thread has a piece of the row as it lies in memory, and takes the
