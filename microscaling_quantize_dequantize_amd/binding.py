@@ -382,7 +382,8 @@ def _heads(t, name: str, dtypes, shape=None):
     if one != 1 and t.shape[2] > 1:
         raise ValueError(f"the dimensions of {name} must be contiguous")
     _place(t, name)
-    return t.data_ptr(), token, head
+    # the stride of a single token or head is whatever its view left there
+    return t.data_ptr(), token if t.shape[0] > 1 else 0, head if t.shape[1] > 1 else 0
 
 
 def _vector(t, name: str, dtype: torch.dtype, n: int) -> int:

@@ -13,10 +13,10 @@ constexpr int TILE = 64;  // tokens of a tile, the unit of the division
 // How the work is divided.  An item is a block of rows of one key/value head of one sequence, its work the tiles of
 // 64 tokens that it reads; items follow one another by sequence, head and block.  `workers` workgroups take equal
 // runs of tiles (not less than min_tiles), so that ragged sequences need no host copy of their lengths to be spread
-// evenly.  A run that covers an item whole writes the result; pieces of an item go to the worker's slots of the
-// workspace (slot 0: a piece that continues its item, which only the run's first can; slot 1: one that begins it, which then is
-// the run's last) and are
-// joined by k_join.  workers == 0: one workgroup for each item, nothing to join.
+// evenly.  A run that covers an item whole writes the result; pieces of an item go to the worker's two slots of the
+// workspace and are joined by k_join.  Slot 0 is for a piece that continues its item, which only the run's first can;
+// slot 1 for one that begins its item, which then is the run's last.  workers == 0: one workgroup for each item,
+// nothing to join.
 struct Division {
   int workers, min_tiles, rows;  // rows: of a block
   int blocks, tiles;             // host's bounds on an item's blocks and tiles
@@ -226,7 +226,8 @@ struct Pieces {
       int64_t work = lane < a.batch ? sequence_work(a, lane, d.rows) : 0;
       const int64_t upto = wave_prefix(work, lane);
       int64_t total = __shfl(upto, 63);
-      for (int b0 = 64; b0 < a.batch; b0 += 64) total += wave_sum(b0 + lane < a.batch ? sequence_work(a, b0 + lane, d.rows) : 0);
+      for (int b0 = 64; b0 < a.batch; b0 += 64)
+        total += wave_sum(b0 + lane < a.batch ? sequence_work(a, b0 + lane, d.rows) : 0);
       total = uniform(total);
       per = (total + d.workers - 1) / d.workers;
       per = per < d.min_tiles ? d.min_tiles : per;

@@ -1,24 +1,30 @@
-// Attention of new tokens over the paged MX cache.
+// Attention of new tokens over the paged MX cache, for up to 32 rows of a
+// key/value head (16 where heads have more than 128 dimensions): single tokens,
+// small trees.
 //
 //   out[i] = sum_j p_ij v_j / sum_j p_ij,  p_ij = exp(scale q_i . k_j - m_i)
 //   over the tokens j that row i sees: all before the sequence's new tokens,
 //   and of those the ones up to its own (causal) or those that its bits name
 //   (a tree of drafted tokens).  A row that sees nothing gives zeros.
 //
+// Bound: HBM, every code and scale once (FETCH: TCC misses of 128 bytes equal
+// the bytes of the case).  Measured on MI355X: 64 sequences of 16384, 8 heads of
+// 128, 4 query heads each: MXFP8 381-384 us, 5.8 TB/s; MXFP4 227-235 us, 5.0 TB/s,
+// where conversions and softmax of half the bytes take the vector units over half
+// of the time; one sequence of 500000 in MXFP4 111 us, 4.9 TB/s.
+//
 // Rows: the queries of the `group` heads that share a key/value head, for all
 // new tokens of the sequence, are the rows of one product: row = token * group
-// + head in the group.  A workgroup takes 16 NT rows and a span of the
-// sequence's tokens, its four waves take units of 64 tokens of it in turn, each
-// with a running maximum and sum of its own, and join in LDS at the end.  Long
-// spans are split over workgroups, whose unnormalised fp32 sums are joined by a
-// second kernel.
+// + head in the group.  A workgroup takes a run of tiles of 64 tokens (see the
+// division in attention.h), its four waves every fourth of them, each with a
+// running maximum and sum of its own, and join in LDS at the end of an item.
 //
 // Everything between the loads and the end stays in the lane that it is in.
 // S^T = K Q^T and O^T = V^T P^T on v_mfma_f32_16x16x32_bf16 (lane l holds for
 // column or row l % 16 of an operand the 8 elements of k = 8 (l / 16) ..; and
 // of the result column l % 16, rows 4 (l / 16) ..).  Which token or dimension
 // an index of k means is free as long as both operands agree:
-//   - tile t of a unit takes tokens 4 m + t as its rows m, so that a lane's
+//   - a tile's score products t = 0 .. 3 take tokens 4 m + t as their rows m, so that a lane's
 //     four K rows are neighbours, with one 32-bit load for their scales, and
 //     the lane holds the scores of the 16 tokens 16 (l / 16) .. of its row;
 //   - a lane's share of a K row is D/4 neighbouring dimensions;
@@ -30,7 +36,8 @@
 // to bf16's smallest normal, queries are bf16, products are accumulated in
 // fp32, the maximum, the sum and the output's sums are fp32.  The weights p are
 // rounded to bf16 (at most 2^-8 of each, independent of one another) for
-// the second product; their sum takes them unrounded.
+// the second product, and their sum takes them rounded, so that the weights add
+// up to one.
 #include "attention.h"
 
 namespace mx {

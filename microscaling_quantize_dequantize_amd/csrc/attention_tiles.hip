@@ -5,7 +5,9 @@
 // much, the vector units (an exponential a pair, which takes four issues).  So
 // keys and values are converted once for a workgroup's 128 or 256 rows: tiles
 // of 64 tokens are widened to bf16 on their way into LDS, two tiles in turn,
-// while the codes of the tile after them are on their way from memory.
+// while the codes of the tile after them are on their way from memory.  The
+// conversion of a tile is issued between the products of the scores before it,
+// the weights of 16 tokens between the products of the 16 before them.
 //
 // S^T = K Q^T and O^T = V^T P^T on v_mfma_f32_32x32x16_bf16: lane l holds for
 // row or column l % 32 of an operand the 8 elements k = 8 (l / 32) .., and of
@@ -16,14 +18,21 @@
 // transposing reads of four tokens by 16 dimensions.  Row statistics need one
 // exchange between the wave's halves.
 //
-// A wave takes 32 RB rows.  With RB = 2 an operand read from LDS serves two
-// products, which halves the LDS traffic (64 bytes a clock of its 128 at full
-// rate of the matrix cores).
+// A wave takes 32 rows: heads of up to 128 dimensions then fit the 256
+// registers of two waves a SIMD, larger ones have one wave and keep the sums
+// in accumulation registers.  (64 rows a wave halve the LDS reads, and measured
+// the same or slower: 4 waves of 64 rows 125 us where 8 of 32 took 108.)
 //
 // LDS rows are padded so that the reads are free of bank conflicts: K rows by
 // 16 bytes (16 lanes' 16-byte reads of one column are then 4 banks apart),
 // V rows to 16 or 48 banks past a multiple of 64 (four tokens' 64 bytes are
 // then apart).
+//
+// Measured on MI355X: 8 sequences x 64 heads over 8 of 128 (MXFP8), 64 new
+// tokens over 32768: 625-640 us, 0.86-0.88 PFLOP/s (a library product of 16384^3
+// in bf16 1.37), its clock falling to 1.85 GHz from 2.2; with 8192 tokens 0.74,
+// heads of 256 0.71.  2 us a tile of 64 tokens by 256 rows; a piece costs some 15 us
+// beside its tiles (plan, first loads, writing and joining the sums).
 #include "attention.h"
 
 namespace mx {
@@ -32,10 +41,11 @@ typedef short i16x4 __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) i16x4 lds_i16x4;
 typedef __attribute__((address_space(3))) uint8_t lds_u8;
 typedef __attribute__((address_space(3))) int lds_int;
+typedef __attribute__((address_space(3))) u32x4 lds_u32x4;
 
-template <int FMT, int D, int RB, int WAVES> struct Tiled {
+template <int FMT, int D, int WAVES> struct Tiled {
   static constexpr int THREADS = 64 * WAVES;
-  static constexpr int ROWS = 32 * RB * WAVES;
+  static constexpr int ROWS = 32 * WAVES;
   static constexpr int CODE = FMT == 0 ? 8 : 16;                       // bytes of 16 dimensions
   static constexpr int ROW = D / 16;                                   // such units of a row
   static constexpr int SHARE = THREADS / TILE;                         // threads of a token
@@ -66,14 +76,15 @@ __device__ __forceinline__ u32x4 read_v(const lds_u8 *p, int far) {
   return u32x4{a.x, a.y, b.x, b.y};
 }
 
-template <int FMT, int D, int RB, int WAVES>
+template <int FMT, int D, int WAVES>
 __global__ __launch_bounds__(64 * WAVES, D <= 128 ? 2 : 1) void k_attention_tiles(AttentionArgs a, Division dv) {
-  using T = Tiled<FMT, D, RB, WAVES>;
+  using T = Tiled<FMT, D, WAVES>;
   extern __shared__ __align__(16) uint8_t lds[];
   const CacheView &cv = a.cache;
   const int wave = uniform((int)threadIdx.x / 64), lane = threadIdx.x % 64, n32 = lane % 32, h = lane / 32;
   const int page_mask = (1 << cv.page_log2) - 1;
-  lds_int *flags = (lds_int *)(lds + 2 * T::BUFFER);  // [0]: a page outside the cache, [1]: values that are not finite in a masked tile
+  // [0]: a page outside the cache was met, [1]: values that are not finite in a tile that needs a mask
+  lds_int *flags = (lds_int *)(lds + 2 * T::BUFFER);
   constexpr bool ACC = D > 128 && WAVES == 4;  // one wave a SIMD: the sums are in accumulation registers
   constexpr int VG = D % 128 == 0 ? 4 : D % 96 == 0 ? 3 : 2;  // V operands of a group
   constexpr int PARTS = D / 32 / VG;                           // groups for 16 tokens
@@ -84,36 +95,26 @@ __global__ __launch_bounds__(64 * WAVES, D <= 128 ? 2 : 1) void k_attention_tile
     const int head = uniform(pc.head), rb = uniform(pc.block);
     const int t0 = uniform(pc.t0), t1 = uniform(pc.t1), tiles = uniform(pc.tiles), slot = uniform(pc.slot);
     const int rows = nq * a.group;
-    const int first_new = len - nq;                           // may be negative
+    const int first_new = len - nq;                              // may be negative
     const int seen_by_all = a.tree ? first_new : first_new + 1;  // tokens before this need no mask
     const int tail0 = (seen_by_all < 0 ? 0 : seen_by_all) / TILE;  // the first tile that needs a mask
     const int *table = a.table + (int64_t)b * a.table_stride;
-    const int row0 = rb * T::ROWS + wave * 32 * RB;
 
-    u32x4 q[RB][D / 16];
-    int node[RB];
+    const int row = rb * T::ROWS + wave * 32 + n32;
+    const bool in = row < rows;
+    const int node = in ? row / a.group : 0;
+    u32x4 q[D / 16];
+    {
+      const unsigned short *x = a.q + (int64_t)(q0 + node) * a.q_token +
+                                (int64_t)(head * a.group + (in ? row - node * a.group : 0)) * a.q_head + 8 * h;
 #pragma unroll
-    for (int n = 0; n < RB; ++n) {
-      const int row = row0 + 32 * n + n32;
-      const bool in = row < rows;
-      node[n] = in ? row / a.group : 0;
-      const unsigned short *x = a.q + (int64_t)(q0 + node[n]) * a.q_token +
-                                (int64_t)(head * a.group + (in ? row - node[n] * a.group : 0)) * a.q_head + 8 * h;
-#pragma unroll
-      for (int i = 0; i < D / 16; ++i) q[n][i] = in ? *(const u32x4 *)(x + 16 * i) : u32x4{0u, 0u, 0u, 0u};
+      for (int i = 0; i < D / 16; ++i) q[i] = in ? *(const u32x4 *)(x + 16 * i) : u32x4{0u, 0u, 0u, 0u};
     }
 
-    f32x16 o[RB][D / 32];
-    float m[RB], l[RB];
+    f32x16 o[D / 32];
+    float m = -__builtin_inff(), l = 0.0f;
 #pragma unroll
-    for (int n = 0; n < RB; ++n) {
-      m[n] = -__builtin_inff();
-      l[n] = 0.0f;
-#pragma unroll
-      for (int i = 0; i < D / 32; ++i)
-#pragma unroll
-        for (int r = 0; r < 16; ++r) o[n][i][r] = 0.0f;
-    }
+    for (int i = 0; i < D / 32; ++i) o[i] = f32x16{};
 
     // codes on their way: a thread has one token of a tile, and of its key and its value (index 0 and 1 below) every
     // SHARE-th unit of 16 dimensions
@@ -180,6 +181,7 @@ __global__ __launch_bounds__(64 * WAVES, D <= 128 ? 2 : 1) void k_attention_tile
     };
     auto needs_clean = [&](int t) { return t >= tail0 || __builtin_amdgcn_ballot_w64(outside) != 0; };
 
+    __syncthreads();  // the flags of the piece before have been read
     if (threadIdx.x < 2) flags[threadIdx.x] = 0;
     __syncthreads();
     if (len > 0) {
@@ -204,7 +206,7 @@ __global__ __launch_bounds__(64 * WAVES, D <= 128 ? 2 : 1) void k_attention_tile
       auto read_k = [&](int g) {
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-          kf[g & 1][i] = *(const __attribute__((address_space(3))) u32x4 *)(kb + (i & 1) * 32 * T::KS + 64 * g + 32 * (i / 2));
+          kf[g & 1][i] = *(const lds_u32x4 *)(kb + (i & 1) * 32 * T::KS + 64 * g + 32 * (i / 2));
       };
       auto read_values = [&](int g) {
 #pragma unroll
@@ -213,7 +215,7 @@ __global__ __launch_bounds__(64 * WAVES, D <= 128 ? 2 : 1) void k_attention_tile
           vf[g & 1][i] = read_v(vb + 16 * k * T::VS + 64 * d, 8 * T::VS);
         }
       };
-      f32x16 s[RB][2];
+      f32x16 s[2];
       read_k(0);
       __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
@@ -227,13 +229,11 @@ __global__ __launch_bounds__(64 * WAVES, D <= 128 ? 2 : 1) void k_attention_tile
           for (int k = D / 32; k < 2 * T::UNITS; ++k) store(t + 1, k % 2, k / 2);
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-#pragma unroll
-          for (int n = 0; n < RB; ++n)
-            s[n][i & 1] = mma32(kf[g & 1][i], q[n][2 * g + i / 2], g == 0 && i < 2 ? f32x16{} : s[n][i & 1]);
+            s[i & 1] = mma32(kf[g & 1][i], q[2 * g + i / 2], g == 0 && i < 2 ? f32x16{} : s[i & 1]);
         order<SCHED_LDS_READ, 4>();
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          order<SCHED_MFMA, RB>();
+          order<SCHED_MFMA, 1>();
           order<SCHED_VALU, 5>();
         }
         __builtin_amdgcn_sched_barrier(0);
@@ -242,9 +242,7 @@ __global__ __launch_bounds__(64 * WAVES, D <= 128 ? 2 : 1) void k_attention_tile
       fetch(t + 2);  // not under a condition: its registers would be copied, which waits for the loads
       look_up(t + 3);
 
-      const bool masked = t >= tail0 || uniform(outside_seen);
-      unsigned vis[RB][2];
-      if (masked) {
+      if (t >= tail0 || uniform(outside_seen)) {
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
           const int tok = t * TILE + 32 * u;
@@ -254,48 +252,38 @@ __global__ __launch_bounds__(64 * WAVES, D <= 128 ? 2 : 1) void k_attention_tile
             if (tok < len && (unsigned)table[tok >> cv.page_log2] >= (uint64_t)cv.pages) in &= 0xFFFF0000u;
             if (tok + 16 < len && (unsigned)table[(tok + 16) >> cv.page_log2] >= (uint64_t)cv.pages) in &= 0xFFFFu;
           }
+          const unsigned vis = (seen_bits<32>(a, q0 + node, node, tok - first_new) & in) >> (4 * h);
 #pragma unroll
-          for (int n = 0; n < RB; ++n) {
-            vis[n][u] = (seen_bits<32>(a, q0 + node[n], node[n], tok - first_new) & in) >> (4 * h);
-#pragma unroll
-            for (int r = 0; r < 16; ++r)
-              s[n][u][r] = (vis[n][u] >> (8 * (r / 4) + r % 4)) & 1u ? s[n][u][r] : -__builtin_inff();
-          }
+          for (int r = 0; r < 16; ++r) s[u][r] = (vis >> (8 * (r / 4) + r % 4)) & 1u ? s[u][r] : -__builtin_inff();
         }
       }
 
-      float base[RB];
+      float top = s[0][0];
 #pragma unroll
-      for (int n = 0; n < RB; ++n) {
-        float top = s[n][0][0];
+      for (int k = 1; k < 32; ++k) top = fmaxf(top, s[k / 16][k % 16]);
+      top = max_halves(top * to_log2);
+      if (__builtin_amdgcn_ballot_w64(top > m + LAG)) {
+        const float big = fmaxf(m, top);
+        const float f = big == -__builtin_inff() ? 1.0f : __builtin_amdgcn_exp2f(m - big);
+        m = big;
+        l *= f;
 #pragma unroll
-        for (int k = 1; k < 32; ++k) top = fmaxf(top, s[n][k / 16][k % 16]);
-        top = max_halves(top * to_log2);
-        if (__builtin_amdgcn_ballot_w64(top > m[n] + LAG)) {
-          const float big = fmaxf(m[n], top);
-          const float f = big == -__builtin_inff() ? 1.0f : __builtin_amdgcn_exp2f(m[n] - big);
-          m[n] = big;
-          l[n] *= f;
-#pragma unroll
-          for (int i = 0; i < D / 32; ++i) rescale<ACC>(o[n][i], f);
-        }
-        base[n] = m[n] == -__builtin_inff() ? 0.0f : m[n];
+        for (int i = 0; i < D / 32; ++i) rescale<ACC>(o[i], f);
       }
+      const float base = m == -__builtin_inff() ? 0.0f : m;
 
       // weights: registers 8 k .. of the scores are the operand for the tokens 16 k ..; those of the next 16 tokens
       // are computed under the products of these
-      u32x4 p[RB][4];
+      u32x4 p[4];
       auto weigh = [&](int k, int from, int to) {
 #pragma unroll
-        for (int n = 0; n < RB; ++n)
-#pragma unroll
-          for (int i = from; i < to; ++i) {
-            const int r = 8 * (k & 1) + 2 * i;
-            const float w0 = __builtin_amdgcn_exp2f(__builtin_fmaf(s[n][k / 2][r], to_log2, -base[n]));
-            const float w1 = __builtin_amdgcn_exp2f(__builtin_fmaf(s[n][k / 2][r + 1], to_log2, -base[n]));
-            p[n][k][i] = bf16x2_rne(w0, w1);
-            l[n] = add_pair(p[n][k][i], l[n]);
-          }
+        for (int i = from; i < to; ++i) {
+          const int r = 8 * (k & 1) + 2 * i;
+          const float w0 = __builtin_amdgcn_exp2f(__builtin_fmaf(s[k / 2][r], to_log2, -base));
+          const float w1 = __builtin_amdgcn_exp2f(__builtin_fmaf(s[k / 2][r + 1], to_log2, -base));
+          p[k][i] = bf16x2_rne(w0, w1);
+          l = add_pair(p[k][i], l);
+        }
       };
       weigh(0, 0, 4);
       __builtin_amdgcn_sched_barrier(0);
@@ -305,29 +293,24 @@ __global__ __launch_bounds__(64 * WAVES, D <= 128 ? 2 : 1) void k_attention_tile
         if (g + 1 < D / 8 / VG) read_values(g + 1);
         if (k < 3) weigh(k + 1, 4 * part / PARTS, 4 * (part + 1) / PARTS);
 #pragma unroll
-        for (int i = 0; i < VG; ++i)
-#pragma unroll
-          for (int n = 0; n < RB; ++n) o[n][part * VG + i] = mma32(vf[g & 1][i], p[n][k], o[n][part * VG + i]);
+        for (int i = 0; i < VG; ++i) o[part * VG + i] = mma32(vf[g & 1][i], p[k], o[part * VG + i]);
 #pragma unroll
         for (int i = 0; i < VG; ++i) {
           order<SCHED_LDS_READ, 2>();
-          order<SCHED_MFMA, RB>();
-          order<SCHED_VALU, (24 * RB / PARTS + VG - 1) / VG>();
+          order<SCHED_MFMA, 1>();
+          order<SCHED_VALU, (24 / PARTS + VG - 1) / VG>();
         }
         __builtin_amdgcn_sched_barrier(0);
       }
       __syncthreads();
     }
 
-#pragma unroll
-    for (int n = 0; n < RB; ++n) {
-      const int row = row0 + 32 * n + n32;
-      l[n] = sum_halves(l[n]);
-      if (row >= rows) continue;
+    l = sum_halves(l);
+    if (in) {
       if (flags[1]) {
         const int from = tail0 * TILE > t0 * TILE ? tail0 * TILE : t0 * TILE;
         const int to = t1 * TILE < len ? t1 * TILE : len;
-        seen_tokens(a, table, head, q0 + node[n], node[n], first_new, from, to, [&](int64_t ph, int r) {
+        seen_tokens(a, table, head, q0 + node, node, first_new, from, to, [&](int64_t ph, int r) {
 #pragma unroll
           for (int i = 0; i < D / 32; ++i) {
             const unsigned sb = cv.scales[1][((ph * (D / 32) + i) << cv.page_log2) + r];
@@ -339,56 +322,57 @@ __global__ __launch_bounds__(64 * WAVES, D <= 128 ? 2 : 1) void k_attention_tile
               widen<FMT, 4>(w, &code, sb);
 #pragma unroll
               for (int e = 0; e < 4; ++e)
-                if ((not_finite(w[e / 2]) >> (16 * (e & 1))) & 1u) o[n][i][4 * c + e] = __uint_as_float(F32_NAN);
+                if ((not_finite(w[e / 2]) >> (16 * (e & 1))) & 1u) o[i][4 * c + e] = __uint_as_float(F32_NAN);
             }
           }
         });
       }
       if (t1 - t0 == tiles) {
-        const int64_t at = (int64_t)(q0 + node[n]) * cv.heads * a.group + head * a.group + (row - node[n] * a.group);
-        const float inv = reciprocal(l[n]);
+        const int64_t at = (int64_t)(q0 + node) * cv.heads * a.group + head * a.group + (row - node * a.group);
+        const float inv = reciprocal(l);
         unsigned short *d = a.out + at * D + 4 * h;
 #pragma unroll
         for (int i = 0; i < D / 32; ++i)
 #pragma unroll
           for (int r = 0; r < 4; ++r)
-            *(u32x2 *)(d + 32 * i + 8 * r) = u32x2{bf16x2_rne(o[n][i][4 * r] * inv, o[n][i][4 * r + 1] * inv),
-                                                   bf16x2_rne(o[n][i][4 * r + 2] * inv, o[n][i][4 * r + 3] * inv)};
+            *(u32x2 *)(d + 32 * i + 8 * r) = u32x2{bf16x2_rne(o[i][4 * r] * inv, o[i][4 * r + 1] * inv),
+                                                   bf16x2_rne(o[i][4 * r + 2] * inv, o[i][4 * r + 3] * inv)};
       } else {
         const int64_t part = 2 * (int64_t)blockIdx.x + slot;
-        const int r0 = wave * 32 * RB + 32 * n + n32;  // of the block
+        const int r0 = wave * 32 + n32;  // of the block
         float *d = part_sums(a, dv, part, D) + (int64_t)r0 * D + 4 * h;
 #pragma unroll
         for (int i = 0; i < D / 32; ++i)
 #pragma unroll
           for (int r = 0; r < 4; ++r)
             *(f32x4 *)(d + 32 * i + 8 * r) =
-                f32x4{o[n][i][4 * r], o[n][i][4 * r + 1], o[n][i][4 * r + 2], o[n][i][4 * r + 3]};
+                f32x4{o[i][4 * r], o[i][4 * r + 1], o[i][4 * r + 2], o[i][4 * r + 3]};
         if (h == 0) {
           float *ml = part_stats(a, dv, part, D) + 2 * r0;
-          ml[0] = m[n];
-          ml[1] = l[n];
+          ml[0] = m;
+          ml[1] = l;
         }
       }
     }
   }
 }
 
-template <int FMT, int D, int RB, int WAVES>
+template <int FMT, int D, int WAVES>
 static hipError_t start(const AttentionArgs &a, const Division &d, hipStream_t stream) {
-  using T = Tiled<FMT, D, RB, WAVES>;
+  using T = Tiled<FMT, D, WAVES>;
   const int64_t grid = d.workers ? d.workers : (int64_t)a.batch * a.cache.heads * d.blocks;
   static std::atomic<uint64_t> done{0};
-  const hipError_t e = allow_lds((const void *)k_attention_tiles<FMT, D, RB, WAVES>, T::LDS, done);
+  const hipError_t e = allow_lds((const void *)k_attention_tiles<FMT, D, WAVES>, T::LDS, done);
   if (e != hipSuccess) return e;
-  k_attention_tiles<FMT, D, RB, WAVES><<<(unsigned)grid, T::THREADS, T::LDS, stream>>>(a, d);
+  k_attention_tiles<FMT, D, WAVES><<<(unsigned)grid, T::THREADS, T::LDS, stream>>>(a, d);
   return hipGetLastError();
 }
 
 template <int FMT, int D>
 static hipError_t by_rows(const AttentionArgs &a, const Division &d, hipStream_t stream) {
-  if (d.rows == 128) return start<FMT, D, 1, 4>(a, d, stream);
-  return start<FMT, D, 1, 8>(a, d, stream);
+  if (d.rows == 128) return start<FMT, D, 4>(a, d, stream);
+  if constexpr (D <= 128) return start<FMT, D, 8>(a, d, stream);
+  return hipErrorInvalidValue;
 }
 
 hipError_t launch_attention_tiles(const AttentionArgs &a, const Division &d, hipStream_t stream) {

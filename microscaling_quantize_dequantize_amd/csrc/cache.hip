@@ -15,6 +15,11 @@
 // quantise kernels.  Keys are rotated in fp64 and rounded to bf16 before the
 // scale is taken: the bf16 rounding and the element rounding after it have
 // borders, and a rotation in fp32 would put some values on their wrong side.
+//
+// Bound: HBM for reading (16384 tokens of 8 heads of 128 out of MXFP4 17 us, 71005
+// of 5 heads of 96 out of MXFP8 33 us: 5.0 and 6.2 TB/s on MI355X).  Writing the
+// former takes 25 us, 3.4 TB/s (15 us of it without the rotation): the conversions
+// to fp64 and back and the angles' reads from LDS are what the rest goes to.
 #include "launch.h"
 #include "rotary.h"
 

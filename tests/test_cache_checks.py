@@ -117,6 +117,7 @@ def test_attention_refusals(b):
     assert attend(total=1 << 31) == ESHAPE
     assert attend(max_q=-1) == ESHAPE
     assert attend(max_kv=(1 << 31) - 1) == ESHAPE
+    assert attend(batch=1 << 24, total=1 << 20, max_q=1 << 20) == ESHAPE  # more rows than a grid has workgroups for
     assert attend(stride=3) == ESHAPE
     assert attend(pages=(1 << 31) // 16) == ESHAPE
     assert attend(words=-1) == ESHAPE

@@ -161,6 +161,19 @@ def test_nan_reaches_only_rows_that_see_it(mx, fmt, tree):
     assert bool(torch.isnan(out).any()) and not bool(torch.isnan(out[:13]).all())
 
 
+@pytest.mark.parametrize("group,nq", [(2, 4), (4, 20), (8, 20)])
+def test_nan_in_some_of_many_sequences(mx, group, nq):
+    """Items that need their NaN next to items that do not, several to a workgroup and divided over several."""
+    kv = [700 + 13 * b for b in range(12)]
+    c = Case(mx, 1, 2, group, 64, 16, kv, [nq] * 12, seed=31).random_tree()
+    for b in range(0, 12, 3):
+        for tok in (kv[b] - 2, kv[b] - nq):
+            c.cache.v_codes[int(c.table[b, tok // 16]), 1, tok % 16, 7] = 0x7F
+    out = c.run(mx)
+    c.check(out)
+    assert bool(torch.isnan(out).any())
+
+
 @pytest.mark.parametrize("bad", [-1, 1 << 30, -(1 << 31)])
 def test_pages_outside_the_cache_are_not_seen(mx, bad):
     c = Case(mx, 1, 2, 4, 64, 32, [700, 64], [3, 1], seed=2)
