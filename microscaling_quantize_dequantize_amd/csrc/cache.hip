@@ -18,7 +18,7 @@
 //
 // Bound: HBM for reading (16384 tokens of 8 heads of 128 out of MXFP4 17 us, 71005
 // of 5 heads of 96 out of MXFP8 33 us: 5.0 and 6.2 TB/s on MI355X).  Writing the
-// former takes 25 us, 3.4 TB/s (15 us of it without the rotation): the conversions
+// former takes 25-27 us, 3.3 TB/s, and 17 without the rotation: the conversions
 // to fp64 and back and the angles' reads from LDS are what the rest goes to.
 #include "launch.h"
 #include "rotary.h"
