@@ -420,13 +420,16 @@ def mx_rope(x: torch.Tensor, positions: torch.Tensor, inv_freq: torch.Tensor, la
     (2p with 2p + 1); scale multiplies the rotated dimensions.  inverse: the transposed rotation, which takes the
     gradient of the output to that of x.  dst may be x itself."""
     ps, st, sh = _heads(x, "x", (torch.bfloat16, torch.float32))
-    if dst is None:
+    tokens, heads, dim = x.shape
+    if dst is None:  # what is allocated here needs no check
         dst = _like(x)
-    pd, dt, dh = _heads(dst, "dst", (x.dtype,), x.shape)
-    pp, pf, rot = _rotary(positions, inv_freq, x.shape[0])
+        pd, dt, dh = dst.data_ptr(), heads * dim, dim
+    else:
+        pd, dt, dh = _heads(dst, "dst", (x.dtype,), x.shape)
+    pp, pf, rot = _rotary(positions, inv_freq, tokens)
     _stream()
-    _call(_lib.mx_rope(ps, st, sh, _DTYPE[x.dtype], *x.shape, pp, pf, rot, layout, scale, 1 if inverse else 0, pd, dt,
-                       dh))
+    _call(_lib.mx_rope(ps, st, sh, _DTYPE[x.dtype], tokens, heads, dim, pp, pf, rot, layout, scale,
+                       1 if inverse else 0, pd, dt, dh))
     return dst
 
 
@@ -464,6 +467,7 @@ class MXCache:
         self.device = k_codes.device
         self._struct = _CacheStruct(fmt, heads, page, dim, pages, *ptrs)
         self._ref = ctypes.addressof(self._struct)
+        self._bf16 = k_codes.new_empty(0, dtype=torch.bfloat16)  # new_empty of this is quicker than torch.empty
 
     @classmethod
     def allocate(cls, fmt: int, pages: int, heads: int, page: int, dim: int, device="cuda") -> "MXCache":
@@ -493,7 +497,7 @@ def mx_cache_write(cache: MXCache, k: torch.Tensor, v: torch.Tensor, slots: torc
     pc = _cache(cache)
     pk, kt, kh = _heads(k, "k", (torch.bfloat16,))
     shape = (k.shape[0], cache.heads, cache.dim)
-    if tuple(k.shape) != shape:
+    if k.shape != shape:
         raise ValueError(f"k must have shape {shape}, got {tuple(k.shape)}")
     pv, vt, vh = _heads(v, "v", (torch.bfloat16,), shape)
     ps = _vector(slots, "slots", torch.int64, shape[0])
@@ -510,13 +514,16 @@ def mx_cache_read(cache: MXCache, slots: torch.Tensor, k: torch.Tensor | None = 
     if not isinstance(slots, torch.Tensor) or slots.dim() != 1:
         raise ValueError("slots must be a one-dimensional int64 tensor")
     shape = (slots.shape[0], cache.heads, cache.dim)
+    for t, name in ((k, "k"), (v, "v")):
+        if t is not None:
+            _want(t, name, torch.bfloat16, shape)
+            _dev(t, name)
+    ps = _vector(slots, "slots", torch.int64, shape[0])
     if k is None:
-        k = torch.empty(shape, dtype=torch.bfloat16, device=slots.device)
+        k = cache._bf16.new_empty(shape)
     if v is None:
-        v = torch.empty(shape, dtype=torch.bfloat16, device=slots.device)
-    _want(k, "k", torch.bfloat16, shape)
-    _want(v, "v", torch.bfloat16, shape)
-    ps, pk, pv = _vector(slots, "slots", torch.int64, shape[0]), _dev(k, "k"), _dev(v, "v")
+        v = cache._bf16.new_empty(shape)
+    pk, pv = k.data_ptr(), v.data_ptr()
     _stream()
     _call(_lib.mx_cache_read(pc, ps, shape[0], pk, pv))
     return k, v
@@ -562,8 +569,10 @@ def mx_cache_attention(cache: MXCache, q: torch.Tensor, q_starts: torch.Tensor, 
         pt = _dev(tree, "tree")
     if out is None:
         out = _like(q)
-    _want(out, "out", torch.bfloat16, (total, heads, dim))
-    po = _dev(out, "out")
+    else:
+        _want(out, "out", torch.bfloat16, (total, heads, dim))
+        _dev(out, "out")
+    po = out.data_ptr()
     need = _lib.mx_cache_attention_workspace(pc, heads, batch, total, max_q, max_kv)
     if need < 0:
         raise MXError(need)
