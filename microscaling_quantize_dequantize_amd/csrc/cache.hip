@@ -16,10 +16,12 @@
 // scale is taken: the bf16 rounding and the element rounding after it have
 // borders, and a rotation in fp32 would put some values on their wrong side.
 //
-// Bound: HBM for reading (16384 tokens of 8 heads of 128 out of MXFP4 17 us, 71005
+// Bound: HBM for reading (16384 tokens of 8 heads of 128 out of MXFP4 17 us, 71004
 // of 5 heads of 96 out of MXFP8 33 us: 5.0 and 6.2 TB/s on MI355X).  Writing the
-// former takes 25-27 us, 3.3 TB/s, and 17 without the rotation: the conversions
-// to fp64 and back and the angles' reads from LDS are what the rest goes to.
+// former takes 26-27 us, 3.2 TB/s, and 17 without the rotation: the rest goes to
+// forming the angles, in fp64 and before a row is loaded, and to the rotation.
+// Loading the first rows before the angles (29 us), tiles of 16 tokens (27) and
+// both pieces of a pair in one thread (26-27) were no faster.  64 tokens take 4 us.
 #include "launch.h"
 #include "rotary.h"
 
@@ -150,7 +152,8 @@ __global__ __launch_bounds__(WRITE_THREADS) void k_cache_write(WriteArgs a) {
 #pragma unroll
     for (int k = 0; k < WRITE_ROWS; ++k) {
       const int row = row0 + k * pass;
-      const int h = (row < rows ? row : rows - 1) / nt, t = (row < rows ? row : rows - 1) - h * nt;
+      if (row >= rows) break;
+      const int h = row / nt, t = row - h * nt;
       u32x4 v = w[k];
       if (half) v = rotate8<LAYOUT, ALIGNED>(x[k], v, q[k], d, half, tc + t * half, ts + t * half);
       unsigned m = piece_amax_bf16(v);
@@ -158,7 +161,7 @@ __global__ __launch_bounds__(WRITE_THREADS) void k_cache_write(WriteArgs a) {
       m = umax(m, dpp<DPP_QUAD_2301>(m));
       const unsigned sb = scale_byte<FMT>(m << 16);
       const float sc = scale_operand(sb);
-      if (row >= rows || slot[k] < 0 || slot[k] >= cv.pages << cv.page_log2) continue;  // padding: nothing is written
+      if (slot[k] < 0 || slot[k] >= cv.pages << cv.page_log2) continue;  // padding: nothing is written
       const int64_t ph = (slot[k] >> cv.page_log2) * cv.heads + h0 + h;
       const int r = (int)(slot[k] & ((1 << cv.page_log2) - 1));
       if (FMT == 0) {
