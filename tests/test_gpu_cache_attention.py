@@ -84,6 +84,14 @@ def test_heads_and_rows(mx, fmt, dim, group, nq):
     c.check(c.run(mx))
 
 
+@pytest.mark.parametrize("fmt,dim", [(0, 64), (1, 128), (1, 192)])
+@pytest.mark.parametrize("group", [16, 17, 71])
+def test_one_key_value_head_for_many(mx, fmt, dim, group):
+    """A single token whose query heads alone are more rows than a block of the few-rows kernel."""
+    c = Case(mx, fmt, 1, group, dim, 32, [700, 33], [1, 1], seed=group)
+    c.check(c.run(mx))
+
+
 @pytest.mark.parametrize("page", [16, 32, 64, 256])
 @pytest.mark.parametrize("kv", [1, 2, 15, 16, 17, 63, 64, 65, 255, 256, 257, 1000])
 def test_lengths_and_pages(mx, page, kv):
