@@ -96,10 +96,11 @@ __device__ __forceinline__ void accumulate(f32x4 (*acc)[W], int base, unsigned (
   }
 }
 
-// In a tile that needs a mask: codes of the tokens from `valid` on and of values that are not finite become zero
-// (`odd` tells of the latter).
+// In a tile that needs a mask: codes of the tokens from `valid` on become zero, and where rows differ in what they see
+// (`differ`, all ones or zero) so do the codes of values that are not finite (`odd` tells of these).
 template <int FMT, int CNT, int CW>
-__device__ __forceinline__ void clear_codes(unsigned (*codes)[CW], unsigned *scales, int valid, unsigned &odd) {
+__device__ __forceinline__ void clear_codes(unsigned (*codes)[CW], unsigned *scales, int valid, unsigned differ,
+                                            unsigned &odd) {
   constexpr int BITS = FMT == 0 ? 4 : 8;
   constexpr unsigned ONE = (1u << BITS) - 1u;
 #pragma unroll
@@ -112,13 +113,13 @@ __device__ __forceinline__ void clear_codes(unsigned (*codes)[CW], unsigned *sca
     unsigned clear[CW] = {};
 #pragma unroll
     for (int i = 0; i < CNT / 2; ++i) {
-      const unsigned bad = not_finite(w[i]) & in;
+      const unsigned bad = not_finite(w[i]) & in & differ;
       odd |= bad;
       clear[2 * i * BITS / 32] |= ((bad & 1u) * ONE | (bad >> 16) * (ONE << BITS)) << (2 * i * BITS % 32);
     }
 #pragma unroll
     for (int i = 0; i < CW; ++i) codes[tok][i] &= in & ~clear[i];
-    if (sb == 255u || !in) scales[tok / 4] &= ~(0xFFu << at);
+    if ((sb == 255u && differ) || !in) scales[tok / 4] &= ~(0xFFu << at);
     __builtin_amdgcn_sched_barrier(0);
   }
 }
@@ -183,7 +184,7 @@ __global__ __launch_bounds__(64 * ATT_WAVES, rows_held(D, NT)) void k_attention_
   unsigned kc[4][A::KW], ks[A::NB];
   unsigned vc0[16][A::VW0], vc1[16][A::VW1 > 0 ? A::VW1 : 1];
   unsigned vs0[4], vs1[4];
-  unsigned odd = 0u;  // values that are not finite were met in a masked tile
+  unsigned odd = 0u;  // values that are not finite were taken out of a tile
   bool bad = false;  // the page of the lane's 16 tokens is not in the cache
 
   // a page, or page 0 in place of one that is not in the cache (its tokens are masked)
@@ -228,6 +229,8 @@ __global__ __launch_bounds__(64 * ATT_WAVES, rows_held(D, NT)) void k_attention_
   };
 
   const float to_log2 = a.scale * 1.4426950408889634f;
+  // rows may differ in what they see of the tile, or it ends behind the tokens
+  auto differs = [&](int base) { return base + TILE > seen_by_all || base + TILE > hi; };
   const int first = lo + TILE * wave;
   if (first < hi) {
     load_k(first);
@@ -261,7 +264,7 @@ __global__ __launch_bounds__(64 * ATT_WAVES, rows_held(D, NT)) void k_attention_
 
     // the tokens of this lane that each row sees: bit 4 r + t
     const int tok0 = base + 16 * g;
-    const bool masked = __builtin_amdgcn_ballot_w64(bad || base + TILE > seen_by_all || base + TILE > hi) != 0;
+    const bool masked = __builtin_amdgcn_ballot_w64(bad || differs(base)) != 0;
     int valid = 16;
     if (masked) {
       valid = bad ? 0 : hi - tok0;
@@ -312,8 +315,9 @@ __global__ __launch_bounds__(64 * ATT_WAVES, rows_held(D, NT)) void k_attention_
     }
 
     if (masked) {
-      clear_codes<FMT, A::C0>(vc0, vs0, valid, odd);
-      if constexpr (A::C1 > 0) clear_codes<FMT, A::C1>(vc1, vs1, valid, odd);
+      const unsigned differ = differs(base) ? 0xFFFFFFFFu : 0u;
+      clear_codes<FMT, A::C0>(vc0, vs0, valid, differ, odd);
+      if constexpr (A::C1 > 0) clear_codes<FMT, A::C1>(vc1, vs1, valid, differ, odd);
     }
     accumulate<FMT, A::C0, NT>(st.o, 0, vc0, vs0, p);
     if constexpr (A::C1 > 0) accumulate<FMT, A::C1, NT>(st.o, A::C0, vc1, vs1, p);
@@ -321,9 +325,9 @@ __global__ __launch_bounds__(64 * ATT_WAVES, rows_held(D, NT)) void k_attention_
   }
 
   if (__builtin_amdgcn_ballot_w64(odd != 0u)) {
-    // of this wave's tiles, the ones that needed a mask
+    // of this wave's tiles, the ones they were taken out of
     for (int base = first; base < hi; base += TILE * ATT_WAVES) {
-      if (base + TILE <= seen_by_all && base + TILE <= hi) continue;
+      if (!differs(base)) continue;
       const int to = base + TILE < hi ? base + TILE : hi;
 #pragma unroll
       for (int n = 0; n < NT; ++n)
