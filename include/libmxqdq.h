@@ -334,7 +334,10 @@ MX_API int mx_cache_read(const mx_cache *cache, const int64_t *slots,
  *                 (64 * tree_words >= max_q, MX_EARG).
  * A query that sees nothing gives zeros; what it does not see has no part in
  * its result, NaN included.  Tokens of a page that is not in the cache count
- * as not seen.
+ * as not seen.  A value above the range of bf16 (a large code with a scale of
+ * 2^120 and more, which mx_cache_write does not produce) is an infinity of
+ * its sign, in every row that sees it with a weight that is not too small for
+ * fp32.
  *   q          [total_q x q_heads x dim] bf16, 16-byte aligned, strides (in
  *              elements) multiples of 8; out the same, contiguous.
  *   q_starts   [batch + 1] int32, ascending from 0; kv_lens [batch] int32;

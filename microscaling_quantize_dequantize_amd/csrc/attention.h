@@ -278,7 +278,8 @@ struct Pieces {
 };
 
 // Values that are not finite, of tokens that some rows see and others do not, are left out of the products; afterwards
-// their dimensions are made NaN in the rows that see them.  For a row (query `query`, place `node` among the new
+// they are added to their dimensions' sums in the rows that see them (a weight is above zero, so NaN and infinities of
+// either sign come out as if they had been in the products).  For a row (query `query`, place `node` among the new
 // tokens) and the tokens from .. to of its sequence: not_finite(codes, scales, row of the head's page) is asked for
 // every token that the row sees.
 template <typename Ask>
@@ -297,6 +298,12 @@ __device__ __forceinline__ void seen_tokens(const AttentionArgs &a, const int *t
 // sign's place).
 __device__ __forceinline__ unsigned not_finite(unsigned pair) {
   return (((pair & 0x7F807F80u) + 0x00800080u) >> 15) & 0x00010001u;
+}
+
+// The low or high half of a packed pair as fp32 if it is not finite, zero otherwise.
+__device__ __forceinline__ float not_finite_or_zero(unsigned pair, int high) {
+  const unsigned v = high ? pair & 0xFFFF0000u : pair << 16;
+  return (v & 0x7F800000u) == 0x7F800000u ? __uint_as_float(v) : 0.0f;
 }
 
 // Takes values that are not finite out of N packed pairs; non-zero if there were any.

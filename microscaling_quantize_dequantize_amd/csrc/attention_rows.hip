@@ -124,7 +124,7 @@ __device__ __forceinline__ void clear_codes(unsigned (*codes)[CW], unsigned *sca
   }
 }
 
-// Makes the dimensions of one run NaN in which a token's value is not finite.
+// Adds a token's values that are not finite to the sums of one run of dimensions.
 template <int FMT, int CNT, int W>
 __device__ __forceinline__ void spoil(f32x4 (&acc)[W], int base, const uint8_t *codes, const uint8_t *scales, int first,
                                       int page_log2) {
@@ -135,8 +135,7 @@ __device__ __forceinline__ void spoil(f32x4 (&acc)[W], int base, const uint8_t *
     load_bytes<FMT == 0 ? CNT / 2 : CNT>(code, codes + (FMT == 0 ? d / 2 : d));
     widen<FMT, CNT>(w, code, scales[(d / 32) << page_log2]);
 #pragma unroll
-    for (int i = 0; i < CNT; ++i)
-      if ((not_finite(w[i / 2]) >> (16 * (i & 1))) & 1u) acc[base + i][r] = __uint_as_float(F32_NAN);
+    for (int i = 0; i < CNT; ++i) acc[base + i][r] += not_finite_or_zero(w[i / 2], i & 1);
   }
 }
 

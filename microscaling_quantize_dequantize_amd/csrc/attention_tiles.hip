@@ -321,8 +321,7 @@ __global__ __launch_bounds__(64 * WAVES, D <= 128 ? 2 : 1) void k_attention_tile
                                                  (32 * i + 8 * c + 4 * h) * T::CODE / 16);
               widen<FMT, 4>(w, &code, sb);
 #pragma unroll
-              for (int e = 0; e < 4; ++e)
-                if ((not_finite(w[e / 2]) >> (16 * (e & 1))) & 1u) o[i][4 * c + e] = __uint_as_float(F32_NAN);
+              for (int e = 0; e < 4; ++e) o[i][4 * c + e] += not_finite_or_zero(w[e / 2], e & 1);
             }
           }
         });
