@@ -22,8 +22,11 @@ struct Division {
   int blocks, tiles;             // host's bounds on an item's blocks and tiles
 };
 
+// What is computed of a sequence: queries q0 .. q0 + nq, tokens 0 .. len.  first_new is the place of its first new token,
+// from the lengths as they are: bounds below them leave queries and tokens out, and move no mask.  It is negative where
+// there are more queries than tokens.
 struct Sequence {
-  int q0, nq, len;
+  int q0, nq, len, first_new;
 };
 
 // Values that are the same in every lane of a wave, told to the compiler: they stay in scalar registers, and branches
@@ -33,7 +36,7 @@ __device__ __forceinline__ int64_t uniform(int64_t v) {
   return (int64_t)(((uint64_t)(unsigned)uniform((int)(v >> 32)) << 32) | (unsigned)uniform((int)v));
 }
 __device__ __forceinline__ Sequence uniform(const Sequence &s) {
-  return Sequence{uniform(s.q0), uniform(s.nq), uniform(s.len)};
+  return Sequence{uniform(s.q0), uniform(s.nq), uniform(s.len), uniform(s.first_new)};
 }
 
 __device__ __forceinline__ Sequence sequence_of(const AttentionArgs &a, int b) {
@@ -41,10 +44,13 @@ __device__ __forceinline__ Sequence sequence_of(const AttentionArgs &a, int b) {
   const int q0 = a.q_starts[b], q1 = a.q_starts[b + 1];
   s.q0 = q0 < 0 ? 0 : q0;
   s.nq = (q1 > a.total_q ? a.total_q : q1) - s.q0;
-  s.nq = s.nq < 0 ? 0 : s.nq > a.max_q ? a.max_q : s.nq;
+  s.nq = s.nq < 0 ? 0 : s.nq;
   const int64_t cap = (int64_t)a.table_pages << a.cache.page_log2;
   int len = a.kv_lens[b];
-  len = len < 0 ? 0 : len > a.max_kv ? a.max_kv : len;
+  len = len < 0 ? 0 : len;
+  s.first_new = len - s.nq;
+  s.nq = s.nq > a.max_q ? a.max_q : s.nq;
+  len = len > a.max_kv ? a.max_kv : len;
   s.len = len > cap ? (int)cap : len;
   return s;
 }
@@ -153,11 +159,11 @@ __device__ __forceinline__ float sum_rows16(float v) {
 template <int N>
 __device__ __forceinline__ unsigned seen_bits(const AttentionArgs &a, int query, int node, int j0) {
   constexpr unsigned ALL = 0xFFFFFFFFu >> (32 - N);
+  if (j0 <= -N) return ALL;
   if (a.tree == nullptr) {
     const int count = node + 1 - j0;
     return count >= N ? ALL : count <= 0 ? 0u : (1u << count) - 1u;
   }
-  if (j0 <= -N) return ALL;
   const int64_t *words = a.tree + (int64_t)query * a.tree_words;
   const int at = j0 < 0 ? 0 : j0, i0 = at / 64, last = a.tree_words - 1;
   uint64_t w0 = words[i0 < last ? i0 : last], w1 = words[i0 < last ? i0 + 1 : last];  // one wait for both

@@ -153,7 +153,7 @@ __global__ __launch_bounds__(64 * ATT_WAVES, rows_held(D, NT)) void k_attention_
     const int t0 = uniform(pc.t0), t1 = uniform(pc.t1), tiles = uniform(pc.tiles), slot = uniform(pc.slot);
   const int rows = nq * a.group;
   const int lo = t0 * TILE, hi = t1 * TILE < len ? t1 * TILE : len;
-  const int first_new = len - nq;                                // may be negative
+  const int first_new = uniform(pc.s.first_new);
   const int seen_by_all = a.tree ? first_new : first_new + 1;       // tokens before this need no mask
   const int *table = a.table + (int64_t)b * a.table_stride;
 

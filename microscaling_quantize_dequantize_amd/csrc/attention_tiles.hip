@@ -95,9 +95,10 @@ __global__ __launch_bounds__(64 * WAVES, D <= 128 ? 2 : 1) void k_attention_tile
     const int head = uniform(pc.head), rb = uniform(pc.block);
     const int t0 = uniform(pc.t0), t1 = uniform(pc.t1), tiles = uniform(pc.tiles), slot = uniform(pc.slot);
     const int rows = nq * a.group;
-    const int first_new = len - nq;                              // may be negative
+    const int first_new = uniform(pc.s.first_new);
     const int seen_by_all = a.tree ? first_new : first_new + 1;  // tokens before this need no mask
-    const int tail0 = (seen_by_all < 0 ? 0 : seen_by_all) / TILE;  // the first tile that needs a mask
+    // the first tile that needs a mask, or ends behind the tokens
+    const int tail0 = (seen_by_all < 0 ? 0 : seen_by_all < len ? seen_by_all : len) / TILE;
     const int *table = a.table + (int64_t)b * a.table_stride;
 
     const int row = rb * T::ROWS + wave * 32 + n32;

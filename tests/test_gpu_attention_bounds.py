@@ -1,0 +1,45 @@
+"""Bounds of attention over the paged MX cache that differ from what the sequences hold: max_q and max_kv below the
+sequences' sizes, queries of no sequence, batches of one long chunk and many single tokens."""
+import pytest
+import torch
+
+from _attentionref import check
+from test_gpu_cache_attention import Case
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def mx():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    from microscaling_quantize_dequantize_amd import binding
+    return binding
+
+
+def attend(mx, c, max_q, max_kv, out=None):
+    return mx.mx_cache_attention(c.cache, c.q, c.q_starts, c.kv_lens, c.table, max_q=max_q, max_kv=max_kv, tree=c.tree,
+                                 out=out)
+
+
+@pytest.mark.parametrize("group,nq", [(1, 10), (2, 12), (8, 40), (4, 90)])
+@pytest.mark.parametrize("tree", [False, True])
+@pytest.mark.parametrize("cut_q,cut_kv", [(True, False), (False, True), (True, True)])
+def test_bounds_below_the_sizes(mx, group, nq, tree, cut_q, cut_kv):
+    """What is beyond max_q and max_kv is left out; the rows that are computed see no token that they should not."""
+    c = Case(mx, 1, 2, group, 64, 16, [50 + nq, nq, 900], [nq, nq, nq // 2], seed=nq)
+    if tree:
+        c.random_tree()
+    max_q = nq // 2 - 1 if cut_q else nq
+    max_kv = 40 + nq // 2 if cut_kv else 900
+    out = attend(mx, c, max_q, max_kv, out=torch.zeros_like(c.q, memory_format=torch.contiguous_format))
+    check(c, out, max_q=max_q, max_kv=max_kv)
+
+
+@pytest.mark.parametrize("group,nq", [(2, 5), (8, 40)])
+def test_tokens_behind_the_table_are_not_seen(mx, group, nq):
+    c = Case(mx, 1, 2, group, 64, 16, [700, 300], [nq, nq], seed=3)
+    c.table = c.table[:, :20].contiguous()
+    out = c.run(mx)
+    c.table = torch.cat((c.table, c.table.new_full((2, 24), -1)), 1)  # the reference takes no part of them
+    check(c, out)
