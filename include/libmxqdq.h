@@ -340,13 +340,14 @@ MX_API int mx_cache_read(const mx_cache *cache, const int64_t *slots,
  * fp32.
  *   q          [total_q x q_heads x dim] bf16, 16-byte aligned, strides (in
  *              elements) multiples of 8; out the same, contiguous.
- *   q_starts   [batch + 1] int32, ascending from 0; kv_lens [batch] int32;
+ *   q_starts   [batch + 1] int32, ascending from 0; queries from q_starts[batch]
+ *              on (padding) give zeros.  kv_lens [batch] int32;
  *              block_table [batch x table_stride] int32, of which the first
  *              table_pages of a row may be read; tree [total_q x tree_words].
  *   max_q, max_kv  at least the most queries and tokens of a sequence.  With
- *              less, a sequence's queries from max_q on are not computed (their
- *              rows are not written), and its tokens from max_kv on count as
- *              not seen; so do tokens behind the pages of table_pages.
+ *              less, a sequence's queries from max_q on are not computed (what
+ *              their rows hold is undefined), and its tokens from max_kv on
+ *              count as not seen; so do tokens behind the pages of table_pages.
  *   workspace  mx_cache_attention_workspace bytes, 16-byte aligned, contents
  *              free; it may be NULL where that is 0.
  * dim is 64, 96, 128, 192 or 256 and scale is positive and finite (MX_EARG);

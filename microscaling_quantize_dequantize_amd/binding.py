@@ -539,8 +539,9 @@ def mx_cache_attention(cache: MXCache, q: torch.Tensor, q_starts: torch.Tensor, 
     [batch]), of which the last are its new ones, one for each query; token t is in page block_table[b, t // page]
     (int32 [batch, pages of the longest], rows contiguous).  A query sees all tokens before the new ones, and of the
     new ones those up to its own, or with tree (int64 [total_q, words]) new token j where bit j % 64 of word j // 64 of
-    its row is set.  A query that sees nothing gives zeros.  max_q, max_kv: at least the most queries and tokens of a
-    sequence (with less, the rows of queries from max_q on are not written and tokens from max_kv on are not seen).
+    its row is set.  A query that sees nothing gives zeros, and so does one of no sequence (from q_starts[batch] on).
+    max_q, max_kv: at least the most queries and tokens of a sequence (with less, the rows of queries from max_q on are
+    undefined and tokens from max_kv on are not seen).
     scale: dim ** -0.5 if not given."""
     pc = _cache(cache)
     pq, qt, qh = _heads(q, "q", (torch.bfloat16,))

@@ -331,9 +331,12 @@ MX_API int mx_cache_attention(const mx_cache *cache, const void *q, int64_t q_to
     return MX_ESHAPE;
   if (!(scale > 0.0f && scale <= 3.402823466e38f)) return MX_EARG;
   if (tree && (max_q < total_q ? max_q : total_q) > 64 * tree_words) return MX_EARG;
-  if (batch == 0 || total_q == 0 || max_q == 0) return MX_OK;
-  if (!q || !q_starts || !kv_lens || !out) return MX_ENULL;
-  if (max_kv > 0 && table_pages > 0 && (!block_table || cache->pages == 0 || empty_cache(cache))) return MX_ENULL;
+  if (total_q == 0) return MX_OK;
+  const bool none = batch == 0 || max_q == 0;  // no sequence has queries: zeros, if there is an output
+  if (none && !out) return MX_OK;
+  if (!out || (!none && (!q || !q_starts || !kv_lens))) return MX_ENULL;
+  if (!none && max_kv > 0 && table_pages > 0 && (!block_table || cache->pages == 0 || empty_cache(cache)))
+    return MX_ENULL;
   if (!aligned(q, 16) || !aligned(out, 16) || q_token_stride % 8 != 0 || q_head_stride % 8 != 0 ||
       !aligned(q_starts, 4) || !aligned(kv_lens, 4) || !aligned(block_table, 4) || !aligned(tree, 8))
     return MX_EALIGN;

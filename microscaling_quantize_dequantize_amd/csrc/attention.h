@@ -55,6 +55,22 @@ __device__ __forceinline__ Sequence sequence_of(const AttentionArgs &a, int b) {
   return s;
 }
 
+// Zeros for the queries from `from` on, written by the last `groups` workgroups (of which `mine` is the place).
+__device__ __forceinline__ void zero_rows(const AttentionArgs &a, int from, int groups, int mine) {
+  const int64_t row = (int64_t)a.cache.heads * a.group * (a.cache.dim / 8), step = (int64_t)groups * blockDim.x;
+  const int64_t first = from * row + (int64_t)mine * blockDim.x + threadIdx.x;
+  for (int64_t i = first; i < a.total_q * row; i += step) ((u32x4 *)a.out)[i] = u32x4{0u, 0u, 0u, 0u};
+}
+
+// Queries of no sequence, from q_starts[batch] on (a batch may be padded at its end), give zeros.  The last 64 workgroups
+// see to it when their runs are done: where there is little work these have none.
+__device__ __forceinline__ void zero_padding(const AttentionArgs &a) {
+  const int groups = gridDim.x < 64 ? gridDim.x : 64, mine = (int)(blockIdx.x - (gridDim.x - groups));
+  if (mine < 0) return;
+  const int end = uniform(a.q_starts[a.batch]);
+  zero_rows(a, end < 0 ? 0 : end, groups, mine);
+}
+
 // Tiles of an item (one at least: rows without tokens get their zeros) and blocks of a head.
 __device__ __forceinline__ int item_tiles(const Sequence &s) { return s.len > 0 ? (s.len + TILE - 1) / TILE : 1; }
 __device__ __forceinline__ int item_blocks(const AttentionArgs &a, const Sequence &s, int rows) {

@@ -101,7 +101,15 @@ static hipError_t join(const AttentionArgs &a, const Division &d, hipStream_t st
   return hipGetLastError();
 }
 
+__global__ __launch_bounds__(256) void k_zero_padding(AttentionArgs a) {
+  zero_rows(a, 0, gridDim.x, blockIdx.x);
+}
+
 hipError_t launch_cache_attention(const AttentionArgs &a, hipStream_t stream) {
+  if (a.batch == 0 || a.max_q == 0) {  // no sequence has queries
+    k_zero_padding<<<4 * device_cu_count(), 256, 0, stream>>>(a);
+    return hipGetLastError();
+  }
   bool tiled;
   const Division d =
       division_of(a.cache.dim, a.cache.heads, a.group, a.batch, a.max_q, a.max_kv, &tiled);

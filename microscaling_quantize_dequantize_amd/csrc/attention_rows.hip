@@ -412,6 +412,7 @@ __global__ __launch_bounds__(64 * ATT_WAVES, rows_held(D, NT)) void k_attention_
     }
   }
   }
+  zero_padding(a);
 }
 
 template <int FMT, int D, int NT>

@@ -355,6 +355,7 @@ __global__ __launch_bounds__(64 * WAVES, D <= 128 ? 2 : 1) void k_attention_tile
       }
     }
   }
+  zero_padding(a);
 }
 
 template <int FMT, int D, int WAVES>

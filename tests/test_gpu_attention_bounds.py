@@ -43,3 +43,26 @@ def test_tokens_behind_the_table_are_not_seen(mx, group, nq):
     out = c.run(mx)
     c.table = torch.cat((c.table, c.table.new_full((2, 24), -1)), 1)  # the reference takes no part of them
     check(c, out)
+
+
+@pytest.mark.parametrize("group,nq,kv", [(1, 1, 30), (4, 1, 9000), (4, 30, 400), (8, 70, 3000)])
+@pytest.mark.parametrize("spare", [1, 57])
+def test_queries_of_no_sequence_give_zeros(mx, group, nq, kv, spare):
+    """A batch padded at its end: rows from q_starts[batch] on are written, and nothing else changes."""
+    c = Case(mx, 1, 2, group, 64, 16, [kv, 17], [nq, 1], seed=spare)
+    want = c.run(mx)
+    c.q = torch.cat((c.q, torch.full((spare, *c.q.shape[1:]), float("nan"), device="cuda").bfloat16()))
+    out = torch.full(c.q.shape, float("nan"), device="cuda").bfloat16()
+    c.run(mx, out=out)
+    assert torch.equal(out[:nq + 1], want)
+    assert not bool(out[nq + 1:].any())
+
+
+@pytest.mark.parametrize("batch", [0, 2])
+def test_only_padding(mx, batch):
+    c = Case(mx, 1, 2, 2, 64, 16, [40, 9], [0, 0], seed=1)
+    q = torch.ones((5, 4, 64), device="cuda").bfloat16()
+    out = torch.full(q.shape, float("nan"), device="cuda").bfloat16()
+    mx.mx_cache_attention(c.cache, q, c.q_starts[:batch + 1], c.kv_lens[:batch], c.table[:batch], max_q=0, max_kv=40,
+                          out=out)
+    assert not bool(out.any())
