@@ -257,7 +257,7 @@ int check_attention(const mx_cache *c, int64_t q_heads, int64_t batch, int64_t t
   if (!fits(batch, 1 << 24) || !fits(total_q, INT32_MAX / q_heads) || !fits(max_q, INT32_MAX / q_heads) ||
       !fits(max_kv, INT32_MAX - 65536))
     return MX_ESHAPE;
-  // grid limits: a workgroup for every four rows of every sequence at its longest
+  // rows of the batch with every sequence at its longest, the bound of the division's numbers
   if ((double)batch * q_heads * (double)(max_q < total_q ? max_q : total_q) > 4294967296.0) return MX_ESHAPE;
   return MX_OK;
 }

@@ -17,9 +17,19 @@ constexpr int TILE = 64;  // tokens of a tile, the unit of the division
 // workspace and are joined by k_join.  Slot 0 is for a piece that continues its item, which only the run's first can;
 // slot 1 for one that begins its item, which then is the run's last.  workers == 0: one workgroup for each item,
 // nothing to join.
+//
+// What k_join goes by: a record for each item that the host's bounds allow, or, where these are more than the workers
+// (one long sequence among many gives every one of them its blocks), a record for each worker, of the divided item that
+// its run ends with.
 struct Division {
   int workers, min_tiles, rows;  // rows: of a block
   int blocks, tiles;             // host's bounds on an item's blocks and tiles
+  int records;                   // of items, or of workers
+  bool by_worker;
+};
+struct Record {
+  int first, last;  // workers that have the item's pieces
+  int b, part;      // the item: sequence, head * blocks + block (of a worker's record)
 };
 
 // What is computed of a sequence: queries q0 .. q0 + nq, tokens 0 .. len.  first_new is the place of its first new token,
@@ -213,7 +223,7 @@ __device__ __forceinline__ void rescale(V &o, float f) {
 // Which sums of exponentials give a result (none: the row saw nothing) and its reciprocal; NaN stays NaN.
 __device__ __forceinline__ float reciprocal(float l) { return l == 0.0f ? 0.0f : 1.0f / l; }
 
-// The workspace: D sums for each row of a slot, the slots' maxima and sums, and the first and last worker of each item.
+// The workspace: D sums for each row of a slot, the slots' maxima and sums, and the records.
 __device__ __forceinline__ float *part_sums(const AttentionArgs &a, const Division &d, int64_t slot, int dim) {
   return a.partial + slot * d.rows * dim;
 }
@@ -221,8 +231,8 @@ __device__ __forceinline__ float *part_stats(const AttentionArgs &a, const Divis
   return a.partial + 2 * (int64_t)d.workers * d.rows * dim + slot * d.rows * 2;
 }
 
-__device__ __forceinline__ int *item_workers(const AttentionArgs &a, const Division &d) {
-  return (int *)(a.partial + 2 * (int64_t)d.workers * d.rows * (a.cache.dim + 2));
+__device__ __forceinline__ Record *records_of(const AttentionArgs &a, const Division &d) {
+  return (Record *)(a.partial + 2 * (int64_t)d.workers * d.rows * (a.cache.dim + 2));
 }
 
 // A worker's run, piece by piece.
@@ -289,13 +299,17 @@ struct Pieces {
     slot = t0 > 0 ? 0 : 1;
     if (slot && d.workers && threadIdx.x == 0) {
       // who has the rest: read by k_join
-      int *w = item_workers(a, d) + 2 * (((int64_t)b * a.cache.heads + head) * d.blocks + block);
-      w[0] = blockIdx.x;
-      w[1] = (int)((at + tiles - 1) / per);
+      const Record r{(int)blockIdx.x, (int)((at + tiles - 1) / per), b, head * d.blocks + block};
+      records_of(a, d)[d.by_worker ? blockIdx.x : (int64_t)b * a.cache.heads * d.blocks + r.part] = r;
     }
     at += t1 - t0;
     in += t1 - t0;
     return true;
+  }
+  // After the last piece: a worker's record where no item began.
+  __device__ __forceinline__ void finish(const AttentionArgs &a, const Division &d) {
+    if (d.by_worker && d.workers && (at == blockIdx.x * per || slot == 0) && threadIdx.x == 0)
+      records_of(a, d)[blockIdx.x] = Record{(int)blockIdx.x, (int)blockIdx.x, 0, 0};
   }
 };
 

@@ -8,18 +8,21 @@ namespace mx {
 // if WIDE) has ROWS rows of an item; WIDE: all waves share one row, as a row of few items has many pieces.
 constexpr int JOIN_ROWS = 4;
 
-template <int D, bool WIDE>
+template <int D, bool WIDE, bool BY_WORKER>
 __global__ __launch_bounds__(WIDE ? 1024 : 256) void k_join(AttentionArgs a, Division dv, int row_groups) {
   constexpr int WAVES = WIDE ? 16 : 4;
-  __shared__ float part[WIDE ? WAVES : 1][D + 2];
+  __shared__ float waves[WIDE ? WAVES : 1][D + 2];
   const int wave = uniform((int)threadIdx.x / 64), lane = threadIdx.x % 64;
-  const int item = blockIdx.x / row_groups, row0 = (blockIdx.x - item * row_groups) * (WIDE ? 1 : JOIN_ROWS);
-  const int block = item % dv.blocks, head = item / dv.blocks % a.cache.heads, b = item / dv.blocks / a.cache.heads;
-  const int2 ws = *(const int2 *)(item_workers(a, dv) + 2 * (int64_t)item);
+  const int at = blockIdx.x / row_groups, row0 = (blockIdx.x - at * row_groups) * (WIDE ? 1 : JOIN_ROWS);
+  const Record rec = records_of(a, dv)[at];
+  // the item's record is where it belongs, so its sequence is read without waiting for it
+  const int item = BY_WORKER ? uniform(rec.part) : at;
+  const int block = item % dv.blocks, head = item / dv.blocks % a.cache.heads;
+  const int b = BY_WORKER ? uniform(rec.b) : item / dv.blocks / a.cache.heads;
   const Sequence s = uniform(sequence_of(a, b));
   const int rows = s.nq * a.group - block * dv.rows;  // of this block, if not more than it holds
   if (row0 >= rows) return;                           // (also for items that are not there, whose workers are not set)
-  const int w0 = uniform(ws.x), w1 = uniform(ws.y);
+  const int w0 = uniform(rec.first), w1 = uniform(rec.last);
   if (w0 == w1) return;  // one worker had all of it and has written the result
   constexpr int N = (D + 63) / 64;
   const int last = rows < dv.rows ? rows : dv.rows;
@@ -52,19 +55,19 @@ __global__ __launch_bounds__(WIDE ? 1024 : 256) void k_join(AttentionArgs a, Div
     }
 #pragma unroll
     for (int i = 0; i < N; ++i)
-      if (D % 64 == 0 || 64 * i + lane < D) part[wave][64 * i + lane] = acc[i];
-    if (lane == 0) part[wave][D] = m, part[wave][D + 1] = l;
+      if (D % 64 == 0 || 64 * i + lane < D) waves[wave][64 * i + lane] = acc[i];
+    if (lane == 0) waves[wave][D] = m, waves[wave][D + 1] = l;
     __syncthreads();
     if (threadIdx.x < D) {
       float top = -__builtin_inff(), sum = 0.0f, v = 0.0f;
 #pragma unroll
-      for (int w = 0; w < WAVES; ++w) top = fmaxf(top, part[w][D]);
+      for (int w = 0; w < WAVES; ++w) top = fmaxf(top, waves[w][D]);
 #pragma unroll
       for (int w = 0; w < WAVES; ++w) {
         // a wave without a maximum has sums of zero, or NaN, which has to stay
-        const float f = part[w][D] == -__builtin_inff() ? 1.0f : __builtin_amdgcn_exp2f(part[w][D] - top);
-        sum += f * part[w][D + 1];
-        v += f * part[w][threadIdx.x];
+        const float f = waves[w][D] == -__builtin_inff() ? 1.0f : __builtin_amdgcn_exp2f(waves[w][D] - top);
+        sum += f * waves[w][D + 1];
+        v += f * waves[w][threadIdx.x];
       }
       out[threadIdx.x] = (unsigned short)bf16x2_rne(v * reciprocal(sum), 0.0f);
     }
@@ -84,19 +87,19 @@ int64_t attention_workspace(int fmt, int dim, int heads, int group, int batch, i
   bool tiled;
   const Division d = division_of(dim, heads, group, batch, max_q, max_kv, &tiled);
   if (d.workers == 0) return 0;
-  return 2 * (int64_t)d.workers * d.rows * (dim + 2) * 4 + (int64_t)batch * heads * d.blocks * 8;
+  return 2 * (int64_t)d.workers * d.rows * (dim + 2) * 4 + (int64_t)d.records * (int64_t)sizeof(Record);
 }
 
 template <int D>
 static hipError_t join(const AttentionArgs &a, const Division &d, hipStream_t stream) {
-  const int64_t items = (int64_t)a.batch * a.cache.heads * d.blocks;
   const int most = a.max_q * a.group < d.rows ? a.max_q * a.group : d.rows;  // rows of a block
   // eight pieces or more of every item on the average and few rows: one row for sixteen waves
-  if (d.workers / items >= 8 && items * most <= 2 * device_cu_count()) {
-    k_join<D, true><<<(unsigned)(items * most), 1024, 0, stream>>>(a, d, most);
+  if (d.workers / d.records >= 8 && d.records * most <= 2 * device_cu_count()) {
+    k_join<D, true, false><<<d.records * most, 1024, 0, stream>>>(a, d, most);
   } else {
     const int groups = (most + JOIN_ROWS - 1) / JOIN_ROWS;
-    k_join<D, false><<<(unsigned)(items * groups), 256, 0, stream>>>(a, d, groups);
+    if (d.by_worker) k_join<D, false, true><<<d.records * groups, 256, 0, stream>>>(a, d, groups);
+    else k_join<D, false, false><<<d.records * groups, 256, 0, stream>>>(a, d, groups);
   }
   return hipGetLastError();
 }
@@ -135,7 +138,12 @@ static Division divide(int rows, int64_t workers, int min_tiles, int heads, int 
   d.tiles = (int)(max_kv > 0 ? (max_kv + TILE - 1) / TILE : 1);
   const int64_t items = (int64_t)batch * heads * d.blocks;
   const double most = __builtin_ceil((double)items * d.tiles / min_tiles);
-  d.workers = d.tiles <= min_tiles && items <= INT32_MAX ? 0 : (int)((double)workers < most ? workers : (int64_t)most);
+  // a launch has fewer than 2^32 threads: items of up to 512 are counted by the workers where there are too many of them
+  d.workers = d.tiles <= min_tiles && items < ((int64_t)1 << 32) / 512
+                  ? 0
+                  : (int)((double)workers < most ? workers : (int64_t)most);
+  d.by_worker = items > d.workers;
+  d.records = d.by_worker ? d.workers : (int)items;
   return d;
 }
 

@@ -147,7 +147,8 @@ __global__ __launch_bounds__(64 * ATT_WAVES, rows_held(D, NT)) void k_attention_
   const CacheView &cv = a.cache;
   const int wave = uniform((int)threadIdx.x / 64), lane = threadIdx.x % 64, n16 = lane % 16, g = lane / 16;
   const int page_mask = (1 << cv.page_log2) - 1;
-  for (Pieces pc(a, dv); pc.next(a, dv);) {
+  Pieces pc(a, dv);
+  while (pc.next(a, dv)) {
     const int nq = uniform(pc.s.nq), len = uniform(pc.s.len), q0 = uniform(pc.s.q0), b = uniform(pc.b);
     const int head = uniform(pc.head), rb = uniform(pc.block);
     const int t0 = uniform(pc.t0), t1 = uniform(pc.t1), tiles = uniform(pc.tiles), slot = uniform(pc.slot);
@@ -412,6 +413,7 @@ __global__ __launch_bounds__(64 * ATT_WAVES, rows_held(D, NT)) void k_attention_
     }
   }
   }
+  pc.finish(a, dv);
   zero_padding(a);
 }
 

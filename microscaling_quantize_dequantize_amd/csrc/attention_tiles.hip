@@ -90,7 +90,8 @@ __global__ __launch_bounds__(64 * WAVES, D <= 128 ? 2 : 1) void k_attention_tile
   constexpr int PARTS = D / 32 / VG;                           // groups for 16 tokens
   const float to_log2 = a.scale * 1.4426950408889634f;
 
-  for (Pieces pc(a, dv); pc.next(a, dv);) {
+  Pieces pc(a, dv);
+  while (pc.next(a, dv)) {
     const int nq = uniform(pc.s.nq), len = uniform(pc.s.len), q0 = uniform(pc.s.q0), b = uniform(pc.b);
     const int head = uniform(pc.head), rb = uniform(pc.block);
     const int t0 = uniform(pc.t0), t1 = uniform(pc.t1), tiles = uniform(pc.tiles), slot = uniform(pc.slot);
@@ -355,6 +356,7 @@ __global__ __launch_bounds__(64 * WAVES, D <= 128 ? 2 : 1) void k_attention_tile
       }
     }
   }
+  pc.finish(a, dv);
   zero_padding(a);
 }
 

@@ -66,3 +66,15 @@ def test_only_padding(mx, batch):
     mx.mx_cache_attention(c.cache, q, c.q_starts[:batch + 1], c.kv_lens[:batch], c.table[:batch], max_q=0, max_kv=40,
                           out=out)
     assert not bool(out.any())
+
+
+@pytest.mark.parametrize("batch,heads,group,chunk,dim,fmt", [(1024, 8, 8, 1024, 64, 1), (60, 4, 4, 500, 128, 0),
+                                                             (300, 2, 3, 40, 256, 1), (900, 2, 2, 1, 64, 1)])
+def test_one_chunk_among_single_tokens(mx, batch, heads, group, chunk, dim, fmt):
+    """Bounds that give every sequence the long one's blocks: far more items than there are, or than workgroups."""
+    kv = [1 + (37 * b) % 60 for b in range(batch)]
+    new = [1] * batch
+    kv[3], kv[batch - 2] = 1500, 700
+    kv[7], new[7] = 1100 + chunk // 8, chunk
+    c = Case(mx, fmt, heads, group, dim, 16, kv, new, seed=batch)
+    check(c, c.run(mx), device="cuda")
