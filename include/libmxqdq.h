@@ -264,6 +264,9 @@ MX_API int mx_nvfp4_dequantize(const uint8_t *codes, const uint8_t *scales,
  *   positions  [tokens] int64; inv_freq [rot/2] fp64 (scaled for long contexts
  *              by the caller).  Angles are formed and reduced in fp64 (accurate
  *              below 2^50 rad) and rounded once to fp32.
+ *   tokens     below 2^31, and with a rotation up to (2^24 - 1) times 4096 / rot
+ *              (rounded down), what a launch holds (MX_ESHAPE); heads up to
+ *              65535.
  *   rot        even, 0 <= rot <= dim <= 4096 (MX_EARG).
  *   layout     MX_ROTARY_HALF: pair p is dimensions p and p + rot/2;
  *              MX_ROTARY_INTERLEAVED: dimensions 2p and 2p + 1.
@@ -304,6 +307,7 @@ typedef struct mx_cache {
  *   k, v       [tokens x heads x dim] bf16, strides in elements as above.
  *   slots      [tokens] int64; a slot outside the cache (a negative one, say)
  *              is skipped.  Two tokens with one slot leave either's bytes.
+ *   tokens     up to 2^27 - 8, what a launch holds (MX_ESHAPE).
  */
 MX_API int mx_cache_write(const mx_cache *cache, const void *k,
                           int64_t k_token_stride, int64_t k_head_stride,
@@ -316,7 +320,7 @@ MX_API int mx_cache_write(const mx_cache *cache, const void *k,
 /*
  * Read slots back: k, v [tokens x heads x dim] bf16, contiguous, 16-byte
  * aligned; values rounded to nearest-even.  A slot outside the cache gives
- * zeros.
+ * zeros.  tokens: up to 2^28 - 16 (MX_ESHAPE).
  */
 MX_API int mx_cache_read(const mx_cache *cache, const int64_t *slots,
                          int64_t tokens, void *k, void *v);

@@ -272,6 +272,8 @@ MX_API int mx_rope(const void *src, int64_t src_token_stride, int64_t src_head_s
   if ((st = check_dtype(dtype))) return st;
   if (tokens < 0 || !fits(heads, 65535) || !fits(dim, 4096) || tokens > INT32_MAX) return MX_ESHAPE;
   if ((st = check_rotary(dim, positions, inv_freq, rot, layout))) return st;
+  // grid limits: tokens of a workgroup at least, and their angles in its table
+  if ((tokens + mx::MAX_GROUPS_256 - 1) / mx::MAX_GROUPS_256 * (rot / 2) > mx::ROPE_TABLE) return MX_ESHAPE;
   if (tokens == 0 || heads == 0 || dim == 0) return MX_OK;
   if (!src || !dst || (rot > 0 && (!positions || !inv_freq))) return MX_ENULL;
   const uintptr_t size = dtype == MX_DTYPE_F32 ? 4 : 2;
@@ -291,7 +293,7 @@ MX_API int mx_cache_write(const mx_cache *cache, const void *k, int64_t k_token_
                           double scale) {
   int st;
   if ((st = check_cache(cache))) return st;
-  if (!fits(tokens, INT32_MAX)) return MX_ESHAPE;
+  if (!fits(tokens, mx::MAX_GROUPS_256 * mx::CACHE_WRITE_TILE)) return MX_ESHAPE;
   if ((st = check_rotary(cache->dim, positions, inv_freq, rot, layout))) return st;
   if (tokens == 0 || cache->pages == 0) return MX_OK;
   if (empty_cache(cache) || !k || !v || !slots || (rot > 0 && (!positions || !inv_freq))) return MX_ENULL;
@@ -304,7 +306,7 @@ MX_API int mx_cache_write(const mx_cache *cache, const void *k, int64_t k_token_
 MX_API int mx_cache_read(const mx_cache *cache, const int64_t *slots, int64_t tokens, void *k, void *v) {
   int st;
   if ((st = check_cache(cache))) return st;
-  if (!fits(tokens, INT32_MAX)) return MX_ESHAPE;
+  if (!fits(tokens, mx::MAX_GROUPS_256 * mx::CACHE_READ_TILE)) return MX_ESHAPE;
   if (tokens == 0) return MX_OK;
   if ((cache->pages > 0 && empty_cache(cache)) || !slots || !k || !v) return MX_ENULL;
   if (!aligned(slots, 8) || !aligned(k, 16) || !aligned(v, 16)) return MX_EALIGN;

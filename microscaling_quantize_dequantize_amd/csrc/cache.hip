@@ -28,7 +28,7 @@
 namespace mx {
 
 constexpr int WRITE_THREADS = 256;
-constexpr int WRITE_TABLE = 1024;  // (token, pair) entries: 16 KiB of LDS
+constexpr int WRITE_TABLE = CACHE_WRITE_TILE * 128;  // (token, pair) entries of up to 128 pairs: 16 KiB of LDS
 
 struct WriteArgs {
   CacheView cache;
@@ -187,8 +187,7 @@ hipError_t launch_cache_write(const CacheView &cache, const void *k, const int64
                               hipStream_t stream) {
   WriteArgs a{cache, {(const unsigned short *)k, (const unsigned short *)v}, {k_strides[0], v_strides[0]},
               {k_strides[1], v_strides[1]}, slots, positions, inv_freq, scale, tokens, (int)(rot / 2), 0, 0};
-  a.tile = 8;
-  while (a.half * a.tile > WRITE_TABLE) a.tile /= 2;
+  a.tile = CACHE_WRITE_TILE;
   // all heads of a tile share its angles, unless there are too few tiles to fill the CUs
   const int64_t tiles = (tokens + a.tile - 1) / a.tile;
   int parts = 1;
@@ -218,7 +217,7 @@ hipError_t launch_cache_write(const CacheView &cache, const void *k, const int64
 // Slots back to bf16 [tokens, H, D]: the same pieces of 8 dimensions, rounded
 // to nearest-even where a value is below bf16's range.  Slots outside the
 // cache (padding) give zeros.
-constexpr int READ_THREADS = 256, READ_TILE = 16;
+constexpr int READ_THREADS = 256, READ_TILE = CACHE_READ_TILE;
 
 template <int FMT>
 __global__ __launch_bounds__(READ_THREADS) void k_cache_read(CacheView cv, const int64_t *__restrict__ slots,

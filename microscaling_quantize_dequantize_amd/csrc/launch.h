@@ -15,6 +15,11 @@ enum Op { OP_QDQ = 0, OP_QUANT = 1, OP_ROTATE = 2 };
 // Number of compute units of the current device (cached per device).
 int device_cu_count();
 
+// Workgroups of 256 threads that a launch holds in x: fewer than 2^32 threads.
+constexpr int64_t MAX_GROUPS_256 = ((int64_t)1 << 24) - 1;
+constexpr int CACHE_WRITE_TILE = 8, CACHE_READ_TILE = 16;  // tokens of a workgroup
+constexpr int ROPE_TABLE = 2048;                           // angles of a workgroup: (token, pair) entries
+
 // bl == nullptr: row-major scales; otherwise the blocked layout it describes.
 hipError_t launch_unrot(int fmt, int op, int dtype, const void *src, void *dst, uint8_t *codes,
                         uint8_t *scales, int64_t n, hipStream_t stream, const BlockedScales *bl = nullptr);

@@ -22,7 +22,6 @@
 namespace mx {
 
 constexpr int ROPE_THREADS = 256;
-constexpr int ROPE_TABLE = 2048;  // (token, pair) entries of a workgroup's table: 16 KiB of LDS
 
 struct RopeArgs {
   int64_t tokens, src_token, src_head, dst_token, dst_head;  // strides in elements
@@ -228,9 +227,11 @@ hipError_t launch_rope(int dtype, const void *src, void *dst, int64_t tokens, in
   // there are four workgroups for every CU
   const int64_t row = heads * dim * size;
   int64_t per = 4 * 16 * ROPE_THREADS / row;
-  if (a.half && per > ROPE_TABLE / a.half) per = ROPE_TABLE / a.half;
+  if (a.half && per > ROPE_TABLE / a.half) per = ROPE_TABLE / a.half;  // 16 KiB of LDS
   const int64_t spread = tokens / (4 * device_cu_count());
   if (per > spread) per = spread;
+  const int64_t least = (tokens + MAX_GROUPS_256 - 1) / MAX_GROUPS_256;  // the table holds it: checked by the caller
+  if (per < least) per = least;
   a.per_wg = per < 1 ? 1 : (int)per;
   if (staged) {
     if (dtype == 1) rope_staged<float, 4>(src, dst, a, stream);

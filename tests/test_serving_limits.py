@@ -14,3 +14,16 @@ def test_short_sequences_of_a_very_large_batch_are_divided(b):
     space = b.raw().mx_cache_attention_workspace
     for batch, divided in ((1 << 20, False), ((1 << 22) - 1, False), (1 << 22, True), (1 << 24, True)):
         assert (space(ctypes.addressof(keep), 4, batch, batch, 1, 64) > 0) == divided, batch
+
+
+def test_more_tokens_than_a_launch_holds(b):
+    """2^32 threads and more: workgroups of 256 threads with 8 tokens (write), 16 (read), or as many as the angle table
+    holds (rotary)."""
+    keep = struct(b)
+    c, lib = ctypes.addressof(keep), b.raw()
+    for tokens in ((1 << 27) - 7, 1 << 27, (1 << 31) - 1):
+        assert lib.mx_cache_write(c, A, 128, 64, A, 128, 64, A, tokens, None, None, 0, 0, 1.0) == ESHAPE
+    for tokens in ((1 << 28) - 15, 1 << 28, (1 << 31) - 1):
+        assert lib.mx_cache_read(c, A, tokens, A, A) == ESHAPE
+    for rot, tokens in ((4096, 1 << 24), (4096, (1 << 31) - 1), (64, (1 << 30) - 63), (34, (1 << 31) - 1)):
+        assert rope(b, dim=4096, rot=rot, tokens=tokens) == ESHAPE
