@@ -354,10 +354,10 @@ MX_API int mx_cache_read(const mx_cache *cache, const int64_t *slots,
  *              count as not seen; so do tokens behind the pages of table_pages.
  *   workspace  mx_cache_attention_workspace bytes, 16-byte aligned, contents
  *              free; it may be NULL where that is 0.
- * dim is 64, 96, 128, 192 or 256 and scale is positive and finite (MX_EARG);
- * scores, weights' sums and output sums are fp32, weights are rounded to bf16
- * for their products with the values.  Enqueues one kernel, or two where the
- * tokens are split over workgroups.
+ * dim is 64, 96, 128, 192 or 256 and scale is positive, and finite also times
+ * log2(e) (MX_EARG); scores, weights' sums and output sums are fp32, weights
+ * are rounded to bf16 for their products with the values.  Enqueues one kernel,
+ * or two where the tokens are split over workgroups.
  */
 MX_API int64_t mx_cache_attention_workspace(const mx_cache *cache,
                                             int64_t q_heads, int64_t batch,

@@ -331,7 +331,7 @@ MX_API int mx_cache_attention(const mx_cache *cache, const void *q, int64_t q_to
   if ((st = check_attention(cache, q_heads, batch, total_q, max_q, max_kv))) return st;
   if (!fits(table_pages, INT32_MAX / cache->page) || table_stride < table_pages || !fits(tree_words, INT32_MAX))
     return MX_ESHAPE;
-  if (!(scale > 0.0f && scale <= 3.402823466e38f)) return MX_EARG;
+  if (!(scale > 0.0f && scale * mx::LOG2_E <= 3.402823466e38f)) return MX_EARG;  // the kernels' factor is finite
   if (tree && (max_q < total_q ? max_q : total_q) > 64 * tree_words) return MX_EARG;
   if (total_q == 0) return MX_OK;
   const bool none = batch == 0 || max_q == 0;  // no sequence has queries: zeros, if there is an output

@@ -228,7 +228,7 @@ __global__ __launch_bounds__(64 * ATT_WAVES, rows_held(D, NT)) void k_attention_
     if constexpr (A::C1 > 0) load_bytes<16>(vs1, s + (((A::B1 + n16 * A::C1) / 32) << cv.page_log2));
   };
 
-  const float to_log2 = a.scale * 1.4426950408889634f;
+  const float to_log2 = a.scale * LOG2_E;
   // rows may differ in what they see of the tile, or it ends behind the tokens
   auto differs = [&](int base) { return base + TILE > seen_by_all || base + TILE > hi; };
   const int first = lo + TILE * wave;

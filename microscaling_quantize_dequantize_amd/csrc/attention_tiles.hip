@@ -88,7 +88,7 @@ __global__ __launch_bounds__(64 * WAVES, D <= 128 ? 2 : 1) void k_attention_tile
   constexpr bool ACC = D > 128 && WAVES == 4;  // one wave a SIMD: the sums are in accumulation registers
   constexpr int VG = D % 128 == 0 ? 4 : D % 96 == 0 ? 3 : 2;  // V operands of a group
   constexpr int PARTS = D / 32 / VG;                           // groups for 16 tokens
-  const float to_log2 = a.scale * 1.4426950408889634f;
+  const float to_log2 = a.scale * LOG2_E;
 
   Pieces pc(a, dv);
   while (pc.next(a, dv)) {

@@ -75,6 +75,8 @@ hipError_t launch_cache_write(const CacheView &cache, const void *k, const int64
 hipError_t launch_cache_read(const CacheView &cache, const int64_t *slots, int64_t tokens, void *k, void *v,
                              hipStream_t stream);
 
+constexpr float LOG2_E = 1.4426950408889634f;  // weights are powers of two: the scores' factor is scale * LOG2_E
+
 struct AttentionArgs {
   CacheView cache;
   const unsigned short *q;

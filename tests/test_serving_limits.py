@@ -4,7 +4,7 @@ import ctypes
 
 import pytest
 
-from test_cache_checks import A, ESHAPE, b, rope, struct  # noqa: F401 (b is a fixture)
+from test_cache_checks import A, EARG, ESHAPE, b, rope, struct  # noqa: F401 (b is a fixture)
 
 
 def test_short_sequences_of_a_very_large_batch_are_divided(b):
@@ -27,3 +27,11 @@ def test_more_tokens_than_a_launch_holds(b):
         assert lib.mx_cache_read(c, A, tokens, A, A) == ESHAPE
     for rot, tokens in ((4096, 1 << 24), (4096, (1 << 31) - 1), (64, (1 << 30) - 63), (34, (1 << 31) - 1)):
         assert rope(b, dim=4096, rot=rot, tokens=tokens) == ESHAPE
+
+
+def test_scale_whose_factor_overflows(b):
+    """The kernels multiply scores by scale * log2(e), which has to be finite too: zero scores would become NaN."""
+    keep = struct(b)
+    for scale in (2.36e38, 3.4e38):
+        assert b.raw().mx_cache_attention(ctypes.addressof(keep), A, 256, 64, 4, A, A, 2, A, 4, 4, 2, 1, 64, None, 0, scale,
+                                          A, A, 1 << 30) == EARG
