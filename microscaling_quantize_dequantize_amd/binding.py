@@ -451,6 +451,8 @@ class MXCache:
         if not isinstance(k_codes, torch.Tensor) or k_codes.dim() != 4:
             raise ValueError("k_codes must be a 4-D uint8 tensor [pages, heads, page, dim/2 or dim]")
         pages, heads, page, cols = k_codes.shape
+        if not 1 <= heads <= 65535:
+            raise ValueError(f"a cache has 1 to 65535 heads, got {heads}")
         dim = 2 * cols if fmt == E2M1 else cols
         if dim % 32 or not 32 <= dim <= 256:
             raise ValueError(f"the head's dimension must be a multiple of 32 up to 256, got {dim}")

@@ -4,7 +4,7 @@ import ctypes
 
 import pytest
 
-from test_cache_checks import A, EARG, ESHAPE, b, rope, struct  # noqa: F401 (b is a fixture)
+from test_cache_checks import A, EARG, ESHAPE, b, mx, rope, struct  # noqa: F401 (b and mx are fixtures)
 
 
 def test_short_sequences_of_a_very_large_batch_are_divided(b):
@@ -35,3 +35,10 @@ def test_scale_whose_factor_overflows(b):
     for scale in (2.36e38, 3.4e38):
         assert b.raw().mx_cache_attention(ctypes.addressof(keep), A, 256, 64, 4, A, A, 2, A, 4, 4, 2, 1, 64, None, 0, scale,
                                           A, A, 1 << 30) == EARG
+
+
+def test_cache_without_heads_is_refused(mx):
+    with pytest.raises(ValueError, match="heads"):
+        mx.MXCache.allocate(1, 2, 0, 16, 64, device="cpu")
+    with pytest.raises(ValueError, match="heads"):
+        mx.MXCache.allocate(1, 1, 65536, 16, 32, device="cpu")
