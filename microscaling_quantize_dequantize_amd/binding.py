@@ -33,6 +33,7 @@ E2M1, E4M3 = 0, 1
 BF16, F32 = 0, 1
 ROWMAJOR, BLOCKED = 0, 1
 HALF, INTERLEAVED = 0, 1
+ATTENTION_DIMS = (64, 96, 128, 192, 256)
 _DTYPE = {torch.bfloat16: BF16, torch.float32: F32}
 
 _vp, _i64, _int = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int
@@ -442,7 +443,8 @@ class MXCache:
     """A paged cache of keys and values in MX codes over the caller's tensors.
 
     fmt E2M1 or E4M3; codes uint8 [pages, heads, page, dim/2 or dim]; scales uint8 [pages, heads, dim/32, page].
-    Token slots are page number * page + row.  The handle keeps the four tensors; it may be used on any stream."""
+    Token slots are page number * page + row.  The handle keeps the four tensors; it may be used on any stream.
+    dim is a multiple of 32 up to 256; attention takes 64, 96, 128, 192 and 256 of these."""
 
     def __init__(self, fmt: int, k_codes: torch.Tensor, k_scales: torch.Tensor, v_codes: torch.Tensor,
                  v_scales: torch.Tensor):
@@ -551,6 +553,8 @@ def mx_cache_attention(cache: MXCache, q: torch.Tensor, q_starts: torch.Tensor, 
     if dim != cache.dim or heads % cache.heads:
         raise ValueError(f"q must have {cache.dim} dimensions and a multiple of {cache.heads} heads, got "
                          f"{tuple(q.shape)}")
+    if dim not in ATTENTION_DIMS:
+        raise ValueError(f"attention takes heads of {', '.join(map(str, ATTENTION_DIMS))} dimensions, got {dim}")
     if not isinstance(kv_lens, torch.Tensor) or kv_lens.dim() != 1:
         raise ValueError("kv_lens must be a one-dimensional int32 tensor")
     batch = kv_lens.shape[0]

@@ -3,8 +3,9 @@
 import ctypes
 
 import pytest
+import torch
 
-from test_cache_checks import A, EARG, ESHAPE, b, mx, rope, struct  # noqa: F401 (b and mx are fixtures)
+from test_cache_checks import A, EARG, ESHAPE, b, bf, ints, mx, rope, struct  # noqa: F401 (b and mx are fixtures)
 
 
 def test_short_sequences_of_a_very_large_batch_are_divided(b):
@@ -42,3 +43,12 @@ def test_cache_without_heads_is_refused(mx):
         mx.MXCache.allocate(1, 2, 0, 16, 64, device="cpu")
     with pytest.raises(ValueError, match="heads"):
         mx.MXCache.allocate(1, 1, 65536, 16, 32, device="cpu")
+
+
+@pytest.mark.parametrize("dim", [32, 160, 224])
+def test_heads_that_attention_does_not_take(mx, dim):
+    """A cache may have them (they are written and read); attention says which it takes."""
+    cache = mx.MXCache.allocate(0, 2, 1, 16, dim, device="cpu")
+    i32 = torch.int32
+    with pytest.raises(ValueError, match="64, 96, 128, 192, 256"):
+        mx.mx_cache_attention(cache, bf(2, 1, dim), ints(3, dtype=i32), ints(2, dtype=i32), ints(2, 2, dtype=i32), 1, 20)
