@@ -8,7 +8,7 @@ outputs [M, K] in the stated dtype), then that each is a contiguous tensor
 on the current device; a mismatch raises ValueError or TypeError.  It then points the
 library at torch's current stream and passes raw pointers.  All computation
 happens in the HIP kernels; there is no fallback: if the library is missing
-the import fails.
+the import fails.  Nothing is recorded for autograd, except by mx_rope.
 
 Tensor conventions: bf16 data is ``torch.bfloat16``; codes and scales are
 ``torch.uint8``; the rotation is an r x r tensor in the source dtype.
@@ -419,8 +419,11 @@ def mx_rope(x: torch.Tensor, positions: torch.Tensor, inv_freq: torch.Tensor, la
 
     positions int64 [tokens]; inv_freq float64 [pairs]; layout HALF (dimension p with p + pairs) or INTERLEAVED
     (2p with 2p + 1); scale multiplies the rotated dimensions.  inverse: the transposed rotation, which takes the
-    gradient of the output to that of x.  dst may be x itself."""
+    gradient of the output to that of x.  dst may be x itself.  Without dst the call is recorded for autograd if x
+    requires a gradient (inv_freq gets none); with dst nothing is recorded."""
     ps, st, sh = _heads(x, "x", (torch.bfloat16, torch.float32))
+    if x.requires_grad and dst is None and torch.is_grad_enabled():
+        return _Rope.apply(x, positions, inv_freq, layout, scale, inverse)
     tokens, heads, dim = x.shape
     if dst is None:  # what is allocated here needs no check
         dst = _like(x)
@@ -432,6 +435,23 @@ def mx_rope(x: torch.Tensor, positions: torch.Tensor, inv_freq: torch.Tensor, la
     _call(_lib.mx_rope(ps, st, sh, _DTYPE[x.dtype], tokens, heads, dim, pp, pf, rot, layout, scale,
                        1 if inverse else 0, pd, dt, dh))
     return dst
+
+
+class _Rope(torch.autograd.Function):
+    """mx_rope with its gradient, the transposed rotation of that of the output (and the other way round)."""
+
+    @staticmethod
+    def forward(ctx, x, positions, inv_freq, layout, scale, inverse):
+        ctx.save_for_backward(positions, inv_freq)
+        ctx.rotation = layout, scale, inverse
+        return mx_rope(x, positions, inv_freq, layout, scale, inverse)
+
+    @staticmethod
+    def backward(ctx, grad):
+        layout, scale, inverse = ctx.rotation
+        if grad.stride(2) != 1:  # that of a sum, say, is one value for all
+            grad = grad.contiguous()
+        return mx_rope(grad, *ctx.saved_tensors, layout, scale, not inverse), None, None, None, None, None
 
 
 class _CacheStruct(ctypes.Structure):
