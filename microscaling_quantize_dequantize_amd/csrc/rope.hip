@@ -42,8 +42,9 @@ __device__ __forceinline__ void from_f32(float &d, float f) { d = f; }
 
 constexpr int ROPE_ROWS = 2;  // rows whose loads a thread has under way together, the first ones before the angles
 
+// src and dst may be one tensor (no __restrict__): a thread reads all of a piece's pairs before it writes them.
 template <typename T, int VEC, int LAYOUT>
-__global__ __launch_bounds__(ROPE_THREADS) void k_rope(const T *__restrict__ src, T *__restrict__ dst, RopeArgs a) {
+__global__ __launch_bounds__(ROPE_THREADS) void k_rope(const T *src, T *dst, RopeArgs a) {
   __shared__ float tc[ROPE_TABLE], ts[ROPE_TABLE];
   // items of a head: pieces of VEC pairs (HALF and single pairs) or of VEC elements, then the pieces that are copied
   constexpr bool PAIRS = LAYOUT == ROTARY_HALF || VEC == 1;
@@ -137,8 +138,7 @@ __global__ __launch_bounds__(ROPE_THREADS) void k_rope(const T *__restrict__ src
 // same case, 62 of 128 dimensions rotated, took 140 us for the 8192 x 64 heads that take 42 with whole pieces.)
 // Every row is in LDS before any of it is written, so dst may be src.
 template <typename T, int VEC>
-__global__ __launch_bounds__(ROPE_THREADS) void k_rope_staged(const T *__restrict__ src, T *__restrict__ dst,
-                                                              RopeArgs a) {
+__global__ __launch_bounds__(ROPE_THREADS) void k_rope_staged(const T *src, T *dst, RopeArgs a) {
   __shared__ float tc[ROPE_TABLE], ts[ROPE_TABLE];
   __shared__ Piece<T, VEC> rows[2][ROPE_THREADS];
   const int64_t t0 = (int64_t)blockIdx.x * a.per_wg;
