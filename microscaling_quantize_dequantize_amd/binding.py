@@ -143,9 +143,14 @@ def _call(status: int) -> None:
         raise MXError(status)
 
 
+# The handle of a device's current stream: the public call builds a Stream object around it, 3 us of a call's 10, so the
+# one that torch's own compiled code takes is used where there is one.
+_current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+    (lambda device: torch.cuda.current_stream(device).cuda_stream)
+
+
 def _stream() -> None:
-    # the handle alone: torch.cuda.current_stream() builds a Stream object around it, 3 us of a call's 10
-    _lib.mx_set_stream(torch._C._cuda_getCurrentRawStream(torch.cuda.current_device()))
+    _lib.mx_set_stream(_current_stream(torch.cuda.current_device()))
 
 
 def mx_qdq(fmt: int, src: torch.Tensor, rot: torch.Tensor | None = None,

@@ -52,3 +52,20 @@ def test_heads_that_attention_does_not_take(mx, dim):
     i32 = torch.int32
     with pytest.raises(ValueError, match="64, 96, 128, 192, 256"):
         mx.mx_cache_attention(cache, bf(2, 1, dim), ints(3, dtype=i32), ints(2, dtype=i32), ints(2, 2, dtype=i32), 1, 20)
+
+
+def test_stream_without_the_private_call(b, monkeypatch):
+    """A torch that lacks the quick way to the stream's handle is served by the public one."""
+    import importlib.util
+    import types
+    monkeypatch.delattr(torch._C, "_cuda_getCurrentRawStream", raising=False)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 3)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda device: types.SimpleNamespace(cuda_stream=1000 + device))
+    spec = importlib.util.spec_from_file_location("binding_without", b.__file__)
+    again = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(again)
+    try:
+        again._stream()
+        assert again.raw().mx_get_stream() == 1003
+    finally:
+        again.raw().mx_set_stream(None)
