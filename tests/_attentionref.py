@@ -59,6 +59,8 @@ def check(c, got, **kw):
     assert torch.equal(torch.isnan(got), torch.isnan(ref)), "NaN elsewhere"
     inf = torch.isinf(ref)
     assert torch.equal(torch.isinf(got), inf) and torch.equal(got[inf], ref[inf]), "infinities elsewhere"
-    bound = R.attention_bound(ref, weight, size, ref.shape[2], max(c.kv))
+    # weights that are off by e_i of themselves, in the products and in their sum, move the result by
+    # sum w_i e_i (v_i - out): up to the largest e_i times (sum w |v| + |out|)
+    bound = R.attention_bound(ref, weight + ref.abs(), size, ref.shape[2], max(c.kv))
     over = torch.where(torch.isfinite(ref), (got - ref).abs() - bound, -1.0)
     assert float(over.max()) <= 0, float(over.max())
