@@ -303,7 +303,7 @@ typedef struct mx_cache {
 /*
  * Quantise new keys and values into their slots (the scale and element rules
  * of mx_quantize).  With rot > 0 the keys are rotated first (as by mx_rope, in
- * fp64) and rounded to bf16.
+ * fp64) and rounded to bf16 (by way of fp32).
  *   k, v       [tokens x heads x dim] bf16, strides in elements as above.
  *   slots      [tokens] int64; a slot outside the cache (a negative one, say)
  *              is skipped.  Two tokens with one slot leave either's bytes.
@@ -356,8 +356,11 @@ MX_API int mx_cache_read(const mx_cache *cache, const int64_t *slots,
  *              free; it may be NULL where that is 0.
  * dim is 64, 96, 128, 192 or 256 and scale is positive, and finite also times
  * log2(e) (MX_EARG); scores, weights' sums and output sums are fp32, weights
- * are rounded to bf16 for their products with the values.  Enqueues one kernel,
- * or two where the tokens are split over workgroups.
+ * are rounded to bf16 for their products with the values.  Weights are powers
+ * of two of up to 2^8 before they are divided by their sum, so values times the
+ * number of tokens should stay below 2^119.  Enqueues one kernel, or two where
+ * the tokens are split over workgroups.  max_q chooses the kernel for the whole
+ * batch: long chunks and many single tokens are quicker in two calls.
  */
 MX_API int64_t mx_cache_attention_workspace(const mx_cache *cache,
                                             int64_t q_heads, int64_t batch,

@@ -138,7 +138,7 @@ static Division divide(int rows, int64_t workers, int min_tiles, int heads, int 
   d.tiles = (int)(max_kv > 0 ? (max_kv + TILE - 1) / TILE : 1);
   const int64_t items = (int64_t)batch * heads * d.blocks;
   const double most = __builtin_ceil((double)items * d.tiles / min_tiles);
-  // a launch has fewer than 2^32 threads: items of up to 512 are counted by the workers where there are too many of them
+  // a launch has fewer than 2^32 threads: with too many items of up to 512 the work is divided all the same
   d.workers = d.tiles <= min_tiles && items < ((int64_t)1 << 32) / 512
                   ? 0
                   : (int)((double)workers < most ? workers : (int64_t)most);

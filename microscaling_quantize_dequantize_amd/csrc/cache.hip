@@ -14,11 +14,13 @@
 // the 32 of a scale and agree on it with two DPP permutations, as in the
 // quantise kernels.  Keys are rotated in fp64 and rounded to bf16 before the
 // scale is taken: the bf16 rounding and the element rounding after it have
-// borders, and a rotation in fp32 would put some values on their wrong side.
+// borders, and a rotation in fp32 would put some values on their wrong side.  The
+// rounding to bf16 goes by way of fp32, as a conversion of fp64 commonly does: it
+// differs from a single rounding for one value in some 10^5.
 //
 // Bound: HBM for reading (16384 tokens of 8 heads of 128 out of MXFP4 17 us, 71004
 // of 5 heads of 96 out of MXFP8 33 us: 5.0 and 6.2 TB/s on MI355X).  Writing the
-// former takes 26-27 us, 3.2 TB/s, and 17 without the rotation: the rest goes to
+// former takes 27 us, 3.1 TB/s, and 17 without the rotation: the rest goes to
 // forming the angles, in fp64 and before a row is loaded, and to the rotation.
 // Loading the first rows before the angles (29 us), tiles of 16 tokens (27) and
 // both pieces of a pair in one thread (26-27) were no faster.  64 tokens take 4 us.

@@ -10,8 +10,8 @@
 // angles are formed once for each (token, pair) in fp64, rounded once to fp32
 // and kept in LDS for all heads of the token, whose pairs are rotated in fp32
 // whatever the type of x.  Measured on MI355X: 8192 x 64 heads of 128 in bf16
-// 41-43 us, 6.3 TB/s; in fp32 103 us, 5.2 TB/s; 4111 x 16 heads of 96 in fp32 10 us,
-// 5.0 TB/s; 8 tokens 3.2 us.
+// 43 us, 6.3 TB/s; in fp32 104 us, 5.2 TB/s; 4111 x 16 heads of 96 in fp32 9.4 us,
+// 5.4 TB/s; 8 tokens 3.4 us.
 //
 // Split: a workgroup owns whole tokens (one, or several while their heads are
 // few), a thread VEC neighbouring pairs of one head, so that both elements of
@@ -134,9 +134,9 @@ __global__ __launch_bounds__(ROPE_THREADS) void k_rope(const T *src, T *dst, Rop
 }
 
 // Half layout whose halves are not whole pieces: a thread has a piece of the row as it lies in memory, and takes the
-// partners of its elements out of LDS, where the workgroup has put the rows' pieces.  (In pieces of single pairs the
-// same case, 62 of 128 dimensions rotated, took 140 us for the 8192 x 64 heads that take 42 with whole pieces.)
-// Every row is in LDS before any of it is written, so dst may be src.
+// partners of its elements out of LDS, where the workgroup has put the rows' pieces.  (62 of 128 dimensions of 8192 x
+// 64 heads in bf16: 66-69 us; 140 in pieces of single pairs; 43 with whole pieces.)  Every row is in LDS before any of
+// it is written, so dst may be src.
 template <typename T, int VEC>
 __global__ __launch_bounds__(ROPE_THREADS) void k_rope_staged(const T *src, T *dst, RopeArgs a) {
   __shared__ float tc[ROPE_TABLE], ts[ROPE_TABLE];

@@ -7,8 +7,8 @@ import _cacheref as R
 
 def reference(c, max_q=None, max_kv=None, device="cpu"):
     """Result, weights and sizes as _cacheref.attention gives them, of a case's sequences.  Queries of a sequence beyond
-    max_q give zeros, tokens beyond max_kv are not seen.  A value above fp32's range is infinite, and a row that sees one
-    (or NaN) has it added to that dimension: its weight is above zero."""
+    max_q give zeros, tokens beyond max_kv are not seen.  A value above fp32's range is infinite, and a row that sees
+    one (or NaN) has it added to that dimension: its weight is above zero."""
     tok = R.Tokens(c.cache)
     q = c.q.double().cpu().to(device)
     total, q_heads, dim = q.shape
@@ -28,8 +28,9 @@ def reference(c, max_q=None, max_kv=None, device="cpu"):
         if tree is None:
             see = place[None] <= torch.arange(m, device=device)[:, None]
         else:
-            word = place.clamp(min=0, max=64 * tree.shape[1] - 1)
-            see = ((tree[at:at + m][:, word // 64] >> (word % 64)) & 1 == 1) & (place < 64 * tree.shape[1]) | (place < 0)
+            bits = 64 * tree.shape[1]
+            word = place.clamp(min=0, max=bits - 1)
+            see = ((tree[at:at + m][:, word // 64] >> (word % 64)) & 1 == 1) & (place < bits) | (place < 0)
         see = see & ok
         kt = k.permute(1, 2, 0).contiguous()
         rows = q[at:at + m].view(m, heads, group, dim).permute(1, 2, 0, 3).reshape(heads, group * m, dim)

@@ -34,8 +34,8 @@ def test_scale_whose_factor_overflows(b):
     """The kernels multiply scores by scale * log2(e), which has to be finite too: zero scores would become NaN."""
     keep = struct(b)
     for scale in (2.36e38, 3.4e38):
-        assert b.raw().mx_cache_attention(ctypes.addressof(keep), A, 256, 64, 4, A, A, 2, A, 4, 4, 2, 1, 64, None, 0, scale,
-                                          A, A, 1 << 30) == EARG
+        assert b.raw().mx_cache_attention(ctypes.addressof(keep), A, 256, 64, 4, A, A, 2, A, 4, 4, 2, 1, 64, None, 0,
+                                          scale, A, A, 1 << 30) == EARG
 
 
 def test_cache_without_heads_is_refused(mx):
@@ -51,7 +51,8 @@ def test_heads_that_attention_does_not_take(mx, dim):
     cache = mx.MXCache.allocate(0, 2, 1, 16, dim, device="cpu")
     i32 = torch.int32
     with pytest.raises(ValueError, match="64, 96, 128, 192, 256"):
-        mx.mx_cache_attention(cache, bf(2, 1, dim), ints(3, dtype=i32), ints(2, dtype=i32), ints(2, 2, dtype=i32), 1, 20)
+        mx.mx_cache_attention(cache, bf(2, 1, dim), ints(3, dtype=i32), ints(2, dtype=i32), ints(2, 2, dtype=i32),
+                              max_q=1, max_kv=20)
 
 
 def test_stream_without_the_private_call(b, monkeypatch):
