@@ -352,6 +352,7 @@ MX_API int mx_cache_read(const mx_cache *cache, const int64_t *slots,
  *              less, a sequence's queries from max_q on are not computed (what
  *              their rows hold is undefined), and its tokens from max_kv on
  *              count as not seen; so do tokens behind the pages of table_pages.
+ *              batch * q_heads * max_q is 2^32 at most (MX_ESHAPE).
  *   workspace  mx_cache_attention_workspace bytes, 16-byte aligned, contents
  *              free; it may be NULL where that is 0.
  * dim is 64, 96, 128, 192 or 256 and scale is positive, and finite also times
