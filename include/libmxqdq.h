@@ -40,7 +40,7 @@
  * Ownership and execution: every pointer is device memory owned by the
  * caller.  The library allocates nothing, frees nothing and never
  * synchronizes; every call validates its arguments on the host, enqueues one
- * kernel (mx_cache_attention: one or two) on the calling thread's stream
+ * kernel (attention, verification and pages: up to three) on the calling thread's stream
  * (mx_set_stream) and returns.  Calls
  * are therefore safe to capture in a HIP graph.  dst == src (an exact alias)
  * is allowed for mx_qdq; any other overlap between inputs and outputs is
@@ -94,8 +94,8 @@ extern "C" {
 #define MX_ELAUNCH (-7) /* the kernel launch failed (hipGetLastError)       */
 #define MX_ELAYOUT (-8) /* scale_layout is not one of MX_SCALES_*, or a
                            rotary layout not one of MX_ROTARY_*             */
-#define MX_EARG (-9)    /* a rotary, cache or attention argument is outside
-                           the range stated at its call                     */
+#define MX_EARG (-9)    /* a rotary, cache, attention or verification argument
+                           is outside the range stated at its call          */
 
 /* Scale layouts. */
 #define MX_SCALES_ROWMAJOR 0 /* [M x K/32] bytes, row-major, unpadded      */
@@ -282,6 +282,24 @@ MX_API int mx_rope(const void *src, int64_t src_token_stride,
                    int64_t dst_token_stride, int64_t dst_head_stride);
 
 /*
+ * mx_rope with several positions a token (time, height and width of an image
+ * or video, say): pair p is turned by
+ *   positions[axes[p] * axis_stride + token] * inv_freq[p].
+ *   positions  [axis_count x tokens] int64, rows axis_stride elements apart.
+ *   axis_count 1 or more (MX_EARG).
+ *   axes       [rot/2] int32: the axis of each pair, in any order; the angle of
+ *              a pair whose axis is outside 0 .. axis_count - 1 is zero.
+ */
+MX_API int mx_rope_axes(const void *src, int64_t src_token_stride,
+                        int64_t src_head_stride, int dtype, int64_t tokens,
+                        int64_t heads, int64_t dim, const int64_t *positions,
+                        int64_t axis_stride, int64_t axis_count,
+                        const int32_t *axes, const double *inv_freq,
+                        int64_t rot, int layout, double scale, int inverse,
+                        void *dst, int64_t dst_token_stride,
+                        int64_t dst_head_stride);
+
+/*
  * Paged MX cache of keys and values.  A plain description: the caller owns
  * the memory and may keep the struct where it likes (it is read during the
  * call only).
@@ -316,6 +334,16 @@ MX_API int mx_cache_write(const mx_cache *cache, const void *k,
                           int64_t tokens, const int64_t *positions,
                           const double *inv_freq, int64_t rot, int layout,
                           double scale);
+
+/* mx_cache_write with several positions a token, as for mx_rope_axes. */
+MX_API int mx_cache_write_axes(const mx_cache *cache, const void *k,
+                               int64_t k_token_stride, int64_t k_head_stride,
+                               const void *v, int64_t v_token_stride,
+                               int64_t v_head_stride, const int64_t *slots,
+                               int64_t tokens, const int64_t *positions,
+                               int64_t axis_stride, int64_t axis_count,
+                               const int32_t *axes, const double *inv_freq,
+                               int64_t rot, int layout, double scale);
 
 /*
  * Read slots back: k, v [tokens x heads x dim] bf16, contiguous, 16-byte
@@ -377,6 +405,127 @@ MX_API int mx_cache_attention(const mx_cache *cache, const void *q,
                               const int64_t *tree, int64_t tree_words,
                               float scale, void *out, void *workspace,
                               int64_t workspace_bytes);
+
+/*
+ * Attention to another sequence's tokens (an encoder's states, the tokens of
+ * images): as mx_cache_attention, but every query of sequence b sees all of its
+ * kv_lens[b] tokens, whatever the number of its queries.  The workspace is that
+ * of mx_cache_attention_workspace.
+ */
+MX_API int mx_cache_cross_attention(const mx_cache *cache, const void *q,
+                                    int64_t q_token_stride,
+                                    int64_t q_head_stride, int64_t q_heads,
+                                    const int32_t *q_starts,
+                                    const int32_t *kv_lens, int64_t batch,
+                                    const int32_t *block_table,
+                                    int64_t table_stride, int64_t table_pages,
+                                    int64_t total_q, int64_t max_q,
+                                    int64_t max_kv, float scale, void *out,
+                                    void *workspace, int64_t workspace_bytes);
+
+/*
+ * The cache's pages.  block_table is [rows x table_stride] int32, of which the
+ * first table_pages of a row are used; an entry outside 0 .. pages - 1 is no
+ * page.  refs [cache->pages] int32 counts the rows that hold each page; a page
+ * is free where it is zero (one that is never to be handed out has another
+ * value there).  Free pages are handed out lowest first, in the order of rows
+ * and columns, so that the same tables give the same pages.  The calls change
+ * refs without a lock: those that share it follow one another on a stream.
+ */
+
+/*
+ * Copy whole pages, keys and values: page src[i] to page dst[i], i < count
+ * (int32; count up to 2^24 - 1, MX_ESHAPE).  Pairs with a page outside the cache
+ * are skipped.  The pages of dst are distinct and no other pair's source; the
+ * bytes of one that is are undefined.
+ */
+MX_API int mx_cache_copy(const mx_cache *cache, const int32_t *src,
+                         const int32_t *dst, int64_t count);
+
+/*
+ * Row r of block_table holds the pages for kv_lens[r] tokens and no more:
+ * pages behind them are released first, in all rows, and their entries become
+ * -1; then entries without a page get free ones.  missing [rows] int32: the
+ * pages that a row needs and did not get, because none was free or the row is
+ * too short.  rows up to 2^24 (MX_ESHAPE).
+ */
+MX_API int mx_cache_resize(const mx_cache *cache, int32_t *refs,
+                           int32_t *block_table, int64_t table_stride,
+                           int64_t table_pages, const int32_t *kv_lens,
+                           int64_t rows, int32_t *missing);
+
+/*
+ * Rows for sequences that go on from others: row c of child_table (columns and
+ * meaning as block_table, no overlap with it) gets the full pages of row
+ * parents[c], which both hold from then on, and, where the last page is not
+ * full, a free page into which that page's tokens are copied (rows behind them
+ * keep what they held).  The rest of the row is -1; so is all of it for a parent
+ * outside 0 .. rows - 1.  missing [children] int32: the pages that a child needs
+ * and does not hold.  children * cache->heads is below 2^23 (MX_ESHAPE).
+ */
+MX_API int mx_cache_fork(const mx_cache *cache, int32_t *refs,
+                         const int32_t *block_table, int64_t table_stride,
+                         int64_t table_pages, const int32_t *kv_lens,
+                         int64_t rows, const int32_t *parents,
+                         int64_t children, int32_t *child_table,
+                         int64_t child_stride, int32_t *missing);
+
+/*
+ * Move the tokens that are kept of each sequence together, in place: place
+ * kv_starts[b] + i gets what place kv_starts[b] + keep[b * keep_stride + i] held
+ * before the call, for 0 <= i < min(counts[b], max_keep), where keep >= i (other
+ * entries, and places without a page of the cache, are skipped).  A page that is
+ * changed is held by one sequence of the batch.  kv_lens [batch] int32, not one
+ * of the inputs, gets kv_starts + the count.  batch * cache->heads is below 2^20
+ * (MX_ESHAPE).
+ */
+MX_API int mx_cache_compact(const mx_cache *cache, const int32_t *kv_starts,
+                            const int32_t *keep, int64_t keep_stride,
+                            int64_t max_keep, const int32_t *counts,
+                            const int32_t *block_table, int64_t table_stride,
+                            int64_t table_pages, int64_t batch,
+                            int32_t *kv_lens);
+
+/*
+ * Verification of drafted tokens: what is kept of them, and the token sampled
+ * after it, are distributed as the target's own.  Sequence b has the nodes
+ * q_starts[b] .. q_starts[b+1] - 1 (int32 [batch + 1], ascending from 0): node 0
+ * is its last settled token, the others are drafted, each a child of a node
+ * before it.  From node c = 0 on, with w = target[c] and W = 1, the children of
+ * c are asked in their order:
+ *   child i with token x is kept if uniforms[i] * W * q(x) < w(x), then c = i;
+ *   if not, w = max(w - W q, 0) and W = sum w, unless that would be zero
+ * (q: draft[c], or 1 for x and 0 for all others if draft == NULL).  Behind the
+ * last kept node a token is sampled from w: the first whose cumulative sum is
+ * above uniforms[node 0] * sum w.  Computed in fp64; probabilities that are
+ * negative or not finite count as zero; nodes with tokens outside the vocabulary
+ * are passed over.
+ *   target, draft  [total_q x vocab] in dtype, strides in elements: row c holds
+ *              the probabilities after node c, and those that its children were
+ *              drawn from.  vocab 1 to 2^30 (MX_ESHAPE).
+ *   tokens     [total_q] int64; uniforms [total_q] fp64 in [0, 1).
+ *   parents    [total_q] int32: a node's parent by its place in the sequence
+ *              (nodes whose parent is not before them are passed over), or NULL:
+ *              each node follows the one before.
+ *   max_q      at least the most nodes of a sequence, 1024 at most (MX_ESHAPE);
+ *              nodes from max_q on are passed over.
+ *   counts     [batch] int32: nodes that stay, node 0 among them (0 for a
+ *              sequence without nodes).
+ *   path       [batch x max_q] int32: their places in the sequence, then -1.
+ *   out        [batch x max_q] int64: the kept tokens and the sampled one, then
+ *              -1; the sampled one is -1 if its row has no weight.
+ *   workspace  mx_verify_workspace bytes, 16-byte aligned, contents free; it may
+ *              be NULL where that is 0.
+ */
+MX_API int64_t mx_verify_workspace(int64_t batch, int64_t total_q,
+                                   int64_t max_q, int64_t vocab);
+MX_API int mx_verify(const void *target, int64_t target_stride,
+                     const void *draft, int64_t draft_stride, int dtype,
+                     int64_t vocab, const int64_t *tokens,
+                     const double *uniforms, const int32_t *q_starts,
+                     const int32_t *parents, int64_t batch, int64_t total_q,
+                     int64_t max_q, int32_t *counts, int32_t *path,
+                     int64_t *out, void *workspace, int64_t workspace_bytes);
 
 /* Stream used by the calling thread's subsequent calls (a hipStream_t;
  * NULL = the default stream).  The setting is thread-local. */

@@ -57,6 +57,20 @@ _lib.mx_cache_attention_workspace.argtypes = [_vp, _i64, _i64, _i64, _i64, _i64]
 _lib.mx_cache_attention_workspace.restype = _i64
 _lib.mx_cache_attention.argtypes = [_vp, _vp, _i64, _i64, _i64, _vp, _vp, _i64, _vp, _i64, _i64, _i64, _i64, _i64, _vp,
                                     _i64, ctypes.c_float, _vp, _vp, _i64]
+_lib.mx_rope_axes.argtypes = [_vp, _i64, _i64, _int, _i64, _i64, _i64, _vp, _i64, _i64, _vp, _vp, _i64, _int, _dbl, _int,
+                              _vp, _i64, _i64]
+_lib.mx_cache_write_axes.argtypes = [_vp, _vp, _i64, _i64, _vp, _i64, _i64, _vp, _i64, _vp, _i64, _i64, _vp, _vp, _i64,
+                                     _int, _dbl]
+_lib.mx_cache_cross_attention.argtypes = [_vp, _vp, _i64, _i64, _i64, _vp, _vp, _i64, _vp, _i64, _i64, _i64, _i64, _i64,
+                                          ctypes.c_float, _vp, _vp, _i64]
+_lib.mx_cache_copy.argtypes = [_vp, _vp, _vp, _i64]
+_lib.mx_cache_fork.argtypes = [_vp, _vp, _vp, _i64, _i64, _vp, _i64, _vp, _i64, _vp, _i64, _vp]
+_lib.mx_cache_resize.argtypes = [_vp, _vp, _vp, _i64, _i64, _vp, _i64, _vp]
+_lib.mx_cache_compact.argtypes = [_vp, _vp, _vp, _i64, _i64, _vp, _vp, _i64, _i64, _i64, _vp]
+_lib.mx_verify_workspace.argtypes = [_i64, _i64, _i64, _i64]
+_lib.mx_verify_workspace.restype = _i64
+_lib.mx_verify.argtypes = [_vp, _i64, _vp, _i64, _int, _i64, _vp, _vp, _vp, _vp, _i64, _i64, _i64, _vp, _vp, _vp, _vp,
+                           _i64]
 _lib.mx_set_stream.argtypes = [_vp]
 _lib.mx_set_stream.restype = None
 _lib.mx_get_stream.restype = _vp
@@ -65,7 +79,8 @@ _lib.mx_status_string.restype = ctypes.c_char_p
 for _f in (_lib.mx_qdq, _lib.mx_quantize, _lib.mx_dequantize, _lib.mx_rotate, _lib.mx_matmul,
            _lib.mx_scales_to_blocked, _lib.mx_quantize_blocked, _lib.mx_nvfp4_quantize, _lib.mx_nvfp4_qdq,
            _lib.mx_nvfp4_dequantize, _lib.mx_rope, _lib.mx_cache_write, _lib.mx_cache_read,
-           _lib.mx_cache_attention):
+           _lib.mx_cache_attention, _lib.mx_rope_axes, _lib.mx_cache_write_axes, _lib.mx_cache_cross_attention,
+           _lib.mx_cache_copy, _lib.mx_cache_fork, _lib.mx_cache_resize, _lib.mx_cache_compact, _lib.mx_verify):
     _f.restype = _int
 
 
@@ -404,13 +419,24 @@ def _vector(t, name: str, dtype: torch.dtype, n: int) -> int:
     return t.data_ptr()
 
 
-def _rotary(positions, inv_freq, tokens: int):
-    """Pointers of the positions and frequencies, and the number of rotated dimensions."""
+def _rotary(positions, inv_freq, tokens: int, axes=None):
+    """What a call takes for the positions (with axes: their pointer, stride and number, and the pairs' axes), the
+    pointer of the frequencies, and the number of rotated dimensions."""
     if not isinstance(inv_freq, torch.Tensor) or inv_freq.dtype != torch.float64 or inv_freq.dim() != 1:
         raise ValueError("inv_freq must be a one-dimensional float64 tensor (angle per position of each pair)")
     pairs = inv_freq.shape[0]
-    return (_vector(positions, "positions", torch.int64, tokens), _vector(inv_freq, "inv_freq", torch.float64, pairs),
-            2 * pairs)
+    if axes is None:
+        at = (_vector(positions, "positions", torch.int64, tokens),)
+    else:
+        if not isinstance(positions, torch.Tensor) or positions.dtype != torch.int64 or positions.dim() != 2 \
+                or positions.shape[0] < 1 or positions.shape[1] != tokens \
+                or (tokens > 1 and positions.stride(1) != 1):
+            raise ValueError(f"with axes, positions must be an int64 tensor [axes, {tokens}] with contiguous rows")
+        _place(positions, "positions")
+        count = positions.shape[0]
+        at = (positions.data_ptr(), positions.stride(0) if count > 1 else 0, count,
+              _vector(axes, "axes", torch.int32, pairs))
+    return at, _vector(inv_freq, "inv_freq", torch.float64, pairs), 2 * pairs
 
 
 def _like(t: torch.Tensor) -> torch.Tensor:
@@ -418,27 +444,30 @@ def _like(t: torch.Tensor) -> torch.Tensor:
 
 
 def mx_rope(x: torch.Tensor, positions: torch.Tensor, inv_freq: torch.Tensor, layout: int = HALF, scale: float = 1.0,
-            inverse: bool = False, dst: torch.Tensor | None = None) -> torch.Tensor:
+            inverse: bool = False, dst: torch.Tensor | None = None, axes: torch.Tensor | None = None) -> torch.Tensor:
     """Rotary positions on the first 2 * len(inv_freq) dimensions of x [tokens, heads, dim] (bf16 or fp32, any token
     and head strides), the others copied.
 
-    positions int64 [tokens]; inv_freq float64 [pairs]; layout HALF (dimension p with p + pairs) or INTERLEAVED
+    positions int64 [tokens], or with axes [number of axes, tokens] (time, height and width, say): axes int32 [pairs]
+    names the axis whose position turns each pair (a pair of an axis that there is not is not turned).
+    inv_freq float64 [pairs]; layout HALF (dimension p with p + pairs) or INTERLEAVED
     (2p with 2p + 1); scale multiplies the rotated dimensions.  inverse: the transposed rotation, which takes the
     gradient of the output to that of x.  dst may be x itself.  Without dst the call is recorded for autograd if x
     requires a gradient (inv_freq gets none); with dst nothing is recorded."""
     ps, st, sh = _heads(x, "x", (torch.bfloat16, torch.float32))
     if x.requires_grad and dst is None and torch.is_grad_enabled():
-        return _Rope.apply(x, positions, inv_freq, layout, scale, inverse)
+        return _Rope.apply(x, positions, inv_freq, layout, scale, inverse, axes)
     tokens, heads, dim = x.shape
     if dst is None:  # what is allocated here needs no check
         dst = _like(x)
         pd, dt, dh = dst.data_ptr(), heads * dim, dim
     else:
         pd, dt, dh = _heads(dst, "dst", (x.dtype,), x.shape)
-    pp, pf, rot = _rotary(positions, inv_freq, tokens)
+    at, pf, rot = _rotary(positions, inv_freq, tokens, axes)
     _stream()
-    _call(_lib.mx_rope(ps, st, sh, _DTYPE[x.dtype], tokens, heads, dim, pp, pf, rot, layout, scale,
-                       1 if inverse else 0, pd, dt, dh))
+    call = _lib.mx_rope if axes is None else _lib.mx_rope_axes
+    _call(call(ps, st, sh, _DTYPE[x.dtype], tokens, heads, dim, *at, pf, rot, layout, scale, 1 if inverse else 0, pd, dt,
+               dh))
     return dst
 
 
@@ -446,17 +475,18 @@ class _Rope(torch.autograd.Function):
     """mx_rope with its gradient, the transposed rotation of that of the output (and the other way round)."""
 
     @staticmethod
-    def forward(ctx, x, positions, inv_freq, layout, scale, inverse):
-        ctx.save_for_backward(positions, inv_freq)
+    def forward(ctx, x, positions, inv_freq, layout, scale, inverse, axes):
+        ctx.save_for_backward(positions, inv_freq, axes)
         ctx.rotation = layout, scale, inverse
-        return mx_rope(x, positions, inv_freq, layout, scale, inverse)
+        return mx_rope(x, positions, inv_freq, layout, scale, inverse, axes=axes)
 
     @staticmethod
     def backward(ctx, grad):
         layout, scale, inverse = ctx.rotation
         if grad.stride(2) != 1:  # that of a sum, say, is one value for all
             grad = grad.contiguous()
-        return mx_rope(grad, *ctx.saved_tensors, layout, scale, not inverse), None, None, None, None, None
+        positions, inv_freq, axes = ctx.saved_tensors
+        return (mx_rope(grad, positions, inv_freq, layout, scale, not inverse, axes=axes),) + (None,) * 6
 
 
 class _CacheStruct(ctypes.Structure):
@@ -519,10 +549,10 @@ def _cache(cache) -> int:
 
 def mx_cache_write(cache: MXCache, k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor,
                    positions: torch.Tensor | None = None, inv_freq: torch.Tensor | None = None, layout: int = HALF,
-                   scale: float = 1.0) -> None:
+                   scale: float = 1.0, axes: torch.Tensor | None = None) -> None:
     """Quantise keys and values [tokens, heads, dim] (bf16, any token and head strides) into the cache's slots
-    (int64 [tokens]; slots outside the cache are skipped).  With positions and inv_freq the keys are rotated first, as
-    by mx_rope, and rounded to bf16."""
+    (int64 [tokens]; slots outside the cache are skipped).  With positions and inv_freq (and axes) the keys are rotated
+    first, as by mx_rope, and rounded to bf16."""
     pc = _cache(cache)
     pk, kt, kh = _heads(k, "k", (torch.bfloat16,))
     shape = (k.shape[0], cache.heads, cache.dim)
@@ -532,9 +562,12 @@ def mx_cache_write(cache: MXCache, k: torch.Tensor, v: torch.Tensor, slots: torc
     ps = _vector(slots, "slots", torch.int64, shape[0])
     if (positions is None) != (inv_freq is None):
         raise ValueError("positions and inv_freq go together")
-    pp, pf, rot = (None, None, 0) if positions is None else _rotary(positions, inv_freq, shape[0])
+    if positions is None and axes is not None:
+        raise ValueError("axes need positions")
+    at, pf, rot = ((None,), None, 0) if positions is None else _rotary(positions, inv_freq, shape[0], axes)
     _stream()
-    _call(_lib.mx_cache_write(pc, pk, kt, kh, pv, vt, vh, ps, shape[0], pp, pf, rot, layout, scale))
+    call = _lib.mx_cache_write if axes is None else _lib.mx_cache_write_axes
+    _call(call(pc, pk, kt, kh, pv, vt, vh, ps, shape[0], *at, pf, rot, layout, scale))
 
 
 def mx_cache_read(cache: MXCache, slots: torch.Tensor, k: torch.Tensor | None = None, v: torch.Tensor | None = None):
@@ -572,6 +605,29 @@ def mx_cache_attention(cache: MXCache, q: torch.Tensor, q_starts: torch.Tensor, 
     max_q, max_kv: at least the most queries and tokens of a sequence (with less, the rows of queries from max_q on are
     undefined and tokens from max_kv on are not seen).
     scale: dim ** -0.5 if not given."""
+    return _attend(cache, q, q_starts, kv_lens, block_table, max_q, max_kv, tree, False, scale, out)
+
+
+def mx_cache_cross_attention(cache: MXCache, q: torch.Tensor, q_starts: torch.Tensor, kv_lens: torch.Tensor,
+                             block_table: torch.Tensor, max_q: int, max_kv: int, scale: float | None = None,
+                             out: torch.Tensor | None = None) -> torch.Tensor:
+    """Attention to another sequence's tokens in the cache (an encoder's states, the tokens of images): as
+    mx_cache_attention, but every query of sequence b sees all of its kv_lens[b] tokens, whatever the number of
+    queries."""
+    return _attend(cache, q, q_starts, kv_lens, block_table, max_q, max_kv, None, True, scale, out)
+
+
+def _table(table, name: str, rows: int):
+    """t must be int32 [rows, pages] with contiguous rows.  Its pointer, row stride and pages of a row."""
+    if not isinstance(table, torch.Tensor) or table.dtype != torch.int32 or table.dim() != 2 \
+            or table.shape[0] != rows or (table.shape[1] > 1 and table.stride(1) != 1):
+        raise ValueError(f"{name} must be an int32 tensor [{rows}, pages] with contiguous rows")
+    _place(table, name)
+    pages = table.shape[1]
+    return table.data_ptr(), table.stride(0) if rows > 1 else pages, pages
+
+
+def _attend(cache, q, q_starts, kv_lens, block_table, max_q, max_kv, tree, everything, scale, out):
     pc = _cache(cache)
     pq, qt, qh = _heads(q, "q", (torch.bfloat16,))
     total, heads, dim = q.shape
@@ -585,12 +641,7 @@ def mx_cache_attention(cache: MXCache, q: torch.Tensor, q_starts: torch.Tensor, 
     batch = kv_lens.shape[0]
     pl = _vector(kv_lens, "kv_lens", torch.int32, batch)
     pst = _vector(q_starts, "q_starts", torch.int32, batch + 1)
-    if not isinstance(block_table, torch.Tensor) or block_table.dtype != torch.int32 or block_table.dim() != 2 \
-            or block_table.shape[0] != batch or (block_table.shape[1] > 1 and block_table.stride(1) != 1):
-        raise ValueError("block_table must be an int32 tensor [batch, pages] with contiguous rows")
-    _place(block_table, "block_table")
-    pages = block_table.shape[1]
-    stride = block_table.stride(0) if batch > 1 else pages
+    pb, stride, pages = _table(block_table, "block_table", batch)
     pt, words = None, 0
     if tree is not None:
         if not isinstance(tree, torch.Tensor) or tree.dim() != 2:
@@ -611,10 +662,164 @@ def mx_cache_attention(cache: MXCache, q: torch.Tensor, q_starts: torch.Tensor, 
         raise MXError(need)
     space = kv_lens.new_empty(need // 4) if need else None  # int32: 4 bytes each
     _stream()
-    _call(_lib.mx_cache_attention(pc, pq, qt, qh, heads, pst, pl, batch, block_table.data_ptr(), stride, pages, total,
-                                  max_q, max_kv, pt, words, dim ** -0.5 if scale is None else scale, po,
-                                  space.data_ptr() if need else None, need))
+    scale = dim ** -0.5 if scale is None else scale
+    ps = space.data_ptr() if need else None
+    if everything:
+        _call(_lib.mx_cache_cross_attention(pc, pq, qt, qh, heads, pst, pl, batch, pb, stride, pages, total, max_q, max_kv,
+                                            scale, po, ps, need))
+    else:
+        _call(_lib.mx_cache_attention(pc, pq, qt, qh, heads, pst, pl, batch, pb, stride, pages, total, max_q, max_kv, pt,
+                                      words, scale, po, ps, need))
     return out
+
+
+# ---- the cache's pages ---------------------------------------------------------
+
+
+def _rows(t, name: str) -> int:
+    """Length of a one-dimensional tensor."""
+    if not isinstance(t, torch.Tensor) or t.dim() != 1:
+        raise ValueError(f"{name} must be a one-dimensional int32 tensor")
+    return t.shape[0]
+
+
+def mx_cache_copy(cache: MXCache, src: torch.Tensor, dst: torch.Tensor) -> None:
+    """Copy whole pages, keys and values, from src to dst (int32 page numbers [pages]).  A page may be the source of
+    several; those of dst are distinct and no sources (the bytes of one that is are not defined).  Pairs with a page
+    outside the cache are skipped."""
+    pc = _cache(cache)
+    n = _rows(src, "src")
+    ps, pd = _vector(src, "src", torch.int32, n), _vector(dst, "dst", torch.int32, n)
+    _stream()
+    _call(_lib.mx_cache_copy(pc, ps, pd, n))
+
+
+def mx_cache_resize(cache: MXCache, refs: torch.Tensor, block_table: torch.Tensor, kv_lens: torch.Tensor) -> torch.Tensor:
+    """Let row b of block_table (int32 [rows, pages], changed in place) hold the pages for kv_lens[b] tokens (int32
+    [rows]) and no more: first those behind them are released, in all rows, and their entries become -1; then entries
+    that hold no page (outside the cache, -1 say) get free ones, the lowest first, in the order of rows and columns.
+
+    refs int32 [pages of the cache], changed in place: how many rows hold each page; it is free at 0.  Start with zeros
+    and a table of -1; a length of 0 frees a row.  Returns int32 [rows], the number of pages that each row needs and did
+    not get, because none was free or the table has no column for them."""
+    pc = _cache(cache)
+    rows = _rows(kv_lens, "kv_lens")
+    pl = _vector(kv_lens, "kv_lens", torch.int32, rows)
+    pr = _vector(refs, "refs", torch.int32, cache.pages)
+    pt, stride, pages = _table(block_table, "block_table", rows)
+    missing = torch.empty_like(kv_lens)
+    _stream()
+    _call(_lib.mx_cache_resize(pc, pr, pt, stride, pages, pl, rows, missing.data_ptr()))
+    return missing
+
+
+def mx_cache_fork(cache: MXCache, refs: torch.Tensor, block_table: torch.Tensor, kv_lens: torch.Tensor,
+                  parents: torch.Tensor, out: torch.Tensor | None = None):
+    """Rows for sequences that go on from others: child c has the tokens of row parents[c] (int32 [children]) of
+    block_table, whose kv_lens (int32 [rows]) say how many.  Full pages are shared (refs, as for mx_cache_resize, counts
+    the child too); the tokens of a last page that is not full are copied into a free page, so that both may go on
+    writing.  The parents' rows keep what they hold.
+
+    Returns the children's rows (int32 [children, pages], -1 where there is none; out if given, which is not
+    block_table) and int32 [children], the pages that each child needs and does not hold.  A parent that there is not
+    gives an empty row."""
+    pc = _cache(cache)
+    rows, children = _rows(kv_lens, "kv_lens"), _rows(parents, "parents")
+    pl, pp = _vector(kv_lens, "kv_lens", torch.int32, rows), _vector(parents, "parents", torch.int32, children)
+    pr = _vector(refs, "refs", torch.int32, cache.pages)
+    pt, stride, pages = _table(block_table, "block_table", rows)
+    if out is None:
+        out = block_table.new_empty((children, pages))
+    po, out_stride, out_pages = _table(out, "out", children)
+    if out_pages != pages:
+        raise ValueError(f"out must have the {pages} columns of block_table, got {out_pages}")
+    if rows and children and pages and po < pt + 4 * ((rows - 1) * stride + pages) \
+            and pt < po + 4 * ((children - 1) * out_stride + pages):
+        raise ValueError("out must not overlap block_table")
+    missing = torch.empty_like(parents)
+    _stream()
+    _call(_lib.mx_cache_fork(pc, pr, pt, stride, pages, pl, rows, pp, children, po, out_stride, missing.data_ptr()))
+    return out, missing
+
+
+def mx_cache_compact(cache: MXCache, kv_starts: torch.Tensor, keep: torch.Tensor, counts: torch.Tensor,
+                     block_table: torch.Tensor) -> torch.Tensor:
+    """Move the tokens that are kept of each sequence together, in place: place kv_starts[b] + i gets what place
+    kv_starts[b] + keep[b, i] held before the call, for i below counts[b].
+
+    kv_starts, counts int32 [batch]; keep int32 [batch, most], rows contiguous, with keep[b, i] >= i (others are
+    skipped), as a row in ascending order has it; block_table int32 [batch, pages].  Places without a page of the cache
+    are skipped.  The pages that are changed are held by one sequence only.  Returns the new lengths, kv_starts +
+    counts, int32 [batch].  The path and counts of mx_verify are such a list."""
+    pc = _cache(cache)
+    batch = _rows(kv_starts, "kv_starts")
+    ps, pn = _vector(kv_starts, "kv_starts", torch.int32, batch), _vector(counts, "counts", torch.int32, batch)
+    pk, keep_stride, most = _table(keep, "keep", batch)
+    pt, stride, pages = _table(block_table, "block_table", batch)
+    lens = torch.empty_like(kv_starts)
+    _stream()
+    _call(_lib.mx_cache_compact(pc, ps, pk, keep_stride, most, pn, pt, stride, pages, batch, lens.data_ptr()))
+    return lens
+
+
+# ---- verification of drafted tokens ------------------------------------------------
+
+
+def _probabilities(t, name: str, dtypes, shape=None):
+    """t must be [nodes, vocabulary] with contiguous rows.  Its pointer and row stride."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch tensor")
+    if t.dtype not in dtypes:
+        raise ValueError(f"{name} must be {' or '.join(str(d) for d in dtypes)}, got {t.dtype}")
+    if t.dim() != 2 or (shape is not None and t.shape != shape):
+        raise ValueError(f"{name} must have shape {'[nodes, vocabulary]' if shape is None else tuple(shape)}, got "
+                         f"{tuple(t.shape)}")
+    if t.shape[1] > 1 and t.stride(1) != 1:
+        raise ValueError(f"the rows of {name} must be contiguous")
+    _place(t, name)
+    return t.data_ptr(), t.stride(0) if t.shape[0] > 1 else 0
+
+
+def mx_verify(target: torch.Tensor, tokens: torch.Tensor, uniforms: torch.Tensor, q_starts: torch.Tensor, max_q: int,
+              draft: torch.Tensor | None = None, parents: torch.Tensor | None = None):
+    """Keep or refuse drafted tokens so that what comes out is distributed as the target's own tokens.
+
+    Sequence b has the nodes q_starts[b] .. q_starts[b + 1] (int32 [batch + 1]): the first is its last settled token, the
+    others are drafted (up to 1024 nodes in all).  tokens int64 [nodes] (the first one's is not read); target [nodes,
+    vocabulary] (bf16 or fp32, any row stride): the target's probabilities after each node; draft, the same: the
+    distribution that the children of each node were drawn from, one by one; without it they count as certain.
+    parents int32 [nodes]: each node's parent as its place in the sequence, below its own; without it each follows the
+    one before (a chain).  uniforms float64 [nodes], in [0, 1): of a drafted node for its own test, of the first one for
+    the token that is sampled.
+
+    From the first node on, the children of a node are asked in their order, with w the node's row of target and W = 1:
+    token x is kept if uniform * W * draft(x) < w(x), and its children are asked next; if not, w = max(w - W * draft, 0)
+    and W = sum(w), unless nothing would be left.  After the last kept node a token is sampled from w: the first whose
+    cumulative sum is above uniform * sum(w).  (fp64; negative and not finite probabilities count as zero; drafted tokens
+    outside the vocabulary are passed over.)
+
+    Returns counts int32 [batch], the nodes that stay (the first one and the kept ones); path int32 [batch, max_q], their
+    places, then -1; and int64 [batch, max_q], the kept tokens and the sampled one, then -1 (the sampled one is -1 too
+    where the row has no weight).  max_q: the most nodes of a sequence; those from max_q on are passed over."""
+    pt, ts = _probabilities(target, "target", (torch.bfloat16, torch.float32))
+    nodes, vocab = target.shape
+    pd, ds = (None, 0) if draft is None else _probabilities(draft, "draft", (target.dtype,), target.shape)
+    px, pu = _vector(tokens, "tokens", torch.int64, nodes), _vector(uniforms, "uniforms", torch.float64, nodes)
+    batch = _rows(q_starts, "q_starts") - 1
+    if batch < 0:
+        raise ValueError("q_starts must be an int32 tensor [batch + 1]")
+    pq = _vector(q_starts, "q_starts", torch.int32, batch + 1)
+    pp = None if parents is None else _vector(parents, "parents", torch.int32, nodes)
+    need = _lib.mx_verify_workspace(batch, nodes, max_q, vocab)
+    if need < 0:
+        raise MXError(need)
+    counts, path = q_starts.new_empty(batch), q_starts.new_empty((batch, max_q))
+    out = tokens.new_empty((batch, max_q))
+    space = uniforms.new_empty(need // 8) if need else None  # float64: 8 bytes each
+    _stream()
+    _call(_lib.mx_verify(pt, ts, pd, ds, _DTYPE[target.dtype], vocab, px, pu, pq, pp, batch, nodes, max_q,
+                         counts.data_ptr(), path.data_ptr(), out.data_ptr(), space.data_ptr() if need else None, need))
+    return counts, path, out
 
 
 def raw():

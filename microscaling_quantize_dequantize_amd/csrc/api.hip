@@ -264,10 +264,12 @@ int check_attention(const mx_cache *c, int64_t q_heads, int64_t batch, int64_t t
 
 }  // namespace
 
-MX_API int mx_rope(const void *src, int64_t src_token_stride, int64_t src_head_stride, int dtype, int64_t tokens,
-                   int64_t heads, int64_t dim, const int64_t *positions, const double *inv_freq, int64_t rot,
-                   int layout, double scale, int inverse, void *dst, int64_t dst_token_stride,
-                   int64_t dst_head_stride) {
+namespace {
+
+int rope(const void *src, int64_t src_token_stride, int64_t src_head_stride, int dtype, int64_t tokens, int64_t heads,
+         int64_t dim, const mx::Positions &at, const double *inv_freq, int64_t rot, int layout, double scale, int inverse,
+         void *dst, int64_t dst_token_stride, int64_t dst_head_stride) {
+  const int64_t *positions = at.at;
   int st;
   if ((st = check_dtype(dtype))) return st;
   if (tokens < 0 || !fits(heads, 65535) || !fits(dim, 4096) || tokens > INT32_MAX) return MX_ESHAPE;
@@ -283,14 +285,14 @@ MX_API int mx_rope(const void *src, int64_t src_token_stride, int64_t src_head_s
     if (rot == 0) return MX_OK;
   }
   const int64_t strides[4] = {src_token_stride, src_head_stride, dst_token_stride, dst_head_stride};
-  return launched(mx::launch_rope(dtype, src, dst, tokens, heads, dim, strides, positions, inv_freq, rot, layout, scale,
-                                  inverse, tl_stream));
+  return launched(mx::launch_rope(dtype, src, dst, tokens, heads, dim, strides, at, inv_freq, rot, layout, scale, inverse,
+                                  tl_stream));
 }
 
-MX_API int mx_cache_write(const mx_cache *cache, const void *k, int64_t k_token_stride, int64_t k_head_stride,
-                          const void *v, int64_t v_token_stride, int64_t v_head_stride, const int64_t *slots,
-                          int64_t tokens, const int64_t *positions, const double *inv_freq, int64_t rot, int layout,
-                          double scale) {
+int cache_write(const mx_cache *cache, const void *k, int64_t k_token_stride, int64_t k_head_stride, const void *v,
+                int64_t v_token_stride, int64_t v_head_stride, const int64_t *slots, int64_t tokens,
+                const mx::Positions &at, const double *inv_freq, int64_t rot, int layout, double scale) {
+  const int64_t *positions = at.at;
   int st;
   if ((st = check_cache(cache))) return st;
   if (!fits(tokens, mx::MAX_GROUPS_256 * mx::CACHE_WRITE_TILE)) return MX_ESHAPE;
@@ -299,8 +301,55 @@ MX_API int mx_cache_write(const mx_cache *cache, const void *k, int64_t k_token_
   if (empty_cache(cache) || !k || !v || !slots || (rot > 0 && (!positions || !inv_freq))) return MX_ENULL;
   if (!aligned(k, 2) || !aligned(v, 2) || !aligned(slots, 8)) return MX_EALIGN;
   const int64_t ks[2] = {k_token_stride, k_head_stride}, vs[2] = {v_token_stride, v_head_stride};
-  return launched(mx::launch_cache_write(view(cache), k, ks, v, vs, slots, tokens, positions, inv_freq, rot, layout,
-                                         scale, tl_stream));
+  return launched(mx::launch_cache_write(view(cache), k, ks, v, vs, slots, tokens, at, inv_freq, rot, layout, scale,
+                                         tl_stream));
+}
+
+// The axes of a call with several positions a token.
+int check_axes(const int32_t *axes, int64_t count, int64_t rot) {
+  if (count < 1 || count > INT32_MAX) return MX_EARG;
+  if (rot > 0 && !axes) return MX_ENULL;
+  return aligned(axes, 4) ? MX_OK : MX_EALIGN;
+}
+
+}  // namespace
+
+MX_API int mx_rope(const void *src, int64_t src_token_stride, int64_t src_head_stride, int dtype, int64_t tokens,
+                   int64_t heads, int64_t dim, const int64_t *positions, const double *inv_freq, int64_t rot,
+                   int layout, double scale, int inverse, void *dst, int64_t dst_token_stride,
+                   int64_t dst_head_stride) {
+  return rope(src, src_token_stride, src_head_stride, dtype, tokens, heads, dim,
+              mx::Positions{positions, nullptr, 0, 1}, inv_freq, rot, layout, scale, inverse, dst, dst_token_stride,
+              dst_head_stride);
+}
+
+MX_API int mx_rope_axes(const void *src, int64_t src_token_stride, int64_t src_head_stride, int dtype, int64_t tokens,
+                        int64_t heads, int64_t dim, const int64_t *positions, int64_t axis_stride, int64_t axis_count,
+                        const int32_t *axes, const double *inv_freq, int64_t rot, int layout, double scale, int inverse,
+                        void *dst, int64_t dst_token_stride, int64_t dst_head_stride) {
+  const int st = check_axes(axes, axis_count, rot);
+  if (st) return st;
+  return rope(src, src_token_stride, src_head_stride, dtype, tokens, heads, dim,
+              mx::Positions{positions, axes, axis_stride, (int)axis_count}, inv_freq, rot, layout, scale, inverse, dst,
+              dst_token_stride, dst_head_stride);
+}
+
+MX_API int mx_cache_write(const mx_cache *cache, const void *k, int64_t k_token_stride, int64_t k_head_stride,
+                          const void *v, int64_t v_token_stride, int64_t v_head_stride, const int64_t *slots,
+                          int64_t tokens, const int64_t *positions, const double *inv_freq, int64_t rot, int layout,
+                          double scale) {
+  return cache_write(cache, k, k_token_stride, k_head_stride, v, v_token_stride, v_head_stride, slots, tokens,
+                     mx::Positions{positions, nullptr, 0, 1}, inv_freq, rot, layout, scale);
+}
+
+MX_API int mx_cache_write_axes(const mx_cache *cache, const void *k, int64_t k_token_stride, int64_t k_head_stride,
+                               const void *v, int64_t v_token_stride, int64_t v_head_stride, const int64_t *slots,
+                               int64_t tokens, const int64_t *positions, int64_t axis_stride, int64_t axis_count,
+                               const int32_t *axes, const double *inv_freq, int64_t rot, int layout, double scale) {
+  const int st = check_axes(axes, axis_count, rot);
+  if (st) return st;
+  return cache_write(cache, k, k_token_stride, k_head_stride, v, v_token_stride, v_head_stride, slots, tokens,
+                     mx::Positions{positions, axes, axis_stride, (int)axis_count}, inv_freq, rot, layout, scale);
 }
 
 MX_API int mx_cache_read(const mx_cache *cache, const int64_t *slots, int64_t tokens, void *k, void *v) {
@@ -322,11 +371,13 @@ MX_API int64_t mx_cache_attention_workspace(const mx_cache *cache, int64_t q_hea
                                  total_q, max_q, max_kv);
 }
 
-MX_API int mx_cache_attention(const mx_cache *cache, const void *q, int64_t q_token_stride, int64_t q_head_stride,
-                              int64_t q_heads, const int32_t *q_starts, const int32_t *kv_lens, int64_t batch,
-                              const int32_t *block_table, int64_t table_stride, int64_t table_pages, int64_t total_q,
-                              int64_t max_q, int64_t max_kv, const int64_t *tree, int64_t tree_words, float scale,
-                              void *out, void *workspace, int64_t workspace_bytes) {
+namespace {
+
+int attention(const mx_cache *cache, const void *q, int64_t q_token_stride, int64_t q_head_stride, int64_t q_heads,
+              const int32_t *q_starts, const int32_t *kv_lens, int64_t batch, const int32_t *block_table,
+              int64_t table_stride, int64_t table_pages, int64_t total_q, int64_t max_q, int64_t max_kv,
+              const int64_t *tree, int64_t tree_words, bool all, float scale, void *out, void *workspace,
+              int64_t workspace_bytes) {
   int st;
   if ((st = check_attention(cache, q_heads, batch, total_q, max_q, max_kv))) return st;
   if (!fits(table_pages, INT32_MAX / cache->page) || table_stride < table_pages || !fits(tree_words, INT32_MAX))
@@ -352,8 +403,136 @@ MX_API int mx_cache_attention(const mx_cache *cache, const void *q, int64_t q_to
   const mx::AttentionArgs a{view(cache), (const unsigned short *)q, (unsigned short *)out, q_token_stride,
                             q_head_stride, q_starts, kv_lens, block_table, tree, table_stride, (float *)workspace,
                             (int)batch, group, (int)table_pages, (int)total_q, (int)max_q, (int)max_kv,
-                            (int)tree_words, scale};
+                            (int)tree_words, scale, all};
   return launched(mx::launch_cache_attention(a, tl_stream));
+}
+
+}  // namespace
+
+MX_API int mx_cache_attention(const mx_cache *cache, const void *q, int64_t q_token_stride, int64_t q_head_stride,
+                              int64_t q_heads, const int32_t *q_starts, const int32_t *kv_lens, int64_t batch,
+                              const int32_t *block_table, int64_t table_stride, int64_t table_pages, int64_t total_q,
+                              int64_t max_q, int64_t max_kv, const int64_t *tree, int64_t tree_words, float scale,
+                              void *out, void *workspace, int64_t workspace_bytes) {
+  return attention(cache, q, q_token_stride, q_head_stride, q_heads, q_starts, kv_lens, batch, block_table, table_stride,
+                   table_pages, total_q, max_q, max_kv, tree, tree_words, false, scale, out, workspace, workspace_bytes);
+}
+
+MX_API int mx_cache_cross_attention(const mx_cache *cache, const void *q, int64_t q_token_stride, int64_t q_head_stride,
+                                    int64_t q_heads, const int32_t *q_starts, const int32_t *kv_lens, int64_t batch,
+                                    const int32_t *block_table, int64_t table_stride, int64_t table_pages,
+                                    int64_t total_q, int64_t max_q, int64_t max_kv, float scale, void *out,
+                                    void *workspace, int64_t workspace_bytes) {
+  return attention(cache, q, q_token_stride, q_head_stride, q_heads, q_starts, kv_lens, batch, block_table, table_stride,
+                   table_pages, total_q, max_q, max_kv, nullptr, 0, true, scale, out, workspace, workspace_bytes);
+}
+
+namespace {
+
+// A table of pages and its rows' lengths.
+int check_table(const mx_cache *c, int64_t rows, int64_t table_stride, int64_t table_pages) {
+  const int st = check_cache(c);
+  if (st) return st;
+  if (!fits(rows, 1 << 24) || !fits(table_pages, INT32_MAX / c->page) || table_stride < table_pages) return MX_ESHAPE;
+  return MX_OK;
+}
+
+}  // namespace
+
+MX_API int mx_cache_resize(const mx_cache *cache, int32_t *refs, int32_t *block_table, int64_t table_stride,
+                           int64_t table_pages, const int32_t *kv_lens, int64_t rows, int32_t *missing) {
+  int st;
+  if ((st = check_table(cache, rows, table_stride, table_pages))) return st;
+  if (rows == 0) return MX_OK;
+  if (!kv_lens || !missing || (table_pages > 0 && !block_table) || (cache->pages > 0 && !refs)) return MX_ENULL;
+  if (!aligned(refs, 4) || !aligned(block_table, 4) || !aligned(kv_lens, 4) || !aligned(missing, 4)) return MX_EALIGN;
+  return launched(mx::launch_cache_resize(view(cache), refs, block_table, table_stride, (int)table_pages, kv_lens,
+                                          (int)rows, missing, tl_stream));
+}
+
+MX_API int mx_cache_fork(const mx_cache *cache, int32_t *refs, const int32_t *block_table, int64_t table_stride,
+                         int64_t table_pages, const int32_t *kv_lens, int64_t rows, const int32_t *parents,
+                         int64_t children, int32_t *child_table, int64_t child_stride, int32_t *missing) {
+  int st;
+  if ((st = check_table(cache, rows, table_stride, table_pages))) return st;
+  if (!fits(children, mx::MAX_FORKS / cache->heads) || child_stride < table_pages) return MX_ESHAPE;
+  if (children == 0) return MX_OK;
+  if (!parents || !missing || (rows > 0 && !kv_lens) || (table_pages > 0 && ((rows > 0 && !block_table) || !child_table)) ||
+      (cache->pages > 0 && (!refs || empty_cache(cache))))
+    return MX_ENULL;
+  if (!aligned(refs, 4) || !aligned(block_table, 4) || !aligned(kv_lens, 4) || !aligned(parents, 4) ||
+      !aligned(child_table, 4) || !aligned(missing, 4))
+    return MX_EALIGN;
+  return launched(mx::launch_cache_fork(view(cache), refs, block_table, table_stride, (int)table_pages, kv_lens,
+                                        (int)rows, parents, (int)children, child_table, child_stride, missing,
+                                        tl_stream));
+}
+
+MX_API int mx_cache_copy(const mx_cache *cache, const int32_t *src, const int32_t *dst, int64_t count) {
+  int st;
+  if ((st = check_cache(cache))) return st;
+  if (!fits(count, mx::MAX_COPIES)) return MX_ESHAPE;
+  if (count == 0 || cache->pages == 0) return MX_OK;
+  if (empty_cache(cache) || !src || !dst) return MX_ENULL;
+  if (!aligned(src, 4) || !aligned(dst, 4)) return MX_EALIGN;
+  return launched(mx::launch_cache_copy(view(cache), src, dst, count, tl_stream));
+}
+
+MX_API int mx_cache_compact(const mx_cache *cache, const int32_t *kv_starts, const int32_t *keep, int64_t keep_stride,
+                            int64_t max_keep, const int32_t *counts, const int32_t *block_table, int64_t table_stride,
+                            int64_t table_pages, int64_t batch, int32_t *kv_lens) {
+  int st;
+  if ((st = check_table(cache, batch, table_stride, table_pages))) return st;
+  if (!fits(max_keep, INT32_MAX) || keep_stride < max_keep || !fits(batch, mx::MAX_COMPACT / cache->heads))
+    return MX_ESHAPE;
+  if (batch == 0) return MX_OK;
+  if (!kv_starts || !counts || !kv_lens || (max_keep > 0 && !keep)) return MX_ENULL;
+  if (max_keep > 0 && table_pages > 0 && (!block_table || (cache->pages > 0 && empty_cache(cache)))) return MX_ENULL;
+  if (!aligned(kv_starts, 4) || !aligned(keep, 4) || !aligned(counts, 4) || !aligned(block_table, 4) ||
+      !aligned(kv_lens, 4))
+    return MX_EALIGN;
+  return launched(mx::launch_cache_compact(view(cache), kv_starts, keep, keep_stride, (int)max_keep, counts, block_table,
+                                           table_stride, (int)table_pages, (int)batch, kv_lens, tl_stream));
+}
+
+namespace {
+
+int check_verify(int64_t batch, int64_t total_q, int64_t max_q, int64_t vocab) {
+  if (!fits(batch, 1 << 24) || !fits(total_q, INT32_MAX) || !fits(max_q, mx::VERIFY_NODES) || vocab < 1 ||
+      vocab > (1 << 30))
+    return MX_ESHAPE;
+  return MX_OK;
+}
+
+}  // namespace
+
+MX_API int64_t mx_verify_workspace(int64_t batch, int64_t total_q, int64_t max_q, int64_t vocab) {
+  const int st = check_verify(batch, total_q, max_q, vocab);
+  if (st) return st;
+  return mx::verify_workspace((int)batch, (int)max_q, (int)vocab);
+}
+
+MX_API int mx_verify(const void *target, int64_t target_stride, const void *draft, int64_t draft_stride, int dtype,
+                     int64_t vocab, const int64_t *tokens, const double *uniforms, const int32_t *q_starts,
+                     const int32_t *parents, int64_t batch, int64_t total_q, int64_t max_q, int32_t *counts,
+                     int32_t *path, int64_t *out, void *workspace, int64_t workspace_bytes) {
+  int st;
+  if ((st = check_dtype(dtype)) || (st = check_verify(batch, total_q, max_q, vocab))) return st;
+  if (batch == 0) return MX_OK;
+  if (!counts || !q_starts || (max_q > 0 && (!path || !out)) ||
+      (total_q > 0 && max_q > 0 && (!target || !tokens || !uniforms)))
+    return MX_ENULL;
+  const uintptr_t size = dtype == MX_DTYPE_F32 ? 4 : 2;
+  if (!aligned(target, size) || !aligned(draft, size) || !aligned(tokens, 8) || !aligned(uniforms, 8) ||
+      !aligned(q_starts, 4) || !aligned(parents, 4) || !aligned(counts, 4) || !aligned(path, 4) || !aligned(out, 8))
+    return MX_EALIGN;
+  const int64_t need = mx::verify_workspace((int)batch, (int)max_q, (int)vocab);
+  if (need > 0 && !workspace) return MX_ENULL;
+  if (workspace_bytes < need) return MX_EARG;
+  if (need > 0 && !aligned(workspace, 16)) return MX_EALIGN;
+  const mx::VerifyArgs a{target, draft, target_stride, draft_stride, tokens, uniforms, q_starts, parents, counts, path,
+                         out, (double *)workspace, (int)batch, (int)total_q, (int)max_q, (int)vocab};
+  return launched(mx::launch_verify(dtype, a, tl_stream));
 }
 
 MX_API void mx_set_stream(void *stream) { tl_stream = (hipStream_t)stream; }
@@ -373,7 +552,7 @@ MX_API const char *mx_status_string(int status) {
     case MX_ELAYOUT:
       return "invalid layout (expected MX_SCALES_ROWMAJOR or MX_SCALES_BLOCKED; rotary: MX_ROTARY_HALF or "
              "MX_ROTARY_INTERLEAVED)";
-    case MX_EARG: return "invalid rotary, cache or attention argument";
+    case MX_EARG: return "invalid rotary, cache, attention or verification argument";
     default: return "unknown status";
   }
 }

@@ -34,7 +34,7 @@ struct Record {
 
 // What is computed of a sequence: queries q0 .. q0 + nq, tokens 0 .. len.  first_new is the place of its first new
 // token, from the lengths as they are: bounds below them leave queries and tokens out, and move no mask.  It is negative
-// where there are more queries than tokens.
+// where there are more queries than tokens, and behind every token that a call can have where queries see all of them.
 struct Sequence {
   int q0, nq, len, first_new;
 };
@@ -58,7 +58,7 @@ __device__ __forceinline__ Sequence sequence_of(const AttentionArgs &a, int b) {
   const int64_t cap = (int64_t)a.table_pages << a.cache.page_log2;
   int len = a.kv_lens[b];
   len = len < 0 ? 0 : len;
-  s.first_new = len - s.nq;
+  s.first_new = a.all ? INT32_MAX - 65536 : len - s.nq;
   s.nq = s.nq > a.max_q ? a.max_q : s.nq;
   len = len > a.max_kv ? a.max_kv : len;
   s.len = len > cap ? (int)cap : len;

@@ -36,7 +36,8 @@ struct WriteArgs {
   CacheView cache;
   const unsigned short *src[2];  // keys, values
   int64_t token_stride[2], head_stride[2];
-  const int64_t *slots, *positions;
+  const int64_t *slots;
+  Positions positions;
   const double *inv_freq;
   double scale;
   int64_t tokens;
@@ -123,7 +124,7 @@ __global__ __launch_bounds__(WRITE_THREADS) void k_cache_write(WriteArgs a) {
   for (int i = threadIdx.x; i < nt * half; i += WRITE_THREADS) {
     const int t = i / half, p = i - t * half;
     double s, c;
-    sine_cosine((double)a.positions[t0 + t] * a.inv_freq[p], s, c);
+    sine_cosine(position_of(a.positions, t0 + t, p) * a.inv_freq[p], s, c);
     tc[i] = c * a.scale;
     ts[i] = s * a.scale;
   }
@@ -185,7 +186,7 @@ __global__ __launch_bounds__(WRITE_THREADS) void k_cache_write(WriteArgs a) {
 
 hipError_t launch_cache_write(const CacheView &cache, const void *k, const int64_t k_strides[2], const void *v,
                               const int64_t v_strides[2], const int64_t *slots, int64_t tokens,
-                              const int64_t *positions, const double *inv_freq, int64_t rot, int layout, double scale,
+                              const Positions &positions, const double *inv_freq, int64_t rot, int layout, double scale,
                               hipStream_t stream) {
   WriteArgs a{cache, {(const unsigned short *)k, (const unsigned short *)v}, {k_strides[0], v_strides[0]},
               {k_strides[1], v_strides[1]}, slots, positions, inv_freq, scale, tokens, (int)(rot / 2), 0, 0};

@@ -1,0 +1,358 @@
+// The cache's pages: whole pages copied, sequences forked, pages taken and
+// freed, and a sequence's tokens compacted to those that are kept.
+//
+// refs[page] counts the rows of tables that hold a page; a page is free while
+// it is zero.  Free pages are handed out lowest first, in the order of the
+// rows and columns that lack one, so that the same tables give the same pages.
+//
+//   resize   row r holds ceil(kv_lens[r] / page) pages: those behind them are
+//            released first, in all rows, then missing ones are taken.
+//   fork     a child row shares its parent's full pages and has the tokens of
+//            the last page, if it is not full, in a page of its own.
+//   compact  token i of what is kept comes from place keep[i] >= i.
+//
+// Bound: HBM for what is moved (each byte read and written once), latency for
+// the tables: one small kernel for the rows, one workgroup that hands out
+// pages.
+#include "launch.h"
+
+namespace mx {
+
+namespace {
+
+struct BookArgs {
+  int *refs;
+  const int *kv_lens, *parents;  // parents: of a fork
+  const int *table;              // of a fork: the parents'
+  int64_t stride, out_stride;
+  int *out, *missing;
+  int pages, page_log2, rows, cols, out_rows;
+};
+
+// What a row of the result holds: `keep` pages of the row it comes from, `need` in all.
+struct Row {
+  int from, keep, need;
+};
+
+template <bool FORK>
+__device__ __forceinline__ Row row_of(const BookArgs &a, int r) {
+  const int from = FORK ? a.parents[r] : r;
+  int len = FORK && (unsigned)from >= (unsigned)a.rows ? 0 : a.kv_lens[from];
+  len = len < 0 ? 0 : len;
+  const int full = len >> a.page_log2, need = full + ((len & ((1 << a.page_log2) - 1)) != 0);
+  return Row{from, FORK ? full : need, need};
+}
+
+// Rows one by one, a wave each: pages are released or shared, and missing[row] is what the row lacks.
+template <bool FORK>
+__global__ __launch_bounds__(256) void k_page_rows(BookArgs a) {
+  const int lane = threadIdx.x % 64;
+  const int r = blockIdx.x * 4 + threadIdx.x / 64;
+  if (r >= a.out_rows) return;
+  const Row row = row_of<FORK>(a, r);
+  const int *src = a.table + (int64_t)row.from * a.stride;
+  int *dst = a.out + (int64_t)r * a.out_stride;
+  int lack = 0;
+#pragma unroll 4
+  for (int j = lane; j < a.cols; j += 64) {
+    const int was = FORK && j >= row.keep ? -1 : src[j];
+    const bool held = (unsigned)was < (unsigned)a.pages;
+    if (FORK) {
+      if (held) atomicAdd(a.refs + was, 1);
+      dst[j] = held ? was : -1;
+      lack += j < row.need && !held;
+    } else if (j < row.need) {
+      if (!held && was != -1) dst[j] = -1;
+      lack += !held;
+    } else {
+      // (a page that nobody holds stays free)
+      if (held && atomicSub(a.refs + was, 1) <= 0) atomicAdd(a.refs + was, 1);
+      if (was != -1) dst[j] = -1;
+    }
+  }
+#pragma unroll
+  for (int d = 32; d > 0; d /= 2) lack += __shfl_xor(lack, d);
+  if (lane == 0) a.missing[r] = lack + (row.need > a.cols ? row.need - a.cols : 0);
+}
+
+constexpr int TAKE_THREADS = 1024, TAKE_ITEMS = 4;  // entries of a table that a step of the workgroup looks at: 4096
+constexpr int SCAN_ITEMS = 8;                       // counts of holders: 8192
+constexpr int QUEUE = TAKE_THREADS * (TAKE_ITEMS + SCAN_ITEMS);
+
+// The sum of v over the threads before this one, and over all of them (total).
+__device__ __forceinline__ int block_prefix(int v, int *waves, int &total) {
+  const int lane = threadIdx.x % 64, wave = threadIdx.x / 64;
+  int sum = v;
+#pragma unroll
+  for (int d = 1; d < 64; d *= 2) {
+    const int u = __shfl_up(sum, d);
+    if (lane >= d) sum += u;
+  }
+  __syncthreads();  // waves[] of the call before has been read
+  if (lane == 63) waves[wave] = sum;
+  __syncthreads();
+  int before = 0;
+  total = 0;
+#pragma unroll
+  for (int w = 0; w < TAKE_THREADS / 64; ++w) {
+    before += w < wave ? waves[w] : 0;
+    total += waves[w];
+  }
+  return before + sum - v;
+}
+
+// One workgroup hands out pages: it goes over the entries that lack one in their order, and over refs for free ones.
+template <bool FORK>
+__global__ __launch_bounds__(TAKE_THREADS) void k_page_take(BookArgs a) {
+  __shared__ int waves[TAKE_THREADS / 64];
+  __shared__ int queue[QUEUE];
+  int lack = 0, total;
+  for (int r = threadIdx.x; r < a.out_rows; r += TAKE_THREADS) lack |= a.missing[r];
+  block_prefix(lack != 0, waves, total);
+  if (total == 0) return;
+
+  int head = 0, size = 0, cursor = 0;  // of the queue of free pages; the first page that was not looked at
+  const int64_t cols = FORK ? 1 : a.cols, entries = a.out_rows * cols;
+  for (int64_t base = 0; base < entries; base += TAKE_THREADS * TAKE_ITEMS) {
+    int *place[TAKE_ITEMS], *miss[TAKE_ITEMS];
+    int wants = 0;
+#pragma unroll
+    for (int k = 0; k < TAKE_ITEMS; ++k) {
+      const int64_t e = base + threadIdx.x * TAKE_ITEMS + k;
+      place[k] = nullptr;
+      if (e >= entries) continue;
+      const int r = FORK ? (int)e : entries >> 32 ? (int)(e / cols) : (int)((unsigned)e / (unsigned)cols);
+      miss[k] = a.missing + r;
+      if (a.missing[r] == 0) continue;
+      const Row row = row_of<FORK>(a, r);
+      const int j = FORK ? row.keep : (int)(e - r * cols);
+      if (j >= row.need || j >= a.cols) continue;
+      int *at = a.out + (int64_t)r * a.out_stride + j;
+      if (*at != -1) continue;
+      place[k] = at;
+      ++wants;
+    }
+    int rank = block_prefix(wants, waves, total);
+    while (size < total && cursor < a.pages) {
+      int found = 0;
+      unsigned free = 0;
+      const unsigned p0 = (unsigned)cursor + threadIdx.x * SCAN_ITEMS;
+#pragma unroll
+      for (int k = 0; k < SCAN_ITEMS; ++k) {
+        const unsigned p = p0 + k;
+        // past the first-level cache: other calls' counts, and those of the kernel before
+        const bool is = p < (unsigned)a.pages &&
+                        __hip_atomic_load(a.refs + p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == 0;
+        free |= (unsigned)is << k;
+        found += is;
+      }
+      int all;
+      int at = head + size + block_prefix(found, waves, all);
+      for (; free; free &= free - 1, ++at) queue[at % QUEUE] = (int)(p0 + __builtin_ctz(free));
+      size += all;
+      cursor = cursor > a.pages - TAKE_THREADS * SCAN_ITEMS ? a.pages : cursor + TAKE_THREADS * SCAN_ITEMS;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < TAKE_ITEMS; ++k) {
+      if (place[k] == nullptr) continue;
+      if (rank < size) {
+        const int page = queue[(head + rank) % QUEUE];
+        *place[k] = page;
+        a.refs[page] = 1;
+        atomicSub(miss[k], 1);
+      }
+      ++rank;
+    }
+    const int gone = total < size ? total : size;
+    head = (head + gone) % QUEUE;
+    size -= gone;
+    __syncthreads();  // the queue's places that are free now are written by the next step
+  }
+}
+
+// ---- moving ----
+
+// The cache's four tensors as pieces of 16 bytes: codes and scales of a head's page.
+struct Moved {
+  u32x4 *codes[2], *scales[2];
+  int code_pieces, scale_pieces;  // of a page of one head
+};
+
+Moved moved(const CacheView &cv) {
+  const int page = 1 << cv.page_log2;
+  return Moved{{(u32x4 *)cv.codes[0], (u32x4 *)cv.codes[1]}, {(u32x4 *)cv.scales[0], (u32x4 *)cv.scales[1]},
+               page * (cv.fmt == 0 ? cv.dim / 2 : cv.dim) / 16, page * (cv.dim / 32) / 16};
+}
+
+constexpr int MOVE_THREADS = 256, MOVE_UNROLL = 4;
+
+// A workgroup copies the pieces from .. to of one tensor's page.
+__device__ __forceinline__ void copy_pieces(const u32x4 *src, u32x4 *dst, int64_t from, int64_t to) {
+  for (int64_t i = from + threadIdx.x; i < to; i += MOVE_THREADS * MOVE_UNROLL) {
+    u32x4 v[MOVE_UNROLL];
+#pragma unroll
+    for (int u = 0; u < MOVE_UNROLL; ++u)
+      if (i + u * MOVE_THREADS < to) v[u] = src[i + u * MOVE_THREADS];
+#pragma unroll
+    for (int u = 0; u < MOVE_UNROLL; ++u)
+      if (i + u * MOVE_THREADS < to) dst[i + u * MOVE_THREADS] = v[u];
+  }
+}
+
+// Part of `parts` workgroups of a page: each has its share of the codes and of the scales.
+__global__ __launch_bounds__(MOVE_THREADS) void k_copy_pages(Moved m, int64_t pages, int heads, const int *src,
+                                                             const int *dst, int parts) {
+  const int64_t n = blockIdx.x / parts;
+  const int part = blockIdx.x - n * parts;
+  const int from = src[n], to = dst[n];
+  if ((unsigned)from >= (uint64_t)pages || (unsigned)to >= (uint64_t)pages || from == to) return;
+#pragma unroll
+  for (int v = 0; v < 2; ++v) {
+    const int64_t codes = (int64_t)heads * m.code_pieces, scales = (int64_t)heads * m.scale_pieces;
+    const u32x4 *c = m.codes[v] + from * codes, *s = m.scales[v] + from * scales;
+    copy_pieces(c, m.codes[v] + to * codes, codes * part / parts, codes * (part + 1) / parts);
+    copy_pieces(s, m.scales[v] + to * scales, scales * part / parts, scales * (part + 1) / parts);
+  }
+}
+
+// The last, partly filled page of each child: its parent's tokens and nothing behind them.
+__global__ __launch_bounds__(MOVE_THREADS) void k_copy_last(Moved m, BookArgs a, int heads, int scale_rows) {
+  const int child = blockIdx.x / heads, head = blockIdx.x - child * heads;
+  const Row row = row_of<true>(a, child);
+  if (row.keep == row.need || row.keep >= a.cols) return;
+  const int from = a.table[(int64_t)row.from * a.stride + row.keep];
+  const int to = a.out[(int64_t)child * a.out_stride + row.keep];
+  if ((unsigned)from >= (unsigned)a.pages || (unsigned)to >= (unsigned)a.pages) return;
+  const int tokens = a.kv_lens[row.from] & ((1 << a.page_log2) - 1);
+  const int v = blockIdx.y, codes = m.code_pieces >> a.page_log2;  // pieces of a token
+  const int64_t f = (int64_t)from * heads + head, t = (int64_t)to * heads + head;
+  copy_pieces(m.codes[v] + f * m.code_pieces, m.codes[v] + t * m.code_pieces, 0, tokens * codes);
+  const uint8_t *s = (const uint8_t *)(m.scales[v] + f * m.scale_pieces);
+  uint8_t *d = (uint8_t *)(m.scales[v] + t * m.scale_pieces);
+  for (int g = 0; g < scale_rows; ++g)
+    for (int i = threadIdx.x; i < tokens; i += MOVE_THREADS)
+      d[(g << a.page_log2) + i] = s[(g << a.page_log2) + i];
+}
+
+struct CompactArgs {
+  CacheView cache;
+  const int *kv_starts, *keep, *counts, *table;
+  int64_t keep_stride, stride;
+  int *kv_lens;
+  int max_keep, cols;
+};
+
+constexpr int COMPACT_THREADS = 1024, COMPACT_UNROLL = 4;
+
+// A workgroup has one head of one sequence, its keys' or values' codes or scales, whose tokens it takes in groups: all
+// of a group is read before any of it is written, and as keep[i] >= i no group writes what a later one reads.  So the
+// tokens may be moved within their own pages, and every place has what place keep[i] held at the beginning.
+// T: what a thread moves of a token, of which there are `per` pieces.
+template <typename T>
+__device__ __forceinline__ void compact(const CompactArgs &a, T *data, int per, bool planes, int b, int head) {
+  const CacheView &cv = a.cache;
+  const int64_t start = a.kv_starts[b];
+  const int *table = a.table + (int64_t)b * a.stride, *keep = a.keep + (int64_t)b * a.keep_stride;
+  int count = a.counts[b];
+  count = count < a.max_keep ? count : a.max_keep;
+  const int group = COMPACT_THREADS / per, token = threadIdx.x / per, piece = threadIdx.x - token * per;
+  const int64_t room = (int64_t)a.cols << cv.page_log2;
+  const int mask = (1 << cv.page_log2) - 1;
+  auto at = [&](int64_t place) -> int64_t {  // -1: no such place
+    if (place < 0 || place >= room) return -1;
+    const int page = table[place >> cv.page_log2];
+    if ((unsigned)page >= (uint64_t)cv.pages) return -1;
+    const int64_t ph = (int64_t)page * cv.heads + head;
+    const int r = (int)place & mask;
+    return planes ? ((ph * per + piece) << cv.page_log2) + r : ((ph << cv.page_log2) + r) * per + piece;
+  };
+  for (int base = 0; base < count; base += group * COMPACT_UNROLL) {
+    T v[COMPACT_UNROLL];
+    int64_t to[COMPACT_UNROLL];
+#pragma unroll
+    for (int u = 0; u < COMPACT_UNROLL; ++u) {
+      const int64_t i = base + (int64_t)u * group + token;
+      to[u] = -1;
+      if (token >= group || i >= count) continue;
+      const int k = keep[i];
+      if (k <= i) continue;  // it is where it belongs, or cannot be moved
+      const int64_t from = at(start + k);
+      to[u] = from < 0 ? -1 : at(start + i);
+      if (to[u] >= 0) v[u] = data[from];
+    }
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // what this wave reads has arrived
+    __syncthreads();
+#pragma unroll
+    for (int u = 0; u < COMPACT_UNROLL; ++u)
+      if (to[u] >= 0) data[to[u]] = v[u];
+  }
+}
+
+__global__ __launch_bounds__(COMPACT_THREADS) void k_compact(CompactArgs a) {
+  const CacheView &cv = a.cache;
+  const int b = blockIdx.x / cv.heads, head = blockIdx.x - b * cv.heads, v = blockIdx.y % 2;
+  if (blockIdx.y >= 2) {
+    compact<uint8_t>(a, cv.scales[v], cv.dim / 32, true, b, head);
+  } else {
+    compact<u32x4>(a, (u32x4 *)cv.codes[v], (cv.fmt == 0 ? cv.dim / 2 : cv.dim) / 16, false, b, head);
+    if (blockIdx.y == 0 && head == 0 && threadIdx.x == 0) {
+      const int count = a.counts[b] < a.max_keep ? a.counts[b] : a.max_keep;
+      a.kv_lens[b] = a.kv_starts[b] + (count < 0 ? 0 : count);
+    }
+  }
+}
+
+BookArgs book(const CacheView &cv, int *refs, const int *table, int64_t stride, int cols, const int *kv_lens, int rows,
+              const int *parents, int *out, int64_t out_stride, int out_rows, int *missing) {
+  return BookArgs{refs, kv_lens, parents, table, stride, out_stride, out, missing, (int)cv.pages, cv.page_log2, rows,
+                  cols, out_rows};
+}
+
+template <bool FORK>
+hipError_t hand_out(const BookArgs &a, hipStream_t stream) {
+  k_page_rows<FORK><<<(a.out_rows + 3) / 4, 256, 0, stream>>>(a);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  k_page_take<FORK><<<1, TAKE_THREADS, 0, stream>>>(a);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_cache_resize(const CacheView &cache, int *refs, int *table, int64_t stride, int pages,
+                               const int *kv_lens, int rows, int *missing, hipStream_t stream) {
+  return hand_out<false>(book(cache, refs, table, stride, pages, kv_lens, rows, nullptr, table, stride, rows, missing),
+                         stream);
+}
+
+hipError_t launch_cache_fork(const CacheView &cache, int *refs, const int *table, int64_t stride, int pages,
+                             const int *kv_lens, int rows, const int *parents, int children, int *child_table,
+                             int64_t child_stride, int *missing, hipStream_t stream) {
+  const BookArgs a = book(cache, refs, table, stride, pages, kv_lens, rows, parents, child_table, child_stride,
+                          children, missing);
+  const hipError_t e = hand_out<true>(a, stream);
+  if (e != hipSuccess) return e;
+  k_copy_last<<<dim3((unsigned)(children * cache.heads), 2), MOVE_THREADS, 0, stream>>>(moved(cache), a, cache.heads,
+                                                                                        cache.dim / 32);
+  return hipGetLastError();
+}
+
+hipError_t launch_cache_copy(const CacheView &cache, const int *src, const int *dst, int64_t count, hipStream_t stream) {
+  const Moved m = moved(cache);
+  // a workgroup's share: 4 pieces for each thread, while the grid holds them
+  int64_t parts = ((int64_t)cache.heads * m.code_pieces + MOVE_THREADS * MOVE_UNROLL - 1) / (MOVE_THREADS * MOVE_UNROLL);
+  if (parts > MAX_GROUPS_256 / count) parts = MAX_GROUPS_256 / count;
+  k_copy_pages<<<(unsigned)(count * parts), MOVE_THREADS, 0, stream>>>(m, cache.pages, cache.heads, src, dst, (int)parts);
+  return hipGetLastError();
+}
+
+hipError_t launch_cache_compact(const CacheView &cache, const int *kv_starts, const int *keep, int64_t keep_stride,
+                                int max_keep, const int *counts, const int *table, int64_t stride, int pages, int batch,
+                                int *kv_lens, hipStream_t stream) {
+  const CompactArgs a{cache, kv_starts, keep, counts, table, keep_stride, stride, kv_lens, max_keep, pages};
+  k_compact<<<dim3((unsigned)(batch * cache.heads), 4), COMPACT_THREADS, 0, stream>>>(a);
+  return hipGetLastError();
+}
+
+}  // namespace mx

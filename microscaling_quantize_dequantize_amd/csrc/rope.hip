@@ -25,7 +25,7 @@ constexpr int ROPE_THREADS = 256;
 
 struct RopeArgs {
   int64_t tokens, src_token, src_head, dst_token, dst_head;  // strides in elements
-  const int64_t *positions;
+  Positions positions;
   const double *inv_freq;
   double scale;
   int heads, dim, half, per_wg, inverse, copy;  // half: pairs; copy: the rest is copied too (dst is not src)
@@ -120,7 +120,7 @@ __global__ __launch_bounds__(ROPE_THREADS) void k_rope(const T *src, T *dst, Rop
   for (int i = threadIdx.x; i < nt * a.half; i += ROPE_THREADS) {
     const int t = i / a.half, p = i - t * a.half;
     double s, c;
-    sine_cosine((double)a.positions[t0 + t] * a.inv_freq[p], s, c);
+    sine_cosine(position_of(a.positions, t0 + t, p) * a.inv_freq[p], s, c);
     tc[i] = (float)(c * a.scale);
     ts[i] = (float)(a.inverse ? -s * a.scale : s * a.scale);
   }
@@ -146,7 +146,7 @@ __global__ __launch_bounds__(ROPE_THREADS) void k_rope_staged(const T *src, T *d
   for (int i = threadIdx.x; i < nt * a.half; i += ROPE_THREADS) {
     const int t = i / a.half, p = i - t * a.half;
     double s, c;
-    sine_cosine((double)a.positions[t0 + t] * a.inv_freq[p], s, c);
+    sine_cosine(position_of(a.positions, t0 + t, p) * a.inv_freq[p], s, c);
     tc[i] = (float)(c * a.scale);
     ts[i] = (float)(a.inverse ? -s * a.scale : s * a.scale);
   }
@@ -207,7 +207,7 @@ static void rope_vec(int vec, const void *src, void *dst, const RopeArgs &a, hip
 }
 
 hipError_t launch_rope(int dtype, const void *src, void *dst, int64_t tokens, int64_t heads, int64_t dim,
-                       const int64_t strides[4], const int64_t *positions, const double *inv_freq, int64_t rot,
+                       const int64_t strides[4], const Positions &positions, const double *inv_freq, int64_t rot,
                        int layout, double scale, int inverse, hipStream_t stream) {
   const int size = dtype == 1 ? 4 : 2;
   RopeArgs a{tokens, strides[0], strides[1], strides[2], strides[3], positions, inv_freq, scale,

@@ -1,11 +1,18 @@
 // Rotary positions on the device: the angle of a pair and its sine and cosine.
 #pragma once
 
-#include "mx_device.h"
+#include "launch.h"
 
 namespace mx {
 
 enum RotaryLayout { ROTARY_HALF = 0, ROTARY_INTERLEAVED = 1 };
+
+// The position that turns a pair of a token; zero on an axis that there is not.
+__device__ __forceinline__ double position_of(const Positions &p, int64_t token, int pair) {
+  if (p.axes == nullptr) return (double)p.at[token];
+  const int axis = p.axes[pair];
+  return (unsigned)axis < (unsigned)p.count ? (double)p.at[axis * p.stride + token] : 0.0;
+}
 
 // Sine and cosine of an angle in radians, in fp64.
 //
