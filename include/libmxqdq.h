@@ -498,12 +498,13 @@ MX_API int mx_cache_compact(const mx_cache *cache, const int32_t *kv_starts,
  * (q: draft[c], or 1 for x and 0 for all others if draft == NULL).  Behind the
  * last kept node a token is sampled from w: the first whose cumulative sum is
  * above uniforms[node 0] * sum w.  Computed in fp64; probabilities that are
- * negative or not finite count as zero; nodes with tokens outside the vocabulary
- * are passed over.
+ * negative or NaN count as zero, infinite ones as fp32's largest number; nodes
+ * with tokens outside the vocabulary are passed over.
  *   target, draft  [total_q x vocab] in dtype, strides in elements: row c holds
  *              the probabilities after node c, and those that its children were
  *              drawn from.  vocab 1 to 2^30 (MX_ESHAPE).
  *   tokens     [total_q] int64; uniforms [total_q] fp64 in [0, 1).
+ *   batch      up to 2^22 - 1 (MX_ESHAPE).
  *   parents    [total_q] int32: a node's parent by its place in the sequence
  *              (nodes whose parent is not before them are passed over), or NULL:
  *              each node follows the one before.

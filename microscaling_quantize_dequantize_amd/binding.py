@@ -795,8 +795,8 @@ def mx_verify(target: torch.Tensor, tokens: torch.Tensor, uniforms: torch.Tensor
     From the first node on, the children of a node are asked in their order, with w the node's row of target and W = 1:
     token x is kept if uniform * W * draft(x) < w(x), and its children are asked next; if not, w = max(w - W * draft, 0)
     and W = sum(w), unless nothing would be left.  After the last kept node a token is sampled from w: the first whose
-    cumulative sum is above uniform * sum(w).  (fp64; negative and not finite probabilities count as zero; drafted tokens
-    outside the vocabulary are passed over.)
+    cumulative sum is above uniform * sum(w).  (fp64; negative probabilities and NaN count as zero, infinity as fp32's
+    largest number; drafted tokens outside the vocabulary are passed over.)
 
     Returns counts int32 [batch], the nodes that stay (the first one and the kept ones); path int32 [batch, max_q], their
     places, then -1; and int64 [batch, max_q], the kept tokens and the sampled one, then -1 (the sampled one is -1 too

@@ -498,7 +498,7 @@ MX_API int mx_cache_compact(const mx_cache *cache, const int32_t *kv_starts, con
 namespace {
 
 int check_verify(int64_t batch, int64_t total_q, int64_t max_q, int64_t vocab) {
-  if (!fits(batch, 1 << 24) || !fits(total_q, INT32_MAX) || !fits(max_q, mx::VERIFY_NODES) || vocab < 1 ||
+  if (!fits(batch, mx::MAX_VERIFY) || !fits(total_q, INT32_MAX) || !fits(max_q, mx::VERIFY_NODES) || vocab < 1 ||
       vocab > (1 << 30))
     return MX_ESHAPE;
   return MX_OK;

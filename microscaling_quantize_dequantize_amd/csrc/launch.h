@@ -119,7 +119,8 @@ hipError_t launch_cache_compact(const CacheView &cache, const int *kv_starts, co
                                 int *kv_lens, hipStream_t stream);
 
 // Verification of drafted tokens (strides in elements).
-constexpr int VERIFY_NODES = 1024;  // of a sequence
+constexpr int VERIFY_NODES = 1024;                      // of a sequence
+constexpr int64_t MAX_VERIFY = ((int64_t)1 << 22) - 1;  // sequences: a workgroup of 1024 threads each at least
 
 struct VerifyArgs {
   const void *target, *draft;  // draft: nullptr if the drafts have no probabilities

@@ -9,27 +9,38 @@
 // u_0 sum(w).  So what is put out is distributed as the target's own tokens,
 // whatever the drafts were (q_c: the distribution the children of c were drawn
 // from; without one, 1 for the child's token and 0 for the others).
-// A refusal that would leave no weight at all leaves w as it is.  Tokens outside the vocabulary are not asked.
+// A refusal that would leave no weight at all leaves w as it is.  Tokens outside
+// the vocabulary are not asked.
 //
-// Weights are computed in fp64 from the rows, entry by entry: what a refusal
-// takes away is remembered by its factor W alone (or its token), so that no row
-// is ever written.  Probabilities that are negative or not finite count as zero.
+// As q is not negative, all that was taken from w is one factor:
+//   w = max(p - F q, 0),  F the sum of the W that were taken,
+// so no row is ever written; without a draft's row it is the tokens refused.
+// Weights and sums are fp64, as the test and the sample have borders that fp32
+// sums of 10^5 entries would miss.  Probabilities that are negative or NaN count
+// as zero, infinite ones as the largest number of fp32.
 //
-// Bound: HBM, the rows of the node where the walk ends; only a refusal with
-// another sibling behind it needs the sum of a row before that.
+// Three kernels.  k_branch (trees only) finds for each node what follows it:
+// which child is kept, or the factors with which the walk ends there.  That does
+// not depend on the way to the node, so nodes are worked on side by side, a
+// workgroup each, and only those that a walk can reach and that have a child
+// behind a refused one need the sum of a row.  k_sums follows the walk and sums
+// the weights at its end in shares, one for each of its waves; k_pick finds the
+// token in one of them.  Where one workgroup has a row's shares both are one
+// kernel.
+//
+// Bound: HBM for large batches (the rows at the walk's end), else the chain of
+// dependent loads (starts, tokens, points of rows, rows, sums).
 #include "launch.h"
 
 namespace mx {
 
 namespace {
 
-constexpr int VERIFY_THREADS = 1024, VERIFY_WAVES = VERIFY_THREADS / 64;
-
-__device__ __forceinline__ double weight_of(unsigned short b) {
-  const float f = __uint_as_float((unsigned)b << 16);
-  return f > 0.0f && f < __builtin_inff() ? (double)f : 0.0;
+// The median of a number, zero and the largest one; of NaN it is the smaller of the other two.
+__device__ __forceinline__ double weight_of(float f) {
+  return (double)__builtin_amdgcn_fmed3f(f, 0.0f, 3.402823466e38f);
 }
-__device__ __forceinline__ double weight_of(float f) { return f > 0.0f && f < __builtin_inff() ? (double)f : 0.0; }
+__device__ __forceinline__ double weight_of(unsigned short b) { return weight_of(__uint_as_float((unsigned)b << 16)); }
 
 template <typename T> struct Chunk {
   static constexpr int N = 16 / sizeof(T);
@@ -37,11 +48,12 @@ template <typename T> struct Chunk {
 } __attribute__((aligned(16)));
 
 // A node's rows, cut at 16-byte boundaries: chunk k holds the entries k N - off ..., of which those outside 0 .. vocab
-// are zero.  DRAFT: there is a row q, which is cut like p; wide says that it lies to the boundaries as p does.
+// are zero; the chunks whole0 .. whole1 have none of these.  DRAFT: there is a row q, which is cut like p; wide says that
+// it lies to the boundaries as p does.
 template <typename T, bool DRAFT> struct Rows {
   static constexpr int N = Chunk<T>::N;
   const T *p, *q;
-  int vocab, off, chunks;
+  int vocab, off, chunks, whole0, whole1;
   bool wide;
 
   __device__ __forceinline__ Rows(const VerifyArgs &a, int64_t row) {
@@ -51,38 +63,39 @@ template <typename T, bool DRAFT> struct Rows {
     off = (int)((uintptr_t)p % 16 / sizeof(T));
     wide = !DRAFT || (uintptr_t)q % 16 / sizeof(T) == (unsigned)off;
     chunks = (vocab + off + N - 1) / N;
+    whole0 = off > 0;
+    whole1 = (vocab + off) / N;
   }
   __device__ __forceinline__ Chunk<T> read(const T *x, int k, bool whole) const {
     Chunk<T> c;
     const int64_t e = (int64_t)k * N - off;
-    if (whole && k < chunks && e >= 0 && e + N <= vocab) return *(const Chunk<T> *)(x + e);
+    if (whole && k >= whole0 && k < whole1) return *(const Chunk<T> *)(x + e);
 #pragma unroll
     for (int i = 0; i < N; ++i) c.v[i] = e + i >= 0 && e + i < vocab ? x[e + i] : T(0);
     return c;
   }
 };
 
-// What refusals have taken from the weights at the walk's node.
+// What was taken from the weights: F q, or without a draft's row the tokens of a list.
 struct Taken {
-  double *factor;  // with a draft's row: the W of each
-  int *token;      // without: the tokens
+  double factor;
+  const int *tokens;
   int count;
 };
 
-// The weights of a chunk.
+// The weights of chunk k.
 template <typename T, bool DRAFT>
 __device__ __forceinline__ void weigh(const Rows<T, DRAFT> &rows, const Taken &taken, int k, const Chunk<T> &p,
                                       const Chunk<T> &q, double *w) {
   constexpr int N = Chunk<T>::N;
 #pragma unroll
   for (int i = 0; i < N; ++i) w[i] = weight_of(p.v[i]);
-  for (int j = 0; j < taken.count; ++j) {
-    if (DRAFT) {
-      const double f = taken.factor[j];
+  if (DRAFT) {
 #pragma unroll
-      for (int i = 0; i < N; ++i) w[i] = fmax(w[i] - f * weight_of(q.v[i]), 0.0);
-    } else {
-      const int at = taken.token[j] - (k * N - rows.off);
+    for (int i = 0; i < N; ++i) w[i] = fmax(__builtin_fma(-taken.factor, weight_of(q.v[i]), w[i]), 0.0);
+  } else {
+    for (int j = 0; j < taken.count; ++j) {
+      const int64_t at = taken.tokens[j] - ((int64_t)k * N - rows.off);
 #pragma unroll
       for (int i = 0; i < N; ++i) w[i] = at == i ? 0.0 : w[i];
     }
@@ -95,193 +108,590 @@ __device__ __forceinline__ double wave_sum_f64(double v) {
   return v;
 }
 
-// Sums of w over each wave's share of the chunks from .. to into sums[], and their sum (in the order of the waves).
-template <typename T, bool DRAFT>
-__device__ double sum_weights(const Rows<T, DRAFT> &rows, const Taken &taken, int from, int to, double *sums) {
-  constexpr int N = Chunk<T>::N, UNROLL = 4;
-  const int wave = threadIdx.x / 64, lane = threadIdx.x % 64;
-  const int per = (to - from + VERIFY_WAVES - 1) / VERIFY_WAVES;
-  const int k0 = from + wave * per, k1 = k0 + per < to ? k0 + per : to;
-  double sum = 0.0;
-  for (int k = k0 + lane; k < k1; k += 64 * UNROLL) {
-    Chunk<T> p[UNROLL], q[UNROLL];
-#pragma unroll
-    for (int u = 0; u < UNROLL; ++u) {
-      const int at = k + 64 * u < k1 ? k + 64 * u : rows.chunks;  // behind the row: zeros
-      p[u] = rows.read(rows.p, at, true);
-      if (DRAFT) q[u] = rows.read(rows.q, at, rows.wide);
-    }
-#pragma unroll
-    for (int u = 0; u < UNROLL; ++u) {
-      double w[N];
-      weigh<T, DRAFT>(rows, taken, k + 64 * u, p[u], q[u], w);
-#pragma unroll
-      for (int i = 0; i < N; ++i) sum += w[i];
-    }
-  }
-  sum = wave_sum_f64(sum);
-  __syncthreads();  // sums of the call before have been read
-  if (lane == 0) sums[wave] = sum;
+// The sum of v over the workgroup, in the order of its waves; waves[] has a place for each.
+template <int THREADS>
+__device__ __forceinline__ double block_sum(double v, double *waves) {
+  v = wave_sum_f64(v);
+  __syncthreads();  // what the call before left there has been read
+  if (threadIdx.x % 64 == 0) waves[threadIdx.x / 64] = v;
   __syncthreads();
   double total = 0.0;
-  for (int w = 0; w < VERIFY_WAVES; ++w) total += sums[w];
+#pragma unroll
+  for (int w = 0; w < THREADS / 64; ++w) total += waves[w];
   return total;
 }
 
-// The first of n places whose running sum, after `before`, is above `target`, with `before` taken to what lies before
-// it; the last one that has any weight if rounding leaves none; -1 if nothing has weight.
-__device__ __forceinline__ int first_above(const double *sums, int n, double target, double &before) {
-  int at = -1;
-  double sum = before;
-  for (int i = 0; i < n; ++i) {
-    if (sums[i] > 0.0) {
-      at = i;
-      before = sum;
-      sum += sums[i];
-      if (sum > target) return at;
+// The sum of the weights of the chunks from .. to that `lanes` lanes have among them, of which this is `lane`; each has
+// its own part of it.
+template <typename T, bool DRAFT>
+__device__ __forceinline__ double add_weights(const Rows<T, DRAFT> &rows, const Taken &taken, int from, int to, int lanes,
+                                              int lane) {
+  constexpr int N = Chunk<T>::N, UNROLL = 4;
+  double sum = 0.0;
+  auto add = [&](int k, const Chunk<T> &p, const Chunk<T> &q) {
+    double w[N];
+    weigh<T, DRAFT>(rows, taken, k, p, q, w);
+#pragma unroll
+    for (int i = 0; i < N; ++i) sum += w[i];
+  };
+  auto add_any = [&](int k) {
+    const Chunk<T> p = rows.read(rows.p, k, true);
+    add(k, p, DRAFT ? rows.read(rows.q, k, rows.wide) : p);
+  };
+  if (rows.wide) {
+    const int k0 = from > rows.whole0 ? from : rows.whole0, k1 = to < rows.whole1 ? to : rows.whole1;
+    const Chunk<T> *ps = (const Chunk<T> *)(rows.p - rows.off), *qs = (const Chunk<T> *)(rows.q - rows.off);
+    for (int64_t k = k0 + (int64_t)lane; k < k1; k += UNROLL * lanes) {
+      Chunk<T> p[UNROLL], q[UNROLL];
+#pragma unroll
+      for (int u = 0; u < UNROLL; ++u) {
+        // behind the end the last chunk, which is not added: no load waits for a branch
+        const int64_t at = k + u * lanes < k1 ? k + u * lanes : k1 - 1;
+        p[u] = ps[at];
+        if (DRAFT) q[u] = qs[at];
+      }
+#pragma unroll
+      for (int u = 0; u < UNROLL; ++u)
+        if (k + u * lanes < k1) add((int)k + u * lanes, p[u], q[u]);
     }
+    // the ends, if they are cut (one lane each)
+    if (lane == 0 && from < rows.whole0 && to > 0) add_any(0);
+    if (lane == lanes - 1 && to > rows.whole1 && to > rows.whole0 && from <= rows.whole1) add_any(rows.whole1);
+  } else {
+    for (int64_t k = from + (int64_t)lane; k < to; k += lanes) add_any((int)k);
   }
-  return at;
+  return sum;
 }
 
-template <typename T, bool DRAFT, bool TREE>
-__global__ __launch_bounds__(VERIFY_THREADS) void k_verify(VerifyArgs a) {
-  __shared__ double u[VERIFY_NODES], wp[VERIFY_NODES], wq[VERIFY_NODES], factor[VERIFY_NODES];
-  __shared__ int64_t token[VERIFY_NODES];
-  __shared__ int parent[VERIFY_NODES], refused[VERIFY_NODES];
-  __shared__ double sums[VERIFY_THREADS];
-  const int b = blockIdx.x, t = threadIdx.x;
-  const int q0 = a.q_starts[b] < 0 ? 0 : a.q_starts[b];
-  int nq = (a.q_starts[b + 1] > a.total_q ? a.total_q : a.q_starts[b + 1]) - q0;
-  nq = nq < 0 ? 0 : nq > a.max_q ? a.max_q : nq;
-  int *path = a.path + (int64_t)b * a.max_q;
-  int64_t *out = a.out + (int64_t)b * a.max_q;
+struct Nodes {
+  int first, count;  // of a sequence
+};
 
-  if (t < nq) {
-    const int64_t x = a.tokens[q0 + t];
-    const int up = t == 0 ? -1 : TREE ? a.parents[q0 + t] : t - 1;
-    u[t] = a.uniforms[q0 + t];
-    token[t] = x;
-    parent[t] = up;
-    wp[t] = wq[t] = 0.0;
-    if (up >= 0 && up < t && x >= 0 && x < a.vocab) {
-      wp[t] = weight_of(((const T *)a.target)[(q0 + up) * a.target_stride + x]);
-      wq[t] = DRAFT ? weight_of(((const T *)a.draft)[(q0 + up) * a.draft_stride + x]) : 1.0;
-    }
-  }
+__device__ __forceinline__ Nodes nodes_of(const VerifyArgs &a, int b) {
+  const int q0 = a.q_starts[b], q1 = a.q_starts[b + 1];
+  const int first = q0 < 0 ? 0 : q0;
+  int n = (q1 > a.total_q ? a.total_q : q1) - first;
+  n = n < 0 ? 0 : n > a.max_q ? a.max_q : n;
+  return Nodes{first, n};
+}
+
+// The workspace: sums of shares, and where each sequence's walk ends; of trees, what follows each node.
+struct End {
+  int node, kept;  // kept: drafted tokens
+  double before, after;  // the factor without and with the last refusal
+};
+struct Follow {
+  int next, pad;  // the child that is kept, or -1
+  double before, after;
+};
+struct Space {
+  End *ends;        // [batch]
+  Follow *follow;   // [batch][max_q], trees
+  int *gone;        // [batch][max_q], trees without a draft's rows: the node's token was taken from its parent's weights
+  double *sums;     // [batch][shares]
+};
+
+int64_t ends_bytes(int batch) { return (int64_t)batch * (int64_t)sizeof(End); }
+int64_t follow_bytes(int batch, int max_q) { return (int64_t)batch * max_q * (int64_t)sizeof(Follow); }
+int64_t gone_bytes(int batch, int max_q) { return ((int64_t)batch * max_q * 4 + 7) / 8 * 8; }
+
+// Whether the test of a point passes, with the weights as they are at first (what k_sums and k_branch ask alike).
+__device__ __forceinline__ bool passes(double u, double W, double q, double w) { return u * W * q < w; }
+
+// The point of a drafted token in its parent's rows.
+template <typename T, bool DRAFT>
+__device__ __forceinline__ void point_of(const VerifyArgs &a, int64_t row, int64_t x, double &p, double &q) {
+  p = weight_of(((const T *)a.target)[row * a.target_stride + x]);
+  q = DRAFT ? weight_of(((const T *)a.draft)[row * a.draft_stride + x]) : 1.0;
+}
+
+// ---- trees: what follows each node ----
+
+constexpr int BRANCH_THREADS = VERIFY_NODES;
+
+// The number of threads before this one for which v holds, and of all.
+__device__ __forceinline__ int block_rank(bool v, int *waves, int &total) {
+  const int lane = threadIdx.x % 64, wave = threadIdx.x / 64;
+  const uint64_t mask = __builtin_amdgcn_ballot_w64(v);
   __syncthreads();
-
-  // the walk, the same in every thread
-  int c = 0, kept = 0;
-  double W = 1.0;
-  Taken taken{factor, refused, 0};
-  bool open = false;  // the last refusal's sum is not known yet
-  auto settle = [&]() {
-    const Rows<T, DRAFT> rows(a, q0 + c);
-    const double left = sum_weights<T, DRAFT>(rows, taken, 0, rows.chunks, sums);
-    if (left > 0.0) W = left;
-    else --taken.count;
-    open = false;
-  };
-  for (int i = 1; i < nq; ++i) {
-    const int64_t x = token[i];
-    if (parent[i] != c || x < 0 || x >= a.vocab) continue;
-    if (open) settle();
-    double w = wp[i];
-    for (int j = 0; j < taken.count; ++j)
-      w = DRAFT ? fmax(w - factor[j] * wq[i], 0.0) : refused[j] == x ? 0.0 : w;
-    if (u[i] * W * wq[i] < w) {
-      if (t == 0) {
-        path[kept + 1] = i;
-        out[kept] = x;
-      }
-      c = i;
-      ++kept;
-      W = 1.0;
-      taken.count = 0;
-    } else {
-      __syncthreads();
-      if (t == 0) {
-        factor[taken.count] = W;
-        refused[taken.count] = (int)x;
-      }
-      __syncthreads();
-      ++taken.count;
-      open = true;
-    }
-  }
-
-  // the token after the last kept one
-  int64_t chosen = -1;
-  if (nq > 0) {
-    const Rows<T, DRAFT> rows(a, q0 + c);
-    double total = sum_weights<T, DRAFT>(rows, taken, 0, rows.chunks, sums);
-    if (!(total > 0.0) && open) {
-      --taken.count;
-      total = sum_weights<T, DRAFT>(rows, taken, 0, rows.chunks, sums);
-    }
-    if (total > 0.0) {
-      const double target = u[0] * total;
-      double before = 0.0;
-      const int wave = first_above(sums, VERIFY_WAVES, target, before);
-      const int per = (rows.chunks + VERIFY_WAVES - 1) / VERIFY_WAVES;
-      const int k0 = wave * per, k1 = k0 + per < rows.chunks ? k0 + per : rows.chunks;
-      // that wave's share again, a run of chunks for each thread
-      constexpr int N = Chunk<T>::N;
-      const int run = (k1 - k0 + VERIFY_THREADS - 1) / VERIFY_THREADS;
-      const int f = k0 + t * run, l = f + run < k1 ? f + run : k1;
-      double mine = 0.0;
-      for (int k = f; k < l; ++k) {
-        double w[N];
-        const Chunk<T> p = rows.read(rows.p, k, true), q = DRAFT ? rows.read(rows.q, k, rows.wide) : p;
-        weigh<T, DRAFT>(rows, taken, k, p, q, w);
+  if (lane == 0) waves[wave] = __builtin_popcountll(mask);
+  __syncthreads();
+  int before = 0;
+  total = 0;
 #pragma unroll
-        for (int i = 0; i < N; ++i) mine += w[i];
-      }
-      __syncthreads();
-      sums[t] = mine;
-      __syncthreads();
-      if (t == 0) {
-        const int who = first_above(sums, VERIFY_THREADS, target, before);
-        const int g = k0 + who * run, h = g + run < k1 ? g + run : k1;
-        double sum = before;
-        bool found = false;
-        for (int k = g; k < h && !found; ++k) {
-          double w[N];
-          const Chunk<T> p = rows.read(rows.p, k, true), q = DRAFT ? rows.read(rows.q, k, rows.wide) : p;
-          weigh<T, DRAFT>(rows, taken, k, p, q, w);
-          for (int i = 0; i < N && !found; ++i) {
-            sum += w[i];
-            if (w[i] > 0.0) chosen = (int64_t)k * N - rows.off + i;
-            found = sum > target && w[i] > 0.0;
-          }
-        }
-      }
-    }
+  for (int w = 0; w < BRANCH_THREADS / 64; ++w) {
+    before += w < wave ? waves[w] : 0;
+    total += waves[w];
   }
-  if (t == 0) a.counts[b] = nq > 0 ? kept + 1 : 0;
-  for (int i = t; i < a.max_q; i += VERIFY_THREADS) {
-    if (i == 0) path[0] = nq > 0 ? 0 : -1;
-    else if (i > kept || nq == 0) path[i] = -1;
-    if (i > kept || nq == 0) out[i] = -1;
-  }
-  if (t == 0 && nq > 0) out[kept] = chosen;
+  return before + __builtin_popcountll(mask & (((uint64_t)1 << lane) - 1));
 }
 
 template <typename T, bool DRAFT>
-hipError_t verify(const VerifyArgs &a, hipStream_t stream) {
-  if (a.parents) k_verify<T, DRAFT, true><<<a.batch, VERIFY_THREADS, 0, stream>>>(a);
-  else k_verify<T, DRAFT, false><<<a.batch, VERIFY_THREADS, 0, stream>>>(a);
+__global__ __launch_bounds__(BRANCH_THREADS) void k_branch(VerifyArgs a, Space space, int groups) {
+  __shared__ double u[VERIFY_NODES], wp[VERIFY_NODES], wq[VERIFY_NODES], sums[BRANCH_THREADS / 64];
+  __shared__ int token[VERIFY_NODES], parent[VERIFY_NODES], first[VERIFY_NODES], kids[VERIFY_NODES], list[VERIFY_NODES];
+  __shared__ int ranks[BRANCH_THREADS / 64];
+  __shared__ bool passed[VERIFY_NODES], open[VERIFY_NODES];
+  const int b = blockIdx.x / groups, group = blockIdx.x - b * groups, t = threadIdx.x;
+  const Nodes nodes = nodes_of(a, b);
+  if (nodes.count == 0) return;
+  Follow *follow = space.follow + (int64_t)b * a.max_q;
+  int *gone = space.gone + (int64_t)b * a.max_q;
+
+  bool asked = false;  // this thread's node has a parent that may ask it
+  first[t] = VERIFY_NODES;
+  kids[t] = 0;
+  parent[t] = -1;
+  if (t > 0 && t < nodes.count) {
+    const int64_t x = a.tokens[nodes.first + t];
+    const int up = a.parents[nodes.first + t];
+    u[t] = a.uniforms[nodes.first + t];
+    asked = up >= 0 && up < t && x >= 0 && x < a.vocab;
+    if (asked) {
+      double p, q;
+      point_of<T, DRAFT>(a, nodes.first + up, x, p, q);
+      wp[t] = p;
+      wq[t] = q;
+      token[t] = (int)x;
+      parent[t] = up;
+      passed[t] = passes(u[t], 1.0, q, p);
+    }
+  }
+  __syncthreads();
+  if (asked) {
+    atomicMin(first + parent[t], t);
+    atomicAdd(kids + parent[t], 1);
+  }
+  __syncthreads();
+  // whether a walk can come from the parent to here: as its first child that is kept, or behind a first that is not
+  if (asked) open[t] = first[parent[t]] == t ? passed[t] : !passed[first[parent[t]]];
+  __syncthreads();
+  int up = t;
+  while (up > 0 && parent[up] >= 0 && open[up]) up = parent[up];
+  const bool reached = t < nodes.count && up == 0;
+  const bool refused = kids[t] > 0 && !passed[first[t]];
+  const bool wanted = reached && refused && kids[t] > 1;
+  if (group == 0 && reached && !wanted) {
+    follow[t] = Follow{kids[t] > 0 && !refused ? first[t] : -1, 0, 0.0, refused ? 1.0 : 0.0};
+    if (!DRAFT && refused) gone[first[t]] = 1;
+  }
+  int count;
+  const int rank = block_rank(wanted, ranks, count);
+  if (wanted) list[rank] = t;
+  __syncthreads();
+
+  for (int l = group; l < count; l += groups) {
+    const int c = list[l];
+    const bool mine = asked && parent[t] == c;
+    int n;
+    const int place = block_rank(mine, ranks, n);
+    __syncthreads();
+    if (mine) kids[place] = t;  // the children of c in their order (numbers of children are not read any more)
+    __syncthreads();
+    const Rows<T, DRAFT> rows(a, nodes.first + c);
+    int next = -1;
+    double before = 0.0, after = 0.0, W = 1.0;
+    if (DRAFT) {
+      for (int k = 0; k < n; ++k) {
+        const int i = kids[k];
+        if (passes(u[i], W, wq[i], fmax(__builtin_fma(-before, wq[i], wp[i]), 0.0))) {
+          next = i;
+          break;
+        }
+        after = before + W;
+        if (k + 1 == n) break;
+        const double left = block_sum<BRANCH_THREADS>(
+            add_weights(rows, Taken{after, nullptr, 0}, 0, rows.chunks, BRANCH_THREADS, t), sums);
+        if (left > 0.0) before = after, W = left;
+      }
+    } else {
+      // the weights beside the children's tokens, once; W is that and those of the tokens that are left
+      __shared__ int tokens[VERIFY_NODES];
+      if (t < n) tokens[t] = token[kids[t]];
+      __syncthreads();
+      int *same = first;   // the first child (in the order) with the same token
+      bool *taken = open;  // by that child: its token was taken
+      if (t < n) {
+        int j = 0;
+        while (tokens[j] != tokens[t]) ++j;
+        same[t] = j;
+        taken[t] = false;
+      }
+      __syncthreads();
+      const bool counts = t < n && same[t] == t;
+      const double weight = counts ? wp[kids[t]] : 0.0;
+      const double others = block_sum<BRANCH_THREADS>(
+          add_weights(rows, Taken{0.0, tokens, n}, 0, rows.chunks, BRANCH_THREADS, t), sums);
+      for (int k = 0; k < n; ++k) {
+        const int i = kids[k], j = same[k];
+        if (passes(u[i], W, 1.0, taken[j] ? 0.0 : wp[i])) {
+          next = i;
+          break;
+        }
+        const double rest = others + block_sum<BRANCH_THREADS>(counts && !taken[t] && t != j ? weight : 0.0, sums);
+        const bool goes = rest > 0.0 || k + 1 == n;  // of the last one k_pick sees to it
+        if (goes) W = rest, after = 1.0;
+        if (t == 0) {
+          if (goes) taken[j] = true;
+          gone[i] = goes;
+        }
+        __syncthreads();
+      }
+    }
+    if (t == 0) follow[c] = Follow{next, 0, before, after};
+    __syncthreads();
+  }
+}
+
+// ---- the walk, and the sums at its end ----
+
+constexpr int SUM_THREADS = 256, ONE_THREADS = 1024;  // of k_sums beside k_pick, and of the kernel that is both
+
+// What was taken from the weights at a sequence's end node, without its last refusal if `all` does not hold.
+// list[VERIFY_NODES] and count are in LDS.
+template <int THREADS, typename T, bool DRAFT, bool TREE>
+__device__ __forceinline__ Taken taken_at(const VerifyArgs &a, const Space &space, int b, const Nodes &nodes,
+                                          const End &end, bool all, int *list, int *count) {
+  if (DRAFT) return Taken{all ? end.after : end.before, nullptr, 0};
+  if (threadIdx.x == 0) *count = 0;
+  __syncthreads();
+  if (end.after > 0.0) {
+    if (TREE) {
+      const int *gone = space.gone + (int64_t)b * a.max_q;
+      int last = 0;  // the last child that was asked
+      if (!all)
+        for (int i = end.node + 1; i < nodes.count; ++i) {
+          const int64_t x = a.tokens[nodes.first + i];
+          if (a.parents[nodes.first + i] == end.node && x >= 0 && x < a.vocab) last = i;
+        }
+      for (int i = end.node + 1 + threadIdx.x; i < nodes.count; i += THREADS) {
+        const int64_t x = a.tokens[nodes.first + i];
+        if (a.parents[nodes.first + i] == end.node && x >= 0 && x < a.vocab && i != last && gone[i])
+          list[atomicAdd(count, 1)] = (int)x;
+      }
+    } else if (all && threadIdx.x == 0) {
+      list[0] = (int)a.tokens[nodes.first + end.node + 1];
+      *count = 1;
+    }
+  }
+  __syncthreads();
+  return Taken{0.0, list, *count};
+}
+
+// Those of a list's tokens that lie in the chunks from .. to.
+template <int THREADS, typename T, bool DRAFT>
+__device__ __forceinline__ Taken near(const Rows<T, DRAFT> &rows, const Taken &taken, int from, int to, int *list,
+                                      int *count) {
+  if (DRAFT || taken.count == 0) return taken;
+  if (threadIdx.x == 0) *count = 0;
+  __syncthreads();
+  for (int j = threadIdx.x; j < taken.count; j += THREADS) {
+    const int k = (taken.tokens[j] + rows.off) / Rows<T, DRAFT>::N;
+    if (k >= from && k < to) list[atomicAdd(count, 1)] = taken.tokens[j];
+  }
+  __syncthreads();
+  return Taken{0.0, list, *count};
+}
+
+// The walk of sequence b; `write`: this workgroup puts out what is known from it.
+template <int THREADS, typename T, bool DRAFT, bool TREE>
+__device__ __forceinline__ End walk(const VerifyArgs &a, const Space &space, int b, const Nodes &nodes, bool write,
+                                    int *next) {
+  const int t = threadIdx.x;
+  int *path = a.path + (int64_t)b * a.max_q;
+  int64_t *out = a.out + (int64_t)b * a.max_q;
+  End end{0, 0, 0.0, 0.0};
+  if (TREE) {
+    const Follow *follow = space.follow + (int64_t)b * a.max_q;
+    for (int i = t; i < nodes.count; i += THREADS) next[i] = follow[i].next;
+    __syncthreads();
+    // what follows nodes that no walk reaches is not set, and not looked at
+    for (int i = nodes.count > 0 ? next[0] : -1; i >= 0; i = next[i]) {
+      end.node = i;
+      ++end.kept;
+      if (write && t == 0) {
+        path[end.kept] = i;
+        out[end.kept - 1] = a.tokens[nodes.first + i];
+      }
+    }
+    if (nodes.count > 0) end.before = follow[end.node].before, end.after = follow[end.node].after;
+  } else {
+    // the first node that is not kept, in each thread its own first
+    int stop = nodes.count;
+    bool there = false;  // its token is one of the vocabulary, and was refused
+    for (int i = 1 + t; i < nodes.count; i += THREADS) {
+      const int64_t x = a.tokens[nodes.first + i];
+      const bool in = x >= 0 && x < a.vocab;
+      bool keep = false;
+      if (in) {
+        double p, q;
+        point_of<T, DRAFT>(a, nodes.first + i - 1, x, p, q);
+        keep = passes(a.uniforms[nodes.first + i], 1.0, q, p);
+      }
+      if (!keep) {
+        stop = i;
+        there = in;
+        break;
+      }
+    }
+    int key = 2 * stop + there;
+#pragma unroll
+    for (int d = 32; d > 0; d /= 2) {
+      const int other = __shfl_xor(key, d);
+      key = other < key ? other : key;
+    }
+    if (t % 64 == 0) next[t / 64] = key;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < THREADS / 64; ++w) key = next[w] < key ? next[w] : key;
+    end.node = end.kept = nodes.count > 0 ? key / 2 - 1 : 0;
+    end.after = key & 1;
+    if (write)
+      for (int i = 1 + t; i <= end.kept; i += THREADS) {
+        path[i] = i;
+        out[i - 1] = a.tokens[nodes.first + i];
+      }
+  }
+  if (write) {
+    if (t == 0) a.counts[b] = nodes.count > 0 ? end.kept + 1 : 0;
+    for (int i = t; i < a.max_q; i += THREADS) {
+      if (i == 0) path[0] = nodes.count > 0 ? 0 : -1;
+      else if (i > end.kept) path[i] = -1;
+      if (i > end.kept || nodes.count == 0) out[i] = -1;
+    }
+  }
+  return end;
+}
+
+// The first thread of the workgroup whose running sum, after `before`, is above target (a thread without weight is
+// not), the last one with weight if rounding leaves none, -1 without any; `before` becomes the sum before it.
+template <int THREADS>
+__device__ __forceinline__ int first_above(double v, double target, double &before, double *waves, int *found) {
+  const int t = threadIdx.x, lane = t % 64, wave = t / 64;
+  double sum = v;
+#pragma unroll
+  for (int d = 1; d < 64; d *= 2) {
+    const double o = __shfl_up(sum, d);
+    if (lane >= d) sum += o;
+  }
+  __syncthreads();
+  if (lane == 63) waves[wave] = sum;
+  if (t == 0) found[0] = THREADS, found[1] = -1;
+  __syncthreads();
+  double base = before;
+  for (int w = 0; w < wave; ++w) base += waves[w];
+  const double after = base + sum;
+  const uint64_t above = __builtin_amdgcn_ballot_w64(v > 0.0 && after > target);
+  const uint64_t any = __builtin_amdgcn_ballot_w64(v > 0.0);
+  if (lane == 0 && above) atomicMin(found, 64 * wave + __builtin_ctzll(above));
+  if (lane == 0 && any) atomicMax(found + 1, 64 * wave + 63 - __builtin_clzll(any));
+  __syncthreads();
+  const int who = found[0] < THREADS ? found[0] : found[1];
+  if (t == who) waves[THREADS / 64] = after - v;
+  __syncthreads();
+  if (who >= 0) before = waves[THREADS / 64];
+  return who;
+}
+
+constexpr int MOST_SHARES = 4096;
+
+// A row's chunks in `shares` runs, one for a wave.
+struct Cut {
+  int shares;
+  __device__ __forceinline__ int at(int chunks, int s) const { return (int)((int64_t)chunks * s / shares); }
+};
+
+// The sampled token: the share that the goal lies in, then each thread's run of its chunks, then that run.  sums[] (LDS)
+// has the shares' sums.
+template <int THREADS, typename T, bool DRAFT, bool TREE>
+__device__ __forceinline__ void pick(const VerifyArgs &a, const Space &space, int b, const Nodes &nodes, const End &end,
+                                     Cut cut, double u, double *sums, double *waves, int *list, int *found) {
+  constexpr int N = Chunk<T>::N;
+  const int t = threadIdx.x;
+  const Rows<T, DRAFT> rows(a, nodes.first + end.node);
+  Taken taken = taken_at<THREADS, T, DRAFT, TREE>(a, space, b, nodes, end, true, list, found);
+  // a run of shares for each thread
+  const int some = (cut.shares + THREADS - 1) / THREADS, s0 = t * some;
+  auto shares = [&]() {
+    double v = 0.0;
+    for (int s = s0; s < s0 + some && s < cut.shares; ++s) v += sums[s];
+    return v;
+  };
+  double mine = shares(), total = block_sum<THREADS>(mine, waves);
+  if (!(total > 0.0) && end.after > end.before) {  // the last refusal would leave nothing: it takes nothing
+    taken = taken_at<THREADS, T, DRAFT, TREE>(a, space, b, nodes, end, false, list, found);
+    for (int s = t / 64; s < cut.shares; s += THREADS / 64) {
+      const double v =
+          wave_sum_f64(add_weights(rows, taken, cut.at(rows.chunks, s), cut.at(rows.chunks, s + 1), 64, t % 64));
+      if (t % 64 == 0) sums[s] = v;
+    }
+    __syncthreads();
+    mine = shares();
+    total = block_sum<THREADS>(mine, waves);
+  }
+  int64_t *out = a.out + (int64_t)b * a.max_q + end.kept;
+  if (!(total > 0.0)) {
+    if (t == 0) *out = -1;
+    return;
+  }
+  const double target = u * total;
+  double before = 0.0;
+  int share = 0;
+  {
+    const int who = first_above<THREADS>(mine, target, before, waves, found);
+    double sum = before;
+    for (int s = who * some; s < (who + 1) * some && s < cut.shares; ++s) {
+      if (!(sums[s] > 0.0)) continue;
+      share = s;
+      before = sum;
+      sum += sums[s];
+      if (sum > target) break;
+    }
+  }
+  const int k0 = cut.at(rows.chunks, share), k1 = cut.at(rows.chunks, share + 1);
+  const int run = (k1 - k0 + THREADS - 1) / THREADS;
+  const int f = (int64_t)k0 + (int64_t)t * run < k1 ? k0 + t * run : k1, l = k1 - f > run ? f + run : k1;
+  double w[N];
+  Chunk<T> p, q;
+  mine = 0.0;
+  for (int k = f; k < l; ++k) {
+    p = rows.read(rows.p, k, true);
+    q = DRAFT ? rows.read(rows.q, k, rows.wide) : p;
+    weigh<T, DRAFT>(rows, taken, k, p, q, w);
+#pragma unroll
+    for (int i = 0; i < N; ++i) mine += w[i];
+  }
+  const int who = first_above<THREADS>(mine, target, before, waves, found);
+  if (t != who) return;
+  double sum = before;
+  bool done = false;
+  int64_t chosen = -1;
+  for (int k = f; k < l && !done; ++k) {
+    if (run > 1) {  // (the one chunk is here already)
+      p = rows.read(rows.p, k, true);
+      q = DRAFT ? rows.read(rows.q, k, rows.wide) : p;
+      weigh<T, DRAFT>(rows, taken, k, p, q, w);
+    }
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      sum += w[i];
+      if (w[i] > 0.0 && !done) {
+        chosen = (int64_t)k * N - rows.off + i;
+        done = sum > target;
+      }
+    }
+  }
+  *out = chosen;
+}
+
+template <int THREADS, typename T, bool DRAFT, bool TREE, bool ONE>
+__global__ __launch_bounds__(THREADS) void k_sums(VerifyArgs a, Space space, Cut cut) {
+  constexpr int WAVES = THREADS / 64;
+  __shared__ double waves[WAVES + 1], sums[WAVES];
+  __shared__ int next[VERIFY_NODES], list[DRAFT ? 1 : VERIFY_NODES], few[DRAFT ? 1 : VERIFY_NODES], found[2];
+  const int groups = cut.shares / WAVES, b = blockIdx.x / groups, group = blockIdx.x - b * groups;
+  const int wave = threadIdx.x / 64;
+  const Nodes nodes = nodes_of(a, b);
+  const double u = ONE && nodes.count > 0 ? a.uniforms[nodes.first] : 0.0;
+  const End end = walk<THREADS, T, DRAFT, TREE>(a, space, b, nodes, group == 0, next);
+  if (!ONE && group == 0 && threadIdx.x == 0) space.ends[b] = end;
+  if (nodes.count == 0) return;
+  const Rows<T, DRAFT> rows(a, nodes.first + end.node);
+  const int s0 = group * WAVES, s = s0 + wave;
+  const Taken all = taken_at<THREADS, T, DRAFT, TREE>(a, space, b, nodes, end, true, list, found);
+  const Taken taken = near<THREADS>(rows, all, cut.at(rows.chunks, s0), cut.at(rows.chunks, s0 + WAVES), few, found + 1);
+  const double sum = wave_sum_f64(
+      add_weights(rows, taken, cut.at(rows.chunks, s), cut.at(rows.chunks, s + 1), 64, threadIdx.x % 64));
+  if (!ONE) {
+    if (threadIdx.x % 64 == 0) space.sums[(int64_t)b * cut.shares + s] = sum;
+    return;
+  }
+  if (threadIdx.x % 64 == 0) sums[wave] = sum;
+  __syncthreads();
+  pick<THREADS, T, DRAFT, TREE>(a, space, b, nodes, end, cut, u, sums, waves, list, found);
+}
+
+template <typename T, bool DRAFT, bool TREE>
+__global__ __launch_bounds__(SUM_THREADS) void k_pick(VerifyArgs a, Space space, Cut cut) {
+  __shared__ double sums[MOST_SHARES], waves[SUM_THREADS / 64 + 1];
+  __shared__ int list[DRAFT ? 1 : VERIFY_NODES], found[2];
+  const int b = blockIdx.x;
+  for (int s = threadIdx.x; s < cut.shares; s += SUM_THREADS) sums[s] = space.sums[(int64_t)b * cut.shares + s];
+  const End end = space.ends[b];
+  const Nodes nodes = nodes_of(a, b);
+  if (nodes.count == 0) return;
+  const double u = a.uniforms[nodes.first];
+  __syncthreads();
+  pick<SUM_THREADS, T, DRAFT, TREE>(a, space, b, nodes, end, cut, u, sums, waves, list, found);
+}
+
+// Shares of a row: those of one workgroup where it is short, else of 2048 entries at most, and as many as it takes for
+// two workgroups on every CU while a workgroup has 1024 entries.
+constexpr int ONE_ENTRIES = 1 << 15;
+
+bool one_kernel(const VerifyArgs &a) {
+  return a.vocab <= ONE_ENTRIES;
+}
+
+int shares_of(int batch, int vocab) {
+  constexpr int WAVES = SUM_THREADS / 64;
+  int64_t s = (vocab + 2048 * WAVES - 1) / (2048 * WAVES);  // workgroups
+  const int64_t fill = 2 * device_cu_count() / (batch > 0 ? batch : 1), most = vocab / 1024;
+  const int64_t more = fill < most ? fill : most;
+  s = s > more ? s : more;
+  if (batch > 0 && s > MAX_GROUPS_256 / batch) s = MAX_GROUPS_256 / batch;
+  return WAVES * (int)(s > MOST_SHARES / WAVES ? MOST_SHARES / WAVES : s < 1 ? 1 : s);
+}
+
+template <typename T, bool DRAFT, bool TREE>
+hipError_t verify(const VerifyArgs &a, const Space &space, bool one, hipStream_t stream) {
+  if (TREE && a.max_q > 0 && a.total_q > 0) {
+    // a workgroup for each node of a sequence, fewer of many sequences
+    int64_t per = 2 * device_cu_count() / a.batch;
+    per = per < 4 ? 4 : per;
+    if (per > a.max_q) per = a.max_q;
+    if (per > MAX_VERIFY / a.batch) per = MAX_VERIFY / a.batch;
+    k_branch<T, DRAFT><<<(unsigned)(per * a.batch), BRANCH_THREADS, 0, stream>>>(a, space, (int)per);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  if (one) {
+    k_sums<ONE_THREADS, T, DRAFT, TREE, true><<<(unsigned)a.batch, ONE_THREADS, 0, stream>>>(a, space,
+                                                                                            Cut{ONE_THREADS / 64});
+    return hipGetLastError();
+  }
+  const Cut cut{shares_of(a.batch, a.vocab)};
+  const unsigned grid = (unsigned)(cut.shares / (SUM_THREADS / 64) * (int64_t)a.batch);
+  k_sums<SUM_THREADS, T, DRAFT, TREE, false><<<grid, SUM_THREADS, 0, stream>>>(a, space, cut);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  k_pick<T, DRAFT, TREE><<<(unsigned)a.batch, SUM_THREADS, 0, stream>>>(a, space, cut);
   return hipGetLastError();
+}
+
+template <typename T>
+hipError_t verify(const VerifyArgs &a, const Space &space, bool one, hipStream_t stream) {
+  if (a.draft)
+    return a.parents ? verify<T, true, true>(a, space, one, stream) : verify<T, true, false>(a, space, one, stream);
+  return a.parents ? verify<T, false, true>(a, space, one, stream) : verify<T, false, false>(a, space, one, stream);
 }
 
 }  // namespace
 
-int64_t verify_workspace(int, int, int) { return 0; }
+int64_t verify_workspace(int batch, int max_q, int vocab) {
+  return ends_bytes(batch) + follow_bytes(batch, max_q) + gone_bytes(batch, max_q) +
+         (int64_t)batch * shares_of(batch, vocab) * 8;
+}
 
 hipError_t launch_verify(int dtype, const VerifyArgs &a, hipStream_t stream) {
-  if (dtype == 1) return a.draft ? verify<float, true>(a, stream) : verify<float, false>(a, stream);
-  return a.draft ? verify<unsigned short, true>(a, stream) : verify<unsigned short, false>(a, stream);
+  char *at = (char *)a.workspace;
+  Space space;
+  space.ends = (End *)at;
+  space.follow = (Follow *)(at += ends_bytes(a.batch));
+  space.gone = (int *)(at += follow_bytes(a.batch, a.max_q));
+  space.sums = (double *)(at += gone_bytes(a.batch, a.max_q));
+  const bool one = one_kernel(a);
+  return dtype == 1 ? verify<float>(a, space, one, stream) : verify<unsigned short>(a, space, one, stream);
 }
 
 }  // namespace mx

@@ -1,14 +1,14 @@
 """Verification of drafted tokens in exact rational arithmetic on the CPU, one sequence and one entry at a time: the
 plain reference of mx_verify.  Nothing here uses the library."""
-import math
 from fractions import Fraction
 
 import torch
 
 
 def row_of(t, r):
-    """Entries of a row as exact numbers; negative and not finite ones count as zero."""
-    return [Fraction(x) if math.isfinite(x) and x > 0 else Fraction(0) for x in t[r].double().tolist()]
+    """Entries of a row as exact numbers; negative ones and NaN count as zero, infinity as fp32's largest number."""
+    top = torch.finfo(torch.float32).max
+    return [Fraction(min(x, top)) if x > 0 else Fraction(0) for x in t[r].double().tolist()]
 
 
 def sequence(target, draft, tokens, uniforms, parents, first, n):

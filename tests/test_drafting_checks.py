@@ -146,6 +146,7 @@ def test_verify_refusals(b):
     assert verify(vocab=0) == ESHAPE
     assert verify(vocab=(1 << 30) + 1) == ESHAPE
     assert verify(batch=-1) == ESHAPE
+    assert verify(batch=1 << 22) == ESHAPE
     assert verify(total=-1) == ESHAPE
     assert verify(total=1 << 31) == ESHAPE
     assert verify(max_q=-1) == ESHAPE

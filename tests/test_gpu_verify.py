@@ -152,7 +152,8 @@ def test_nodes_that_are_passed_over(mx, draft):
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
 @pytest.mark.parametrize("draft", [False, True])
 def test_probabilities_that_are_none(mx, dtype, draft):
-    """NaN, infinities and negative entries count as zero, in the walk and in the sample; a row of nothing gives -1."""
+    """NaN and negative entries count as zero, infinity as the largest number, in the walk and in the sample; a row of
+    nothing gives -1."""
     c = Case([8, 8, 8, 8], 45, dtype, True, draft, seed=17)
     bad = torch.tensor([math.nan, math.inf, -math.inf, -0.25], dtype=dtype, device="cuda")
     for t in (c.target, c.draft):
