@@ -43,36 +43,48 @@ __device__ __forceinline__ Row row_of(const BookArgs &a, int r) {
   return Row{from, FORK ? full : need, need};
 }
 
-// Rows one by one, a wave each: pages are released or shared, and missing[row] is what the row lacks.
+// Entry `j` of row `r`, of which `was` is what the row that it comes from holds there: the page is released or shared.
+// True if the row lacks a page there.
+template <bool FORK>
+__device__ __forceinline__ bool settle(const BookArgs &a, const Row &row, int r, int j, int was) {
+  const bool held = (unsigned)was < (unsigned)a.pages;
+  int *dst = a.out + (int64_t)r * a.out_stride + j;
+  if (FORK) {
+    if (held) atomicAdd(a.refs + was, 1);
+    *dst = held ? was : -1;
+    return j < row.need && !held;
+  }
+  if (j < row.need) {
+    if (!held && was != -1) *dst = -1;
+    return !held;
+  }
+  // (a page that nobody holds stays free)
+  if (held && atomicSub(a.refs + was, 1) <= 0) atomicAdd(a.refs + was, 1);
+  if (was != -1) *dst = -1;
+  return false;
+}
+
+template <bool FORK>
+__device__ __forceinline__ int entry_of(const BookArgs &a, const Row &row, int j) {
+  return FORK && j >= row.keep ? -1 : a.table[(int64_t)row.from * a.stride + j];
+}
+
+__device__ __forceinline__ int beyond(const BookArgs &a, const Row &row) {  // pages that the row has no column for
+  return row.need > a.cols ? row.need - a.cols : 0;
+}
+
+// A wave has a row; missing[row] is what the row lacks.
 template <bool FORK>
 __global__ __launch_bounds__(256) void k_page_rows(BookArgs a) {
-  const int lane = threadIdx.x % 64;
-  const int r = blockIdx.x * 4 + threadIdx.x / 64;
+  const int r = blockIdx.x * 4 + threadIdx.x / 64, lane = threadIdx.x % 64;
   if (r >= a.out_rows) return;
   const Row row = row_of<FORK>(a, r);
-  const int *src = a.table + (int64_t)row.from * a.stride;
-  int *dst = a.out + (int64_t)r * a.out_stride;
   int lack = 0;
 #pragma unroll 4
-  for (int j = lane; j < a.cols; j += 64) {
-    const int was = FORK && j >= row.keep ? -1 : src[j];
-    const bool held = (unsigned)was < (unsigned)a.pages;
-    if (FORK) {
-      if (held) atomicAdd(a.refs + was, 1);
-      dst[j] = held ? was : -1;
-      lack += j < row.need && !held;
-    } else if (j < row.need) {
-      if (!held && was != -1) dst[j] = -1;
-      lack += !held;
-    } else {
-      // (a page that nobody holds stays free)
-      if (held && atomicSub(a.refs + was, 1) <= 0) atomicAdd(a.refs + was, 1);
-      if (was != -1) dst[j] = -1;
-    }
-  }
+  for (int j = lane; j < a.cols; j += 64) lack += settle<FORK>(a, row, r, j, entry_of<FORK>(a, row, j));
 #pragma unroll
   for (int d = 32; d > 0; d /= 2) lack += __shfl_xor(lack, d);
-  if (lane == 0) a.missing[r] = lack + (row.need > a.cols ? row.need - a.cols : 0);
+  if (lane == 0) a.missing[r] = lack + beyond(a, row);
 }
 
 constexpr int TAKE_THREADS = 1024, TAKE_ITEMS = 4;  // entries of a table that a step of the workgroup looks at: 4096
@@ -101,17 +113,109 @@ __device__ __forceinline__ int block_prefix(int v, int *waves, int &total) {
   return before + sum - v;
 }
 
+// Free pages, found from the lowest on.
+struct FreePages {
+  int *queue;                          // in LDS
+  int head = 0, size = 0, cursor = 0;  // of the queue; the first page that was not looked at
+
+  // At least `wanted` (up to a step's entries), if there are so many.
+  __device__ __forceinline__ void find(const BookArgs &a, int wanted, int *waves) {
+    while (size < wanted && cursor < a.pages) {
+      int found = 0;
+      unsigned free = 0;
+      const unsigned p0 = (unsigned)cursor + threadIdx.x * SCAN_ITEMS;
+#pragma unroll
+      for (int k = 0; k < SCAN_ITEMS; ++k) {
+        const unsigned p = p0 + k;
+        // atomic, as the changes of this kernel are, which a barrier has put before it
+        const bool is = p < (unsigned)a.pages &&
+                        __hip_atomic_load(a.refs + p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == 0;
+        free |= (unsigned)is << k;
+        found += is;
+      }
+      int all;
+      int at = head + size + block_prefix(found, waves, all);
+      for (; free; free &= free - 1, ++at) queue[at % QUEUE] = (int)(p0 + __builtin_ctz(free));
+      size += all;
+      cursor = cursor > a.pages - TAKE_THREADS * SCAN_ITEMS ? a.pages : cursor + TAKE_THREADS * SCAN_ITEMS;
+    }
+    __syncthreads();
+  }
+  // The page of this rank, or -1.
+  __device__ __forceinline__ int operator[](int rank) const { return rank < size ? queue[(head + rank) % QUEUE] : -1; }
+  __device__ __forceinline__ void drop(int count) {
+    count = count < size ? count : size;
+    head = (head + count) % QUEUE;
+    size -= count;
+    __syncthreads();  // the places that are free now are written by the next step
+  }
+};
+
+// Small tables: one workgroup sees to the rows and hands out pages.
+constexpr int SMALL_ROWS = 1024, SMALL_ITEMS = 16;  // rows; entries of a thread
+
+template <bool FORK>
+__global__ __launch_bounds__(TAKE_THREADS) void k_pages_small(BookArgs a) {
+  __shared__ int waves[TAKE_THREADS / 64], queue[QUEUE], lacks[SMALL_ROWS];
+  __shared__ Row rows[SMALL_ROWS];
+  __shared__ unsigned any;  // OR of the threads' wants
+  const int t = threadIdx.x, entries = a.out_rows * a.cols;
+  if (t < a.out_rows) {
+    rows[t] = row_of<FORK>(a, t);
+    lacks[t] = 0;
+  }
+  if (t == 0) any = 0u;
+  __syncthreads();
+  unsigned wants = 0;  // bit k: this thread's entry k lacks a page that is to be taken
+#pragma unroll
+  for (int k0 = 0; k0 < SMALL_ITEMS; k0 += 4) {
+    if (k0 * TAKE_THREADS >= entries) break;
+    int was[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int e = (k0 + k) * TAKE_THREADS + t, r = e / a.cols;
+      was[k] = e < entries ? entry_of<FORK>(a, rows[r], e - r * a.cols) : -1;
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int e = (k0 + k) * TAKE_THREADS + t, r = e / a.cols, j = e - r * a.cols;
+      if (e >= entries || !settle<FORK>(a, rows[r], r, j, was[k])) continue;
+      atomicAdd(lacks + r, 1);
+      wants |= (unsigned)(!FORK || j == rows[r].keep) << (k0 + k);
+    }
+  }
+  FreePages free{queue};
+  if (wants) atomicOr(&any, wants);
+  __syncthreads();
+  for (unsigned left = any; left; left &= left - 1) {  // in the order of the entries
+    const int k = __builtin_ctz(left);
+    const bool want = wants >> k & 1u;
+    int total;
+    const int rank = block_prefix(want, waves, total);
+    free.find(a, total, waves);
+    const int page = want ? free[rank] : -1;
+    if (page >= 0) {
+      const int e = k * TAKE_THREADS + t, r = e / a.cols;
+      a.out[(int64_t)r * a.out_stride + (e - r * a.cols)] = page;
+      a.refs[page] = 1;
+      atomicSub(lacks + r, 1);
+    }
+    free.drop(total);
+  }
+  __syncthreads();
+  if (t < a.out_rows) a.missing[t] = lacks[t] + beyond(a, rows[t]);
+}
+
 // One workgroup hands out pages: it goes over the entries that lack one in their order, and over refs for free ones.
 template <bool FORK>
 __global__ __launch_bounds__(TAKE_THREADS) void k_page_take(BookArgs a) {
-  __shared__ int waves[TAKE_THREADS / 64];
-  __shared__ int queue[QUEUE];
+  __shared__ int waves[TAKE_THREADS / 64], queue[QUEUE];
   int lack = 0, total;
   for (int r = threadIdx.x; r < a.out_rows; r += TAKE_THREADS) lack |= a.missing[r];
   block_prefix(lack != 0, waves, total);
   if (total == 0) return;
 
-  int head = 0, size = 0, cursor = 0;  // of the queue of free pages; the first page that was not looked at
+  FreePages free{queue};
   const int64_t cols = FORK ? 1 : a.cols, entries = a.out_rows * cols;
   for (int64_t base = 0; base < entries; base += TAKE_THREADS * TAKE_ITEMS) {
     int *place[TAKE_ITEMS], *miss[TAKE_ITEMS];
@@ -133,41 +237,17 @@ __global__ __launch_bounds__(TAKE_THREADS) void k_page_take(BookArgs a) {
       ++wants;
     }
     int rank = block_prefix(wants, waves, total);
-    while (size < total && cursor < a.pages) {
-      int found = 0;
-      unsigned free = 0;
-      const unsigned p0 = (unsigned)cursor + threadIdx.x * SCAN_ITEMS;
-#pragma unroll
-      for (int k = 0; k < SCAN_ITEMS; ++k) {
-        const unsigned p = p0 + k;
-        // past the first-level cache: other calls' counts, and those of the kernel before
-        const bool is = p < (unsigned)a.pages &&
-                        __hip_atomic_load(a.refs + p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == 0;
-        free |= (unsigned)is << k;
-        found += is;
-      }
-      int all;
-      int at = head + size + block_prefix(found, waves, all);
-      for (; free; free &= free - 1, ++at) queue[at % QUEUE] = (int)(p0 + __builtin_ctz(free));
-      size += all;
-      cursor = cursor > a.pages - TAKE_THREADS * SCAN_ITEMS ? a.pages : cursor + TAKE_THREADS * SCAN_ITEMS;
-    }
-    __syncthreads();
+    free.find(a, total, waves);
 #pragma unroll
     for (int k = 0; k < TAKE_ITEMS; ++k) {
       if (place[k] == nullptr) continue;
-      if (rank < size) {
-        const int page = queue[(head + rank) % QUEUE];
-        *place[k] = page;
-        a.refs[page] = 1;
-        atomicSub(miss[k], 1);
-      }
-      ++rank;
+      const int page = free[rank++];
+      if (page < 0) continue;
+      *place[k] = page;
+      a.refs[page] = 1;
+      atomicSub(miss[k], 1);
     }
-    const int gone = total < size ? total : size;
-    head = (head + gone) % QUEUE;
-    size -= gone;
-    __syncthreads();  // the queue's places that are free now are written by the next step
+    free.drop(total);
   }
 }
 
@@ -187,7 +267,8 @@ Moved moved(const CacheView &cv) {
 
 constexpr int MOVE_THREADS = 256, MOVE_UNROLL = 4;
 
-// A workgroup copies the pieces from .. to of one tensor's page.
+// A workgroup copies the pieces from .. to of one tensor's page.  PAST: what is written is not kept in the caches.
+template <bool PAST>
 __device__ __forceinline__ void copy_pieces(const u32x4 *src, u32x4 *dst, int64_t from, int64_t to) {
   for (int64_t i = from + threadIdx.x; i < to; i += MOVE_THREADS * MOVE_UNROLL) {
     u32x4 v[MOVE_UNROLL];
@@ -196,11 +277,15 @@ __device__ __forceinline__ void copy_pieces(const u32x4 *src, u32x4 *dst, int64_
       if (i + u * MOVE_THREADS < to) v[u] = src[i + u * MOVE_THREADS];
 #pragma unroll
     for (int u = 0; u < MOVE_UNROLL; ++u)
-      if (i + u * MOVE_THREADS < to) dst[i + u * MOVE_THREADS] = v[u];
+      if (i + u * MOVE_THREADS < to) {
+        if (PAST) __builtin_nontemporal_store(v[u], dst + i + u * MOVE_THREADS);
+        else dst[i + u * MOVE_THREADS] = v[u];
+      }
   }
 }
 
 // Part of `parts` workgroups of a page: each has its share of the codes and of the scales.
+template <bool PAST>
 __global__ __launch_bounds__(MOVE_THREADS) void k_copy_pages(Moved m, int64_t pages, int heads, const int *src,
                                                              const int *dst, int parts) {
   const int64_t n = blockIdx.x / parts;
@@ -211,8 +296,8 @@ __global__ __launch_bounds__(MOVE_THREADS) void k_copy_pages(Moved m, int64_t pa
   for (int v = 0; v < 2; ++v) {
     const int64_t codes = (int64_t)heads * m.code_pieces, scales = (int64_t)heads * m.scale_pieces;
     const u32x4 *c = m.codes[v] + from * codes, *s = m.scales[v] + from * scales;
-    copy_pieces(c, m.codes[v] + to * codes, codes * part / parts, codes * (part + 1) / parts);
-    copy_pieces(s, m.scales[v] + to * scales, scales * part / parts, scales * (part + 1) / parts);
+    copy_pieces<PAST>(c, m.codes[v] + to * codes, codes * part / parts, codes * (part + 1) / parts);
+    copy_pieces<PAST>(s, m.scales[v] + to * scales, scales * part / parts, scales * (part + 1) / parts);
   }
 }
 
@@ -227,7 +312,7 @@ __global__ __launch_bounds__(MOVE_THREADS) void k_copy_last(Moved m, BookArgs a,
   const int tokens = a.kv_lens[row.from] & ((1 << a.page_log2) - 1);
   const int v = blockIdx.y, codes = m.code_pieces >> a.page_log2;  // pieces of a token
   const int64_t f = (int64_t)from * heads + head, t = (int64_t)to * heads + head;
-  copy_pieces(m.codes[v] + f * m.code_pieces, m.codes[v] + t * m.code_pieces, 0, tokens * codes);
+  copy_pieces<false>(m.codes[v] + f * m.code_pieces, m.codes[v] + t * m.code_pieces, 0, tokens * codes);
   const uint8_t *s = (const uint8_t *)(m.scales[v] + f * m.scale_pieces);
   uint8_t *d = (uint8_t *)(m.scales[v] + t * m.scale_pieces);
   for (int g = 0; g < scale_rows; ++g)
@@ -240,47 +325,65 @@ struct CompactArgs {
   const int *kv_starts, *keep, *counts, *table;
   int64_t keep_stride, stride;
   int *kv_lens;
-  int max_keep, cols;
+  int max_keep, cols, code_parts, scale_parts;  // parts: workgroups that share a head's tokens
 };
 
 constexpr int COMPACT_THREADS = 1024, COMPACT_UNROLL = 4;
+constexpr int COMPACT_TABLE = 4096;  // entries of the table in LDS
 
-// A workgroup has one head of one sequence, its keys' or values' codes or scales, whose tokens it takes in groups: all
-// of a group is read before any of it is written, and as keep[i] >= i no group writes what a later one reads.  So the
-// tokens may be moved within their own pages, and every place has what place keep[i] held at the beginning.
-// T: what a thread moves of a token, of which there are `per` pieces.
+// A workgroup has some of the pieces of one head's tokens of one sequence, its keys' or values' codes or scales, and
+// takes the tokens in groups: all of a group is read before any of it is written, and as keep[i] >= i no group writes
+// what a later one reads.  So the tokens may be moved within their own pages, and every place has what place keep[i] held
+// at the beginning.
+// T: what a thread moves of a token, of which there are `per` pieces; this workgroup has those from piece0 to piece1.
 template <typename T>
-__device__ __forceinline__ void compact(const CompactArgs &a, T *data, int per, bool planes, int b, int head) {
+__device__ __forceinline__ void compact(const CompactArgs &a, T *data, int per, int piece0, int piece1, bool planes,
+                                        int b, int head) {
+  __shared__ int near[COMPACT_TABLE];
   const CacheView &cv = a.cache;
   const int64_t start = a.kv_starts[b];
   const int *table = a.table + (int64_t)b * a.stride, *keep = a.keep + (int64_t)b * a.keep_stride;
   int count = a.counts[b];
   count = count < a.max_keep ? count : a.max_keep;
-  const int group = COMPACT_THREADS / per, token = threadIdx.x / per, piece = threadIdx.x - token * per;
+  const int mine = piece1 - piece0, group = COMPACT_THREADS / mine;
+  const int token = threadIdx.x / mine, piece = piece0 + threadIdx.x - token * mine;
   const int64_t room = (int64_t)a.cols << cv.page_log2;
   const int mask = (1 << cv.page_log2) - 1;
+  int next[COMPACT_UNROLL];  // entries of `keep` for the next group
+  auto look_up = [&](int64_t base) {
+#pragma unroll
+    for (int u = 0; u < COMPACT_UNROLL; ++u) {
+      const int64_t i = base + (int64_t)u * group + token;
+      next[u] = token < group && i < count ? keep[i] : -1;
+    }
+  };
+  look_up(0);
+  // the table from the first place on, as far as it goes
+  const int page0 = start < 0 ? 0 : start >= room ? a.cols : (int)(start >> cv.page_log2);
+  for (int j = threadIdx.x; j < COMPACT_TABLE && j < a.cols - page0; j += COMPACT_THREADS) near[j] = table[page0 + j];
+  __syncthreads();
   auto at = [&](int64_t place) -> int64_t {  // -1: no such place
     if (place < 0 || place >= room) return -1;
-    const int page = table[place >> cv.page_log2];
+    const int j = (int)(place >> cv.page_log2) - page0;
+    const int page = (unsigned)j < COMPACT_TABLE ? near[j] : table[page0 + j];
     if ((unsigned)page >= (uint64_t)cv.pages) return -1;
     const int64_t ph = (int64_t)page * cv.heads + head;
     const int r = (int)place & mask;
     return planes ? ((ph * per + piece) << cv.page_log2) + r : ((ph << cv.page_log2) + r) * per + piece;
   };
-  for (int base = 0; base < count; base += group * COMPACT_UNROLL) {
+  for (int64_t base = 0; base < count; base += group * COMPACT_UNROLL) {
     T v[COMPACT_UNROLL];
     int64_t to[COMPACT_UNROLL];
 #pragma unroll
     for (int u = 0; u < COMPACT_UNROLL; ++u) {
       const int64_t i = base + (int64_t)u * group + token;
       to[u] = -1;
-      if (token >= group || i >= count) continue;
-      const int k = keep[i];
-      if (k <= i) continue;  // it is where it belongs, or cannot be moved
-      const int64_t from = at(start + k);
+      if (next[u] <= i) continue;  // it is where it belongs, or cannot be moved
+      const int64_t from = at(start + next[u]);
       to[u] = from < 0 ? -1 : at(start + i);
       if (to[u] >= 0) v[u] = data[from];
     }
+    look_up(base + group * COMPACT_UNROLL);
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // what this wave reads has arrived
     __syncthreads();
 #pragma unroll
@@ -291,11 +394,14 @@ __device__ __forceinline__ void compact(const CompactArgs &a, T *data, int per, 
 
 __global__ __launch_bounds__(COMPACT_THREADS) void k_compact(CompactArgs a) {
   const CacheView &cv = a.cache;
-  const int b = blockIdx.x / cv.heads, head = blockIdx.x - b * cv.heads, v = blockIdx.y % 2;
-  if (blockIdx.y >= 2) {
-    compact<uint8_t>(a, cv.scales[v], cv.dim / 32, true, b, head);
+  const int b = blockIdx.x / cv.heads, head = blockIdx.x - b * cv.heads, v = blockIdx.y % 2, part = blockIdx.y / 2;
+  if (part >= a.code_parts) {
+    const int per = cv.dim / 32, p = part - a.code_parts;
+    compact<uint8_t>(a, cv.scales[v], per, per * p / a.scale_parts, per * (p + 1) / a.scale_parts, true, b, head);
   } else {
-    compact<u32x4>(a, (u32x4 *)cv.codes[v], (cv.fmt == 0 ? cv.dim / 2 : cv.dim) / 16, false, b, head);
+    const int per = (cv.fmt == 0 ? cv.dim / 2 : cv.dim) / 16;
+    compact<u32x4>(a, (u32x4 *)cv.codes[v], per, per * part / a.code_parts, per * (part + 1) / a.code_parts, false, b,
+                   head);
     if (blockIdx.y == 0 && head == 0 && threadIdx.x == 0) {
       const int count = a.counts[b] < a.max_keep ? a.counts[b] : a.max_keep;
       a.kv_lens[b] = a.kv_starts[b] + (count < 0 ? 0 : count);
@@ -311,6 +417,10 @@ BookArgs book(const CacheView &cv, int *refs, const int *table, int64_t stride, 
 
 template <bool FORK>
 hipError_t hand_out(const BookArgs &a, hipStream_t stream) {
+  if (a.out_rows <= SMALL_ROWS && (int64_t)a.out_rows * a.cols <= TAKE_THREADS * SMALL_ITEMS) {
+    k_pages_small<FORK><<<1, TAKE_THREADS, 0, stream>>>(a);
+    return hipGetLastError();
+  }
   k_page_rows<FORK><<<(a.out_rows + 3) / 4, 256, 0, stream>>>(a);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
@@ -338,20 +448,38 @@ hipError_t launch_cache_fork(const CacheView &cache, int *refs, const int *table
   return hipGetLastError();
 }
 
+// Copies of so many bytes are written past the caches, which they would empty: 94 MB take 32 us so and 41 otherwise, but
+// 18 MB that are compacted afterwards 33 with the compaction, and 26 out of the caches.
+constexpr int64_t PAST_BYTES = (int64_t)64 << 20;
+
 hipError_t launch_cache_copy(const CacheView &cache, const int *src, const int *dst, int64_t count, hipStream_t stream) {
   const Moved m = moved(cache);
   // a workgroup's share: 4 pieces for each thread, while the grid holds them
   int64_t parts = ((int64_t)cache.heads * m.code_pieces + MOVE_THREADS * MOVE_UNROLL - 1) / (MOVE_THREADS * MOVE_UNROLL);
   if (parts > MAX_GROUPS_256 / count) parts = MAX_GROUPS_256 / count;
-  k_copy_pages<<<(unsigned)(count * parts), MOVE_THREADS, 0, stream>>>(m, cache.pages, cache.heads, src, dst, (int)parts);
+  const unsigned grid = (unsigned)(count * parts);
+  if (2 * 16 * (int64_t)cache.heads * (m.code_pieces + m.scale_pieces) * count >= PAST_BYTES)
+    k_copy_pages<true><<<grid, MOVE_THREADS, 0, stream>>>(m, cache.pages, cache.heads, src, dst, (int)parts);
+  else
+    k_copy_pages<false><<<grid, MOVE_THREADS, 0, stream>>>(m, cache.pages, cache.heads, src, dst, (int)parts);
   return hipGetLastError();
 }
 
 hipError_t launch_cache_compact(const CacheView &cache, const int *kv_starts, const int *keep, int64_t keep_stride,
                                 int max_keep, const int *counts, const int *table, int64_t stride, int pages, int batch,
                                 int *kv_lens, hipStream_t stream) {
-  const CompactArgs a{cache, kv_starts, keep, counts, table, keep_stride, stride, kv_lens, max_keep, pages};
-  k_compact<<<dim3((unsigned)(batch * cache.heads), 4), COMPACT_THREADS, 0, stream>>>(a);
+  // long lists of few heads are shared by the pieces of a token, down to one each, until every CU has a workgroup
+  const int codes = (cache.fmt == 0 ? cache.dim / 2 : cache.dim) / 16, scales = cache.dim / 32;
+  CompactArgs a{cache, kv_starts, keep, counts, table, keep_stride, stride, kv_lens, max_keep, pages, 1, 1};
+  const int64_t heads = (int64_t)batch * cache.heads;
+  const auto groups = [](int parts) { return COMPACT_THREADS * COMPACT_UNROLL * parts; };
+  while (a.code_parts < codes && 2 * heads * a.code_parts < device_cu_count() &&
+         (int64_t)max_keep * codes > groups(a.code_parts))
+    a.code_parts = 2 * a.code_parts < codes ? 2 * a.code_parts : codes;
+  while (a.scale_parts < scales && 2 * heads * a.scale_parts < device_cu_count() &&
+         (int64_t)max_keep * scales > groups(a.scale_parts))
+    a.scale_parts = 2 * a.scale_parts < scales ? 2 * a.scale_parts : scales;
+  k_compact<<<dim3((unsigned)heads, (unsigned)(2 * (a.code_parts + a.scale_parts))), COMPACT_THREADS, 0, stream>>>(a);
   return hipGetLastError();
 }
 
