@@ -368,7 +368,7 @@ MX_API int64_t mx_cache_attention_workspace(const mx_cache *cache, int64_t q_hea
   if (st) return st;
   if (max_q > total_q) max_q = total_q;
   return mx::attention_workspace(cache->fmt, cache->dim, cache->heads, (int)(q_heads / cache->heads), (int)batch,
-                                 total_q, max_q, max_kv);
+                                 total_q, max_q, max_kv, false);
 }
 
 namespace {
@@ -396,7 +396,7 @@ int attention(const mx_cache *cache, const void *q, int64_t q_token_stride, int6
   const int group = (int)(q_heads / cache->heads);
   if (max_q > total_q) max_q = total_q;
   const int64_t need = mx::attention_workspace(cache->fmt, cache->dim, cache->heads, group, (int)batch, total_q, max_q,
-                                               max_kv);
+                                               max_kv, all);
   if (need > 0 && !workspace) return MX_ENULL;
   if (workspace_bytes < need) return MX_EARG;
   if (need > 0 && !aligned(workspace, 16)) return MX_EALIGN;

@@ -373,8 +373,8 @@ inline hipError_t allow_lds(const void *kernel, int bytes, std::atomic<uint64_t>
   return e;
 }
 
-Division attention_division_rows(int dim, int heads, int group, int batch, int64_t max_q, int64_t max_kv);
-Division attention_division_tiles(int dim, int heads, int group, int batch, int64_t max_q, int64_t max_kv);
+Division attention_division_rows(int dim, int heads, int group, int batch, int64_t max_q, int64_t max_kv, bool all);
+Division attention_division_tiles(int dim, int heads, int group, int batch, int64_t max_q, int64_t max_kv, bool all);
 hipError_t launch_attention_rows(const AttentionArgs &a, const Division &d, hipStream_t stream);
 hipError_t launch_attention_tiles(const AttentionArgs &a, const Division &d, hipStream_t stream);
 

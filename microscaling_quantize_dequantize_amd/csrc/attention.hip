@@ -75,17 +75,18 @@ __global__ __launch_bounds__(WIDE ? 1024 : 256) void k_join(AttentionArgs a, Div
 }
 
 // The few-rows kernel as far as its registers go: a row more and a tile's conversion serves 128.
-static Division division_of(int dim, int heads, int group, int batch, int64_t max_q, int64_t max_kv, bool *tiled) {
+static Division division_of(int dim, int heads, int group, int batch, int64_t max_q, int64_t max_kv, bool all,
+                            bool *tiled) {
   *tiled = max_q * group > (dim > 128 ? 16 : 32);
-  return *tiled ? attention_division_tiles(dim, heads, group, batch, max_q, max_kv)
-                : attention_division_rows(dim, heads, group, batch, max_q, max_kv);
+  return *tiled ? attention_division_tiles(dim, heads, group, batch, max_q, max_kv, all)
+                : attention_division_rows(dim, heads, group, batch, max_q, max_kv, all);
 }
 
 int64_t attention_workspace(int fmt, int dim, int heads, int group, int batch, int64_t total_q, int64_t max_q,
-                            int64_t max_kv) {
+                            int64_t max_kv, bool all) {
   if (batch == 0 || total_q == 0 || max_q == 0) return 0;
   bool tiled;
-  const Division d = division_of(dim, heads, group, batch, max_q, max_kv, &tiled);
+  const Division d = division_of(dim, heads, group, batch, max_q, max_kv, all, &tiled);
   if (d.workers == 0) return 0;
   return 2 * (int64_t)d.workers * d.rows * (dim + 2) * 4 + (int64_t)d.records * (int64_t)sizeof(Record);
 }
@@ -115,7 +116,7 @@ hipError_t launch_cache_attention(const AttentionArgs &a, hipStream_t stream) {
   }
   bool tiled;
   const Division d =
-      division_of(a.cache.dim, a.cache.heads, a.group, a.batch, a.max_q, a.max_kv, &tiled);
+      division_of(a.cache.dim, a.cache.heads, a.group, a.batch, a.max_q, a.max_kv, a.all, &tiled);
   const hipError_t e = tiled ? launch_attention_tiles(a, d, stream) : launch_attention_rows(a, d, stream);
   if (e != hipSuccess || d.workers == 0) return e;
   switch (a.cache.dim) {
@@ -130,7 +131,7 @@ hipError_t launch_cache_attention(const AttentionArgs &a, hipStream_t stream) {
 
 // The division for a kernel of `rows` rows a block, with this many workers as long as they have runs of min_tiles.
 static Division divide(int rows, int64_t workers, int min_tiles, int heads, int group, int batch, int64_t max_q,
-                       int64_t max_kv) {
+                       int64_t max_kv, bool all, int64_t held, int cost) {
   Division d;
   d.rows = rows;
   d.min_tiles = min_tiles;
@@ -139,7 +140,13 @@ static Division divide(int rows, int64_t workers, int min_tiles, int heads, int 
   const int64_t items = (int64_t)batch * heads * d.blocks;
   const double most = __builtin_ceil((double)items * d.tiles / min_tiles);
   // a launch has fewer than 2^32 threads: with too many items of up to 512 the work is divided all the same
-  d.workers = d.tiles <= min_tiles && items < ((int64_t)1 << 32) / 512
+  // Where all of a sequence's tokens are seen (states of an encoder, a few thousand as a rule) items are alike, and what a
+  // division costs, `cost` tiles of a workgroup, is often more than the rounds of whole items lose.  (256 items of 224
+  // rows, heads of 64: 44 us undivided and 58 divided for 1500 tokens, 80 and 91 for 3000; 64 such items 41 and 34, 73
+  // and 47; 512 items of one row 22 and 40, 35 and 58.)  Up to 4096 tokens: one long sequence may be among short ones.
+  const int64_t rounds = (items + held - 1) / held;
+  const bool whole = all && d.tiles <= 64 && (rounds * held - items) * d.tiles <= cost * held;
+  d.workers = (d.tiles <= min_tiles || whole) && items < ((int64_t)1 << 32) / 512
                   ? 0
                   : (int)((double)workers < most ? workers : (int64_t)most);
   d.by_worker = items > d.workers;
@@ -147,23 +154,24 @@ static Division divide(int rows, int64_t workers, int min_tiles, int heads, int 
   return d;
 }
 
-Division attention_division_rows(int dim, int heads, int group, int batch, int64_t max_q, int64_t max_kv) {
+Division attention_division_rows(int dim, int heads, int group, int batch, int64_t max_q, int64_t max_kv, bool all) {
   const int rows = max_q * group <= 16 ? 16 : 32;
   // One run for every workgroup that the CUs hold at once (rows_held); of several sequences,
   // whose lengths differ as a rule, two, so that a CU that has finished early takes another: 64 ragged sequences in
   // MXFP8 224 us against 235 with one run each, 64 equal ones 384 against 381, one of 500000 tokens 129 against 120.
   const int64_t held = rows_held(dim, rows / 16) * (int64_t)device_cu_count();
-  return divide(rows, batch > 1 ? 2 * held : held, 4, heads, group, batch, max_q, max_kv);
+  return divide(rows, batch > 1 ? 2 * held : held, 4, heads, group, batch, max_q, max_kv, all, held, 32);
 }
 
-Division attention_division_tiles(int dim, int heads, int group, int batch, int64_t max_q, int64_t max_kv) {
+Division attention_division_tiles(int dim, int heads, int group, int batch, int64_t max_q, int64_t max_kv, bool all) {
   // More rows share a tile's conversion in blocks of 256 (the 512 rows of 8192 tokens: 184 us against 196 in blocks of
   // 128), for which heads of more than 128 dimensions have no registers.  One workgroup for every CU, or two of the
   // small ones (64 rows over 32768 tokens: 201 us against 309 with one), in runs of eight tiles at least: a piece costs
   // as much as seven of them (512 tokens 30 us against 45 in runs of two tiles).
   const int rows = max_q * group <= 128 || dim > 128 ? 128 : 256;
-  const int64_t held = (rows == 128 && dim <= 128 ? 2 : 1) * (int64_t)device_cu_count();
-  return divide(rows, held, 8, heads, group, batch, max_q, max_kv);
+  const int two = rows == 128 && dim <= 128;
+  const int64_t held = (1 + two) * (int64_t)device_cu_count();
+  return divide(rows, held, 8, heads, group, batch, max_q, max_kv, all, held, two ? 20 : 13);
 }
 
 }  // namespace mx

@@ -100,7 +100,7 @@ struct AttentionArgs {
 };
 
 int64_t attention_workspace(int fmt, int dim, int heads, int group, int batch, int64_t total_q, int64_t max_q,
-                            int64_t max_kv);
+                            int64_t max_kv, bool all);
 hipError_t launch_cache_attention(const AttentionArgs &a, hipStream_t stream);
 
 // The cache's pages: tables [rows][pages] with rows `stride` apart, refs[page] holders of each page.

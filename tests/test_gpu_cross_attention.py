@@ -94,10 +94,11 @@ def test_nan_behind_the_sequence_stays_there(mx, nq):
     check(c, out)
 
 
-def test_causal_calls_are_what_they_were(mx):
-    """One query is the last token: both calls are the same then."""
+def test_one_query_is_the_causal_call(mx):
+    """It is the last token then, so both calls have the same value (their work may be divided in other ways)."""
     c = Case(mx, 0, 2, 4, 128, 32, [700, 31, 64], [1, 1, 1], seed=3)
-    assert torch.equal(run(mx, c), c.run(mx))
+    c.check(run(mx, c))
+    check(c, c.run(mx))
 
 
 def test_streams_and_replays(mx):
