@@ -129,6 +129,8 @@ hipError_t launch_cache_attention(const AttentionArgs &a, hipStream_t stream) {
   }
 }
 
+constexpr int WHOLE_TILES = 64;  // up to which items are not divided where queries see all tokens
+
 // The division for a kernel of `rows` rows a block, with this many workers as long as they have runs of min_tiles.
 static Division divide(int rows, int64_t workers, int min_tiles, int heads, int group, int batch, int64_t max_q,
                        int64_t max_kv, bool all, int64_t held, int cost) {
@@ -145,7 +147,7 @@ static Division divide(int rows, int64_t workers, int min_tiles, int heads, int 
   // rows, heads of 64: 44 us undivided and 58 divided for 1500 tokens, 80 and 91 for 3000; 64 such items 41 and 34, 73
   // and 47; 512 items of one row 22 and 40, 35 and 58.)  Up to 4096 tokens: one long sequence may be among short ones.
   const int64_t rounds = (items + held - 1) / held;
-  const bool whole = all && d.tiles <= 64 && (rounds * held - items) * d.tiles <= cost * held;
+  const bool whole = all && d.tiles <= WHOLE_TILES && (rounds * held - items) * d.tiles <= cost * held;
   d.workers = (d.tiles <= min_tiles || whole) && items < ((int64_t)1 << 32) / 512
                   ? 0
                   : (int)((double)workers < most ? workers : (int64_t)most);
@@ -168,7 +170,9 @@ Division attention_division_tiles(int dim, int heads, int group, int batch, int6
   // 128), for which heads of more than 128 dimensions have no registers.  One workgroup for every CU, or two of the
   // small ones (64 rows over 32768 tokens: 201 us against 309 with one), in runs of eight tiles at least: a piece costs
   // as much as seven of them (512 tokens 30 us against 45 in runs of two tiles).
-  const int rows = max_q * group <= 128 || dim > 128 ? 128 : 256;
+  // Whole items are better smaller: 320 of up to 224 rows, heads of 64, 1500 tokens 63 us and 84 in blocks of 256.
+  const bool small = all && max_kv <= WHOLE_TILES * TILE;
+  const int rows = max_q * group <= 128 || dim > 128 || small ? 128 : 256;
   const int two = rows == 128 && dim <= 128;
   const int64_t held = (1 + two) * (int64_t)device_cu_count();
   return divide(rows, held, 8, heads, group, batch, max_q, max_kv, all, held, two ? 20 : 13);
