@@ -89,7 +89,7 @@ __global__ __launch_bounds__(256) void k_page_rows(BookArgs a) {
 
 constexpr int TAKE_THREADS = 1024, TAKE_ITEMS = 4;  // entries of a table that a step of the workgroup looks at: 4096
 constexpr int SCAN_ITEMS = 8;                       // counts of holders: 8192
-constexpr int QUEUE = TAKE_THREADS * (TAKE_ITEMS + SCAN_ITEMS);
+constexpr int queue_of(int items) { return TAKE_THREADS * (items + SCAN_ITEMS); }  // pages, for steps of so many items a thread
 
 // The sum of v over the threads before this one, and over all of them (total).
 __device__ __forceinline__ int block_prefix(int v, int *waves, int &total) {
@@ -113,12 +113,14 @@ __device__ __forceinline__ int block_prefix(int v, int *waves, int &total) {
   return before + sum - v;
 }
 
-// Free pages, found from the lowest on.
+// Free pages, found from the lowest on, for steps that want ITEMS for each thread at most.
+template <int ITEMS>
 struct FreePages {
+  static constexpr int QUEUE = queue_of(ITEMS);
   int *queue;                          // in LDS
   int head = 0, size = 0, cursor = 0;  // of the queue; the first page that was not looked at
 
-  // At least `wanted` (up to a step's entries), if there are so many.
+  // At least `wanted`, if there are so many.
   __device__ __forceinline__ void find(const BookArgs &a, int wanted, int *waves) {
     while (size < wanted && cursor < a.pages) {
       int found = 0;
@@ -156,7 +158,7 @@ constexpr int SMALL_ROWS = 1024, SMALL_ITEMS = 16;  // rows; entries of a thread
 
 template <bool FORK>
 __global__ __launch_bounds__(TAKE_THREADS) void k_pages_small(BookArgs a) {
-  __shared__ int waves[TAKE_THREADS / 64], queue[QUEUE], lacks[SMALL_ROWS];
+  __shared__ int waves[TAKE_THREADS / 64], queue[queue_of(1)], lacks[SMALL_ROWS];
   __shared__ Row rows[SMALL_ROWS];
   __shared__ unsigned any;  // OR of the threads' wants
   const int t = threadIdx.x, entries = a.out_rows * a.cols;
@@ -184,7 +186,7 @@ __global__ __launch_bounds__(TAKE_THREADS) void k_pages_small(BookArgs a) {
       wants |= (unsigned)(!FORK || j == rows[r].keep) << (k0 + k);
     }
   }
-  FreePages free{queue};
+  FreePages<1> free{queue};
   if (wants) atomicOr(&any, wants);
   __syncthreads();
   for (unsigned left = any; left; left &= left - 1) {  // in the order of the entries
@@ -209,13 +211,13 @@ __global__ __launch_bounds__(TAKE_THREADS) void k_pages_small(BookArgs a) {
 // One workgroup hands out pages: it goes over the entries that lack one in their order, and over refs for free ones.
 template <bool FORK>
 __global__ __launch_bounds__(TAKE_THREADS) void k_page_take(BookArgs a) {
-  __shared__ int waves[TAKE_THREADS / 64], queue[QUEUE];
+  __shared__ int waves[TAKE_THREADS / 64], queue[queue_of(TAKE_ITEMS)];
   int lack = 0, total;
   for (int r = threadIdx.x; r < a.out_rows; r += TAKE_THREADS) lack |= a.missing[r];
   block_prefix(lack != 0, waves, total);
   if (total == 0) return;
 
-  FreePages free{queue};
+  FreePages<TAKE_ITEMS> free{queue};
   const int64_t cols = FORK ? 1 : a.cols, entries = a.out_rows * cols;
   for (int64_t base = 0; base < entries; base += TAKE_THREADS * TAKE_ITEMS) {
     int *place[TAKE_ITEMS], *miss[TAKE_ITEMS];
