@@ -168,7 +168,7 @@ __global__ __launch_bounds__(TAKE_THREADS) void k_pages_small(BookArgs a) {
   }
   if (t == 0) any = 0u;
   __syncthreads();
-  unsigned wants = 0;  // bit k: this thread's entry k lacks a page that is to be taken
+  unsigned wants = 0;  // bit k: this thread's entry k lacks a page
 #pragma unroll
   for (int k0 = 0; k0 < SMALL_ITEMS; k0 += 4) {
     if (k0 * TAKE_THREADS >= entries) break;
@@ -183,10 +183,23 @@ __global__ __launch_bounds__(TAKE_THREADS) void k_pages_small(BookArgs a) {
       const int e = (k0 + k) * TAKE_THREADS + t, r = e / a.cols, j = e - r * a.cols;
       if (e >= entries || !settle<FORK>(a, rows[r], r, j, was[k])) continue;
       atomicAdd(lacks + r, 1);
-      wants |= (unsigned)(!FORK || j == rows[r].keep) << (k0 + k);
+      wants |= 1u << (k0 + k);
     }
   }
   FreePages<1> free{queue};
+  if (FORK) {  // a page each for the rows whose last one is not full
+    const bool want = t < a.out_rows && rows[t].keep < rows[t].need && rows[t].keep < a.cols;
+    int total;
+    const int rank = block_prefix(want, waves, total);
+    free.find(a, total, waves);
+    const int page = want ? free[rank] : -1;
+    if (page >= 0) {
+      a.out[t * a.out_stride + rows[t].keep] = page;
+      a.refs[page] = 1;
+    }
+    if (t < a.out_rows) a.missing[t] = lacks[t] - (page >= 0) + beyond(a, rows[t]);
+    return;
+  }
   if (wants) atomicOr(&any, wants);
   __syncthreads();
   for (unsigned left = any; left; left &= left - 1) {  // in the order of the entries
