@@ -24,12 +24,16 @@
 // not depend on the way to the node, so nodes are worked on side by side, a
 // workgroup each, and only those that a walk can reach and that have a child
 // behind a refused one need the sum of a row.  k_sums follows the walk and sums
-// the weights at its end in shares, one for each of its waves; k_pick finds the
-// token in one of them.  Where one workgroup has a row's shares both are one
-// kernel.
+// the weights at its end in shares of 1024 entries; k_pick finds the token in one
+// of them, with one wave.  Short rows are one workgroup's, which does both.
 //
-// Bound: HBM for large batches (the rows at the walk's end), else the chain of
-// dependent loads (starts, tokens, points of rows, rows, sums).
+// Bound: HBM for large batches (64 rows of p and q of 128001 entries in fp32: 13 us
+// of k_sums, 5 TB/s, and 6 of k_pick on MI355X); else the chain of dependent loads
+// (starts, tokens, points of rows, rows, sums: 6 us for small rows); of a node with
+// several refused children the vector units of its one CU: 7 fp64 instructions an
+// entry, 5 us a refusal for 50001 entries and 10 for 128000, whatever their type.
+// (A refusal's sum in fp32 would be quicker, but its error would move every border
+// of the sample: one token in some thousand would be another.)
 #include "launch.h"
 
 namespace mx {
@@ -96,17 +100,42 @@ __device__ __forceinline__ void weigh(const Rows<T, DRAFT> &rows, const Taken &t
   } else {
     for (int j = 0; j < taken.count; ++j) {
       const int64_t at = taken.tokens[j] - ((int64_t)k * N - rows.off);
+      if ((uint64_t)at < N) {
 #pragma unroll
-      for (int i = 0; i < N; ++i) w[i] = at == i ? 0.0 : w[i];
+        for (int i = 0; i < N; ++i) w[i] = at == i ? 0.0 : w[i];
+      }
     }
   }
 }
 
-__device__ __forceinline__ double wave_sum_f64(double v) {
-#pragma unroll
-  for (int d = 32; d > 0; d /= 2) v += __shfl_xor(v, d);
+// Sums over the lanes of a wave go by row shifts and row broadcasts, which take a tenth of the time of exchanges by way
+// of LDS; every lane is active.
+template <int CTRL, int ROWS> __device__ __forceinline__ double shifted(double v) {
+  const uint64_t b = __builtin_bit_cast(uint64_t, v);
+  const unsigned lo = __builtin_amdgcn_update_dpp(0, (int)(unsigned)b, CTRL, ROWS, 0xF, false);
+  const unsigned hi = __builtin_amdgcn_update_dpp(0, (int)(unsigned)(b >> 32), CTRL, ROWS, 0xF, false);
+  return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+}
+
+// Of the lanes up to this one.
+__device__ __forceinline__ double wave_scan_f64(double v) {
+  v += shifted<0x111, 0xF>(v);  // by 1, 2, 4 and 8 within rows of 16
+  v += shifted<0x112, 0xF>(v);
+  v += shifted<0x114, 0xF>(v);
+  v += shifted<0x118, 0xF>(v);
+  v += shifted<0x142, 0xA>(v);  // the last of rows 0 and 2 to rows 1 and 3
+  v += shifted<0x143, 0xC>(v);  // the last of row 1 to rows 2 and 3
   return v;
 }
+
+__device__ __forceinline__ double lane_value(double v, int lane) {
+  const uint64_t b = __builtin_bit_cast(uint64_t, v);
+  const unsigned lo = __builtin_amdgcn_readlane((int)(unsigned)b, lane);
+  const unsigned hi = __builtin_amdgcn_readlane((int)(unsigned)(b >> 32), lane);
+  return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+}
+
+__device__ __forceinline__ double wave_sum_f64(double v) { return lane_value(wave_scan_f64(v), 63); }
 
 // The sum of v over the workgroup, in the order of its waves; waves[] has a place for each.
 template <int THREADS>
@@ -346,58 +375,48 @@ __global__ __launch_bounds__(BRANCH_THREADS) void k_branch(VerifyArgs a, Space s
 // ---- the walk, and the sums at its end ----
 
 constexpr int SUM_THREADS = 256, ONE_THREADS = 1024;  // of k_sums beside k_pick, and of the kernel that is both
+constexpr int SHARE = 1024;                           // entries of a share, a wave's unit, unless there are too many
+constexpr int MOST_SHARES = 4096;
 
-// What was taken from the weights at a sequence's end node, without its last refusal if `all` does not hold.
-// list[VERIFY_NODES] and count are in LDS.
-template <int THREADS, typename T, bool DRAFT, bool TREE>
+// A row's chunks in `shares` runs, of which a wave has `each`.
+struct Cut {
+  int shares, each;
+  __device__ __forceinline__ int at(int chunks, int s) const { return (int)((int64_t)chunks * s / shares); }
+};
+
+// What was taken from the weights at a sequence's end node; !all: without its last refusal.  A wave puts the tokens into
+// list[VERIFY_NODES] (LDS).
+template <bool DRAFT, bool TREE>
 __device__ __forceinline__ Taken taken_at(const VerifyArgs &a, const Space &space, int b, const Nodes &nodes,
-                                          const End &end, bool all, int *list, int *count) {
+                                          const End &end, bool all, int *list) {
   if (DRAFT) return Taken{all ? end.after : end.before, nullptr, 0};
-  if (threadIdx.x == 0) *count = 0;
-  __syncthreads();
-  if (end.after > 0.0) {
-    if (TREE) {
-      const int *gone = space.gone + (int64_t)b * a.max_q;
-      int last = 0;  // the last child that was asked
-      if (!all)
-        for (int i = end.node + 1; i < nodes.count; ++i) {
-          const int64_t x = a.tokens[nodes.first + i];
-          if (a.parents[nodes.first + i] == end.node && x >= 0 && x < a.vocab) last = i;
-        }
-      for (int i = end.node + 1 + threadIdx.x; i < nodes.count; i += THREADS) {
-        const int64_t x = a.tokens[nodes.first + i];
-        if (a.parents[nodes.first + i] == end.node && x >= 0 && x < a.vocab && i != last && gone[i])
-          list[atomicAdd(count, 1)] = (int)x;
-      }
-    } else if (all && threadIdx.x == 0) {
-      list[0] = (int)a.tokens[nodes.first + end.node + 1];
-      *count = 1;
+  Taken taken{0.0, list, 0};
+  if (!(end.after > 0.0)) return taken;
+  const int lane = threadIdx.x % 64;
+  if (!TREE) {
+    if (lane == 0 && all) list[0] = (int)a.tokens[nodes.first + end.node + 1];
+    taken.count = all;
+  } else {
+    const int *gone = space.gone + (int64_t)b * a.max_q;
+    for (int base = end.node + 1; base < nodes.count; base += 64) {
+      const int i = base + lane;
+      int64_t x = -1;
+      if (i < nodes.count && a.parents[nodes.first + i] == end.node) x = a.tokens[nodes.first + i];
+      const bool asked = x >= 0 && x < a.vocab;
+      const uint64_t mask = __builtin_amdgcn_ballot_w64(asked && gone[asked ? i : 0]);
+      if (mask >> lane & 1) list[taken.count + __builtin_popcountll(mask & (((uint64_t)1 << lane) - 1))] = (int)x;
+      taken.count += __builtin_popcountll(mask);
     }
+    taken.count -= !all;  // the last child's, which is always there
   }
-  __syncthreads();
-  return Taken{0.0, list, *count};
-}
-
-// Those of a list's tokens that lie in the chunks from .. to.
-template <int THREADS, typename T, bool DRAFT>
-__device__ __forceinline__ Taken near(const Rows<T, DRAFT> &rows, const Taken &taken, int from, int to, int *list,
-                                      int *count) {
-  if (DRAFT || taken.count == 0) return taken;
-  if (threadIdx.x == 0) *count = 0;
-  __syncthreads();
-  for (int j = threadIdx.x; j < taken.count; j += THREADS) {
-    const int k = (taken.tokens[j] + rows.off) / Rows<T, DRAFT>::N;
-    if (k >= from && k < to) list[atomicAdd(count, 1)] = taken.tokens[j];
-  }
-  __syncthreads();
-  return Taken{0.0, list, *count};
+  return taken;
 }
 
 // The walk of sequence b; `write`: this workgroup puts out what is known from it.
 template <int THREADS, typename T, bool DRAFT, bool TREE>
 __device__ __forceinline__ End walk(const VerifyArgs &a, const Space &space, int b, const Nodes &nodes, bool write,
                                     int *next) {
-  const int t = threadIdx.x;
+  const int t = threadIdx.x, wave = t / 64, lane = t % 64;
   int *path = a.path + (int64_t)b * a.max_q;
   int64_t *out = a.out + (int64_t)b * a.max_q;
   End end{0, 0, 0.0, 0.0};
@@ -416,31 +435,27 @@ __device__ __forceinline__ End walk(const VerifyArgs &a, const Space &space, int
     }
     if (nodes.count > 0) end.before = follow[end.node].before, end.after = follow[end.node].after;
   } else {
-    // the first node that is not kept, in each thread its own first
-    int stop = nodes.count;
-    bool there = false;  // its token is one of the vocabulary, and was refused
-    for (int i = 1 + t; i < nodes.count; i += THREADS) {
-      const int64_t x = a.tokens[nodes.first + i];
+    // the first node that is not kept, in each wave its own first; bit 0: its token was refused, and is not outside
+    // the vocabulary
+    int key = 2 * nodes.count;
+    for (int base = 1 + 64 * wave; base < nodes.count; base += THREADS) {
+      const int i = base + lane;
+      const int64_t x = i < nodes.count ? a.tokens[nodes.first + i] : -1;
       const bool in = x >= 0 && x < a.vocab;
-      bool keep = false;
+      bool keep = i >= nodes.count;
       if (in) {
         double p, q;
         point_of<T, DRAFT>(a, nodes.first + i - 1, x, p, q);
         keep = passes(a.uniforms[nodes.first + i], 1.0, q, p);
       }
-      if (!keep) {
-        stop = i;
-        there = in;
+      const uint64_t stop = __builtin_amdgcn_ballot_w64(!keep), there = __builtin_amdgcn_ballot_w64(in);
+      if (stop) {
+        const int l = __builtin_ctzll(stop);
+        key = 2 * (base + l) + (int)(there >> l & 1);
         break;
       }
     }
-    int key = 2 * stop + there;
-#pragma unroll
-    for (int d = 32; d > 0; d /= 2) {
-      const int other = __shfl_xor(key, d);
-      key = other < key ? other : key;
-    }
-    if (t % 64 == 0) next[t / 64] = key;
+    if (lane == 0) next[wave] = key;
     __syncthreads();
 #pragma unroll
     for (int w = 0; w < THREADS / 64; ++w) key = next[w] < key ? next[w] : key;
@@ -463,115 +478,88 @@ __device__ __forceinline__ End walk(const VerifyArgs &a, const Space &space, int
   return end;
 }
 
-// The first thread of the workgroup whose running sum, after `before`, is above target (a thread without weight is
-// not), the last one with weight if rounding leaves none, -1 without any; `before` becomes the sum before it.
-template <int THREADS>
-__device__ __forceinline__ int first_above(double v, double target, double &before, double *waves, int *found) {
-  const int t = threadIdx.x, lane = t % 64, wave = t / 64;
-  double sum = v;
-#pragma unroll
-  for (int d = 1; d < 64; d *= 2) {
-    const double o = __shfl_up(sum, d);
-    if (lane >= d) sum += o;
-  }
-  __syncthreads();
-  if (lane == 63) waves[wave] = sum;
-  if (t == 0) found[0] = THREADS, found[1] = -1;
-  __syncthreads();
-  double base = before;
-  for (int w = 0; w < wave; ++w) base += waves[w];
-  const double after = base + sum;
-  const uint64_t above = __builtin_amdgcn_ballot_w64(v > 0.0 && after > target);
-  const uint64_t any = __builtin_amdgcn_ballot_w64(v > 0.0);
-  if (lane == 0 && above) atomicMin(found, 64 * wave + __builtin_ctzll(above));
-  if (lane == 0 && any) atomicMax(found + 1, 64 * wave + 63 - __builtin_clzll(any));
-  __syncthreads();
-  const int who = found[0] < THREADS ? found[0] : found[1];
-  if (t == who) waves[THREADS / 64] = after - v;
-  __syncthreads();
-  if (who >= 0) before = waves[THREADS / 64];
-  return who;
+// The first lane whose running sum, after `before`, is above target (a lane without weight is not), the last one with
+// weight if rounding leaves none, -1 without any; `before` becomes the sum before it.
+__device__ __forceinline__ int first_above(double v, double target, double &before) {
+  const double after = before + wave_scan_f64(v);
+  const uint64_t any = __builtin_amdgcn_ballot_w64(v > 0.0), above = __builtin_amdgcn_ballot_w64(v > 0.0 && after > target);
+  if (!any) return -1;
+  const int lane = above ? __builtin_ctzll(above) : 63 - __builtin_clzll(any);
+  before = lane_value(after - v, lane);
+  return lane;
 }
 
-constexpr int MOST_SHARES = 4096;
-
-// A row's chunks in `shares` runs, one for a wave.
-struct Cut {
-  int shares;
-  __device__ __forceinline__ int at(int chunks, int s) const { return (int)((int64_t)chunks * s / shares); }
-};
-
-// The sampled token: the share that the goal lies in, then each thread's run of its chunks, then that run.  sums[] (LDS)
-// has the shares' sums.
-template <int THREADS, typename T, bool DRAFT, bool TREE>
+// The sampled token, by one wave: the share that the goal lies in, then each lane's run of its chunks, then that run.
+// sums[] (LDS) has the shares' sums.
+template <typename T, bool DRAFT, bool TREE>
 __device__ __forceinline__ void pick(const VerifyArgs &a, const Space &space, int b, const Nodes &nodes, const End &end,
-                                     Cut cut, double u, double *sums, double *waves, int *list, int *found) {
-  constexpr int N = Chunk<T>::N;
-  const int t = threadIdx.x;
+                                     Cut cut, double u, Taken taken, double *sums, int *list) {
+  constexpr int N = Chunk<T>::N, HELD = 4;  // chunks of a lane that are read together
+  const int lane = threadIdx.x % 64;
   const Rows<T, DRAFT> rows(a, nodes.first + end.node);
-  Taken taken = taken_at<THREADS, T, DRAFT, TREE>(a, space, b, nodes, end, true, list, found);
-  // a run of shares for each thread
-  const int some = (cut.shares + THREADS - 1) / THREADS, s0 = t * some;
+  const int some = (cut.shares + 63) / 64, s0 = lane * some;
   auto shares = [&]() {
     double v = 0.0;
     for (int s = s0; s < s0 + some && s < cut.shares; ++s) v += sums[s];
     return v;
   };
-  double mine = shares(), total = block_sum<THREADS>(mine, waves);
+  double mine = shares(), total = wave_sum_f64(mine);
   if (!(total > 0.0) && end.after > end.before) {  // the last refusal would leave nothing: it takes nothing
-    taken = taken_at<THREADS, T, DRAFT, TREE>(a, space, b, nodes, end, false, list, found);
-    for (int s = t / 64; s < cut.shares; s += THREADS / 64) {
-      const double v =
-          wave_sum_f64(add_weights(rows, taken, cut.at(rows.chunks, s), cut.at(rows.chunks, s + 1), 64, t % 64));
-      if (t % 64 == 0) sums[s] = v;
+    taken = taken_at<DRAFT, TREE>(a, space, b, nodes, end, false, list);
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "workgroup");
+    for (int s = 0; s < cut.shares; ++s) {
+      const double v = wave_sum_f64(add_weights(rows, taken, cut.at(rows.chunks, s), cut.at(rows.chunks, s + 1), 64, lane));
+      if (lane == 0) sums[s] = v;
     }
-    __syncthreads();
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "workgroup");
     mine = shares();
-    total = block_sum<THREADS>(mine, waves);
+    total = wave_sum_f64(mine);
   }
   int64_t *out = a.out + (int64_t)b * a.max_q + end.kept;
   if (!(total > 0.0)) {
-    if (t == 0) *out = -1;
+    if (lane == 0) *out = -1;
     return;
   }
   const double target = u * total;
-  double before = 0.0;
-  int share = 0;
-  {
-    const int who = first_above<THREADS>(mine, target, before, waves, found);
-    double sum = before;
-    for (int s = who * some; s < (who + 1) * some && s < cut.shares; ++s) {
-      if (!(sums[s] > 0.0)) continue;
-      share = s;
-      before = sum;
-      sum += sums[s];
-      if (sum > target) break;
-    }
+  double before = 0.0, sum;
+  int share = first_above(mine, target, before) * some;
+  sum = before;
+  for (int s = share, last = s + some < cut.shares ? s + some : cut.shares; s < last; ++s) {
+    if (!(sums[s] > 0.0)) continue;
+    share = s;
+    before = sum;
+    sum += sums[s];
+    if (sum > target) break;
   }
   const int k0 = cut.at(rows.chunks, share), k1 = cut.at(rows.chunks, share + 1);
-  const int run = (k1 - k0 + THREADS - 1) / THREADS;
-  const int f = (int64_t)k0 + (int64_t)t * run < k1 ? k0 + t * run : k1, l = k1 - f > run ? f + run : k1;
-  double w[N];
-  Chunk<T> p, q;
+  const int run = (k1 - k0 + 63) / 64;
+  const int f = (int64_t)k0 + (int64_t)lane * run < k1 ? k0 + lane * run : k1, l = k1 - f > run ? f + run : k1;
   mine = 0.0;
-  for (int k = f; k < l; ++k) {
-    p = rows.read(rows.p, k, true);
-    q = DRAFT ? rows.read(rows.q, k, rows.wide) : p;
-    weigh<T, DRAFT>(rows, taken, k, p, q, w);
+  for (int k = f; k < l; k += HELD) {
+    Chunk<T> p[HELD], q[HELD];
 #pragma unroll
-    for (int i = 0; i < N; ++i) mine += w[i];
-  }
-  const int who = first_above<THREADS>(mine, target, before, waves, found);
-  if (t != who) return;
-  double sum = before;
-  bool done = false;
-  int64_t chosen = -1;
-  for (int k = f; k < l && !done; ++k) {
-    if (run > 1) {  // (the one chunk is here already)
-      p = rows.read(rows.p, k, true);
-      q = DRAFT ? rows.read(rows.q, k, rows.wide) : p;
-      weigh<T, DRAFT>(rows, taken, k, p, q, w);
+    for (int h = 0; h < HELD; ++h) {
+      const int at = k + h < l ? k + h : l - 1;
+      p[h] = rows.read(rows.p, at, true);
+      if (DRAFT) q[h] = rows.read(rows.q, at, rows.wide);
     }
+#pragma unroll
+    for (int h = 0; h < HELD; ++h) {
+      if (k + h >= l) continue;
+      double w[N];
+      weigh<T, DRAFT>(rows, taken, k + h, p[h], q[h], w);
+#pragma unroll
+      for (int i = 0; i < N; ++i) mine += w[i];
+    }
+  }
+  if (lane != first_above(mine, target, before)) return;
+  sum = before;
+  int64_t chosen = -1;
+  bool done = false;
+  for (int k = f; k < l && !done; ++k) {
+    double w[N];
+    const Chunk<T> p = rows.read(rows.p, k, true);
+    weigh<T, DRAFT>(rows, taken, k, p, DRAFT ? rows.read(rows.q, k, rows.wide) : p, w);
 #pragma unroll
     for (int i = 0; i < N; ++i) {
       sum += w[i];
@@ -587,64 +575,73 @@ __device__ __forceinline__ void pick(const VerifyArgs &a, const Space &space, in
 template <int THREADS, typename T, bool DRAFT, bool TREE, bool ONE>
 __global__ __launch_bounds__(THREADS) void k_sums(VerifyArgs a, Space space, Cut cut) {
   constexpr int WAVES = THREADS / 64;
-  __shared__ double waves[WAVES + 1], sums[WAVES];
-  __shared__ int next[VERIFY_NODES], list[DRAFT ? 1 : VERIFY_NODES], few[DRAFT ? 1 : VERIFY_NODES], found[2];
-  const int groups = cut.shares / WAVES, b = blockIdx.x / groups, group = blockIdx.x - b * groups;
-  const int wave = threadIdx.x / 64;
+  __shared__ double sums[ONE ? 2 * WAVES : 1];
+  __shared__ int next[VERIFY_NODES], list[DRAFT ? 1 : VERIFY_NODES], held;
+  const int groups = cut.shares / (WAVES * cut.each), b = blockIdx.x / groups, group = blockIdx.x - b * groups;
+  const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x / 64), lane = threadIdx.x % 64;
   const Nodes nodes = nodes_of(a, b);
   const double u = ONE && nodes.count > 0 ? a.uniforms[nodes.first] : 0.0;
   const End end = walk<THREADS, T, DRAFT, TREE>(a, space, b, nodes, group == 0, next);
   if (!ONE && group == 0 && threadIdx.x == 0) space.ends[b] = end;
   if (nodes.count == 0) return;
   const Rows<T, DRAFT> rows(a, nodes.first + end.node);
-  const int s0 = group * WAVES, s = s0 + wave;
-  const Taken all = taken_at<THREADS, T, DRAFT, TREE>(a, space, b, nodes, end, true, list, found);
-  const Taken taken = near<THREADS>(rows, all, cut.at(rows.chunks, s0), cut.at(rows.chunks, s0 + WAVES), few, found + 1);
-  const double sum = wave_sum_f64(
-      add_weights(rows, taken, cut.at(rows.chunks, s), cut.at(rows.chunks, s + 1), 64, threadIdx.x % 64));
-  if (!ONE) {
-    if (threadIdx.x % 64 == 0) space.sums[(int64_t)b * cut.shares + s] = sum;
-    return;
+  Taken taken{end.after, list, 0};
+  if (!DRAFT) {
+    if (wave == 0) {
+      taken = taken_at<DRAFT, TREE>(a, space, b, nodes, end, true, list);
+      if (lane == 0) held = taken.count;
+    }
+    __syncthreads();
+    taken.count = held;
   }
-  if (threadIdx.x % 64 == 0) sums[wave] = sum;
+  for (int e = 0; e < cut.each; ++e) {
+    const int s = (group * WAVES + wave) * cut.each + e;
+    const double sum =
+        wave_sum_f64(add_weights(rows, taken, cut.at(rows.chunks, s), cut.at(rows.chunks, s + 1), 64, lane));
+    if (lane == 0) (ONE ? sums[ONE ? s : 0] : space.sums[(int64_t)b * cut.shares + s]) = sum;
+  }
+  if (!ONE) return;
   __syncthreads();
-  pick<THREADS, T, DRAFT, TREE>(a, space, b, nodes, end, cut, u, sums, waves, list, found);
+  if (wave == 0) pick<T, DRAFT, TREE>(a, space, b, nodes, end, cut, u, taken, sums, list);
 }
 
 template <typename T, bool DRAFT, bool TREE>
-__global__ __launch_bounds__(SUM_THREADS) void k_pick(VerifyArgs a, Space space, Cut cut) {
-  __shared__ double sums[MOST_SHARES], waves[SUM_THREADS / 64 + 1];
-  __shared__ int list[DRAFT ? 1 : VERIFY_NODES], found[2];
+__global__ __launch_bounds__(64) void k_pick(VerifyArgs a, Space space, Cut cut) {
+  __shared__ double sums[MOST_SHARES];
+  __shared__ int list[DRAFT ? 1 : VERIFY_NODES];
   const int b = blockIdx.x;
-  for (int s = threadIdx.x; s < cut.shares; s += SUM_THREADS) sums[s] = space.sums[(int64_t)b * cut.shares + s];
+  for (int s = threadIdx.x; s < cut.shares; s += 64) sums[s] = space.sums[(int64_t)b * cut.shares + s];
   const End end = space.ends[b];
   const Nodes nodes = nodes_of(a, b);
   if (nodes.count == 0) return;
   const double u = a.uniforms[nodes.first];
+  const Taken taken = taken_at<DRAFT, TREE>(a, space, b, nodes, end, true, list);
   __syncthreads();
-  pick<SUM_THREADS, T, DRAFT, TREE>(a, space, b, nodes, end, cut, u, sums, waves, list, found);
+  pick<T, DRAFT, TREE>(a, space, b, nodes, end, cut, u, taken, sums, list);
 }
 
-// Shares of a row: those of one workgroup where it is short, else of 2048 entries at most, and as many as it takes for
-// two workgroups on every CU while a workgroup has 1024 entries.
+// Short rows are the work of one workgroup: a launch less, of 2.5 us for the host.  (Chains over 32000 entries: kernels
+// 8.8 us against 7.6 of two for one sequence, 17 against 19 for 256.)  Longer ones have a share for each wave, or two
+// where that is four workgroups for every CU.
 constexpr int ONE_ENTRIES = 1 << 15;
 
-bool one_kernel(const VerifyArgs &a) {
-  return a.vocab <= ONE_ENTRIES;
-}
-
-int shares_of(int batch, int vocab) {
+Cut cut_of(int batch, int vocab) {
   constexpr int WAVES = SUM_THREADS / 64;
-  int64_t s = (vocab + 2048 * WAVES - 1) / (2048 * WAVES);  // workgroups
-  const int64_t fill = 2 * device_cu_count() / (batch > 0 ? batch : 1), most = vocab / 1024;
-  const int64_t more = fill < most ? fill : most;
-  s = s > more ? s : more;
-  if (batch > 0 && s > MAX_GROUPS_256 / batch) s = MAX_GROUPS_256 / batch;
-  return WAVES * (int)(s > MOST_SHARES / WAVES ? MOST_SHARES / WAVES : s < 1 ? 1 : s);
+  if (vocab <= ONE_ENTRIES) {
+    constexpr int waves = ONE_THREADS / 64;
+    static_assert(ONE_ENTRIES <= 2 * waves * SHARE, "sums of k_sums");
+    return vocab <= waves * SHARE ? Cut{waves, 1} : Cut{2 * waves, 2};
+  }
+  int64_t groups = ((int64_t)vocab + SHARE * WAVES - 1) / (SHARE * WAVES);
+  const int each = batch * groups >= 4 * device_cu_count() ? 2 : 1;
+  groups = (groups + each - 1) / each;
+  if (groups > MOST_SHARES / (WAVES * each)) groups = MOST_SHARES / (WAVES * each);
+  if (batch > 0 && groups > MAX_GROUPS_256 / batch) groups = MAX_GROUPS_256 / batch;
+  return Cut{WAVES * each * (int)(groups < 1 ? 1 : groups), each};
 }
 
 template <typename T, bool DRAFT, bool TREE>
-hipError_t verify(const VerifyArgs &a, const Space &space, bool one, hipStream_t stream) {
+hipError_t verify(const VerifyArgs &a, const Space &space, hipStream_t stream) {
   if (TREE && a.max_q > 0 && a.total_q > 0) {
     // a workgroup for each node of a sequence, fewer of many sequences
     int64_t per = 2 * device_cu_count() / a.batch;
@@ -655,32 +652,31 @@ hipError_t verify(const VerifyArgs &a, const Space &space, bool one, hipStream_t
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
-  if (one) {
-    k_sums<ONE_THREADS, T, DRAFT, TREE, true><<<(unsigned)a.batch, ONE_THREADS, 0, stream>>>(a, space,
-                                                                                            Cut{ONE_THREADS / 64});
+  const Cut cut = cut_of(a.batch, a.vocab);
+  if (a.vocab <= ONE_ENTRIES) {
+    k_sums<ONE_THREADS, T, DRAFT, TREE, true><<<(unsigned)a.batch, ONE_THREADS, 0, stream>>>(a, space, cut);
     return hipGetLastError();
   }
-  const Cut cut{shares_of(a.batch, a.vocab)};
-  const unsigned grid = (unsigned)(cut.shares / (SUM_THREADS / 64) * (int64_t)a.batch);
+  const unsigned grid = (unsigned)(cut.shares / (SUM_THREADS / 64 * cut.each) * (int64_t)a.batch);
   k_sums<SUM_THREADS, T, DRAFT, TREE, false><<<grid, SUM_THREADS, 0, stream>>>(a, space, cut);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  k_pick<T, DRAFT, TREE><<<(unsigned)a.batch, SUM_THREADS, 0, stream>>>(a, space, cut);
+  k_pick<T, DRAFT, TREE><<<(unsigned)a.batch, 64, 0, stream>>>(a, space, cut);
   return hipGetLastError();
 }
 
 template <typename T>
-hipError_t verify(const VerifyArgs &a, const Space &space, bool one, hipStream_t stream) {
+hipError_t verify(const VerifyArgs &a, const Space &space, hipStream_t stream) {
   if (a.draft)
-    return a.parents ? verify<T, true, true>(a, space, one, stream) : verify<T, true, false>(a, space, one, stream);
-  return a.parents ? verify<T, false, true>(a, space, one, stream) : verify<T, false, false>(a, space, one, stream);
+    return a.parents ? verify<T, true, true>(a, space, stream) : verify<T, true, false>(a, space, stream);
+  return a.parents ? verify<T, false, true>(a, space, stream) : verify<T, false, false>(a, space, stream);
 }
 
 }  // namespace
 
 int64_t verify_workspace(int batch, int max_q, int vocab) {
   return ends_bytes(batch) + follow_bytes(batch, max_q) + gone_bytes(batch, max_q) +
-         (int64_t)batch * shares_of(batch, vocab) * 8;
+         (int64_t)batch * cut_of(batch, vocab).shares * 8;
 }
 
 hipError_t launch_verify(int dtype, const VerifyArgs &a, hipStream_t stream) {
@@ -690,8 +686,7 @@ hipError_t launch_verify(int dtype, const VerifyArgs &a, hipStream_t stream) {
   space.follow = (Follow *)(at += ends_bytes(a.batch));
   space.gone = (int *)(at += follow_bytes(a.batch, a.max_q));
   space.sums = (double *)(at += gone_bytes(a.batch, a.max_q));
-  const bool one = one_kernel(a);
-  return dtype == 1 ? verify<float>(a, space, one, stream) : verify<unsigned short>(a, space, one, stream);
+  return dtype == 1 ? verify<float>(a, space, stream) : verify<unsigned short>(a, space, stream);
 }
 
 }  // namespace mx
