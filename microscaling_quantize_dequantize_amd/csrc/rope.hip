@@ -116,11 +116,21 @@ __global__ __launch_bounds__(ROPE_THREADS) void k_rope(const T *src, T *dst, Rop
     }
   };
 
-  if (active) load(item0, first);
-  for (int i = threadIdx.x; i < nt * a.half; i += ROPE_THREADS) {
+  // what the first angle takes is asked for before the rows: loads come back in their order, and the angle is formed
+  // while the rows are on their way
+  double at = 0.0, per = 0.0;
+  auto ask = [&](int i) {
     const int t = i / a.half, p = i - t * a.half;
+    at = position_of(a.positions, t0 + t, p);
+    per = a.inv_freq[p];
+  };
+  const int angles = nt * a.half;
+  if ((int)threadIdx.x < angles) ask(threadIdx.x);
+  if (active) load(item0, first);
+  for (int i = threadIdx.x; i < angles; i += ROPE_THREADS) {
+    if (i != (int)threadIdx.x) ask(i);
     double s, c;
-    sine_cosine(position_of(a.positions, t0 + t, p) * a.inv_freq[p], s, c);
+    sine_cosine(at * per, s, c);
     tc[i] = (float)(c * a.scale);
     ts[i] = (float)(a.inverse ? -s * a.scale : s * a.scale);
   }
