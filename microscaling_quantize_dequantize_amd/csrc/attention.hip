@@ -9,7 +9,7 @@ namespace mx {
 // A lane has four dimensions of a row, so that its pieces come in loads of 16 bytes, and a wave several rows side by side;
 // a workgroup of four waves has join_rows() rows of an item, all of whose first loads are under way together.  (A wave
 // with one row at a time, its lanes two dimensions apart: 29 us against 14 for 248 items of 256 rows, heads of 128, in two or three pieces.)
-constexpr int JOIN_PASSES = 4;
+constexpr int JOIN_PASSES = 2;  // four: 29.6 us against 28.4 for 16 small trees, whose rows are few
 constexpr int join_side(int dim) { return 64 / (dim / 4); }  // rows of a wave's pass
 constexpr int join_rows(int dim) { return 4 * JOIN_PASSES * join_side(dim); }
 
