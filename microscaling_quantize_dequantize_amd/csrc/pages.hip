@@ -343,7 +343,10 @@ struct CompactArgs {
   int max_keep, cols, code_parts, scale_parts;  // parts: workgroups that share a head's tokens
 };
 
-constexpr int COMPACT_THREADS = 1024, COMPACT_UNROLL = 4;
+// Threads of a workgroup and tokens that each has under way.  Long lists have the large workgroups, whose groups are
+// fewer, and two of them on a CU; short ones, of whole batches, the small ones: 64 sequences of up to 60 new tokens, 8
+// heads of 128, 7.7 us against 15 with large ones, one of 8000 tokens 30 against 18.
+constexpr int LARGE_THREADS = 1024, LARGE_UNROLL = 2, SMALL_THREADS = 256, SMALL_UNROLL = 4;
 constexpr int COMPACT_TABLE = 4096;  // entries of the table in LDS
 
 // A workgroup has some of the pieces of one head's tokens of one sequence, its keys' or values' codes or scales, and
@@ -351,7 +354,7 @@ constexpr int COMPACT_TABLE = 4096;  // entries of the table in LDS
 // what a later one reads.  So the tokens may be moved within their own pages, and every place has what place keep[i] held
 // at the beginning.
 // T: what a thread moves of a token, of which there are `per` pieces; this workgroup has those from piece0 to piece1.
-template <typename T>
+template <int COMPACT_THREADS, int COMPACT_UNROLL, typename T>
 __device__ __forceinline__ void compact(const CompactArgs &a, T *data, int per, int piece0, int piece1, bool planes,
                                         int b, int head) {
   __shared__ int near[COMPACT_TABLE];
@@ -407,15 +410,16 @@ __device__ __forceinline__ void compact(const CompactArgs &a, T *data, int per, 
   }
 }
 
-__global__ __launch_bounds__(COMPACT_THREADS) void k_compact(CompactArgs a) {
+template <int THREADS, int UNROLL>
+__global__ __launch_bounds__(THREADS) void k_compact(CompactArgs a) {
   const CacheView &cv = a.cache;
   const int b = blockIdx.x / cv.heads, head = blockIdx.x - b * cv.heads, v = blockIdx.y % 2, part = blockIdx.y / 2;
   if (part >= a.code_parts) {
     const int per = cv.dim / 32, p = part - a.code_parts;
-    compact<uint8_t>(a, cv.scales[v], per, per * p / a.scale_parts, per * (p + 1) / a.scale_parts, true, b, head);
+    compact<THREADS, UNROLL, uint8_t>(a, cv.scales[v], per, per * p / a.scale_parts, per * (p + 1) / a.scale_parts, true, b, head);
   } else {
     const int per = (cv.fmt == 0 ? cv.dim / 2 : cv.dim) / 16;
-    compact<u32x4>(a, (u32x4 *)cv.codes[v], per, per * part / a.code_parts, per * (part + 1) / a.code_parts, false, b,
+    compact<THREADS, UNROLL, u32x4>(a, (u32x4 *)cv.codes[v], per, per * part / a.code_parts, per * (part + 1) / a.code_parts, false, b,
                    head);
     if (blockIdx.y == 0 && head == 0 && threadIdx.x == 0) {
       const int count = a.counts[b] < a.max_keep ? a.counts[b] : a.max_keep;
@@ -483,18 +487,24 @@ hipError_t launch_cache_copy(const CacheView &cache, const int *src, const int *
 hipError_t launch_cache_compact(const CacheView &cache, const int *kv_starts, const int *keep, int64_t keep_stride,
                                 int max_keep, const int *counts, const int *table, int64_t stride, int pages, int batch,
                                 int *kv_lens, hipStream_t stream) {
-  // long lists of few heads are shared by the pieces of a token, down to one each, until every CU has a workgroup
   const int codes = (cache.fmt == 0 ? cache.dim / 2 : cache.dim) / 16, scales = cache.dim / 32;
   CompactArgs a{cache, kv_starts, keep, counts, table, keep_stride, stride, kv_lens, max_keep, pages, 1, 1};
   const int64_t heads = (int64_t)batch * cache.heads;
-  const auto groups = [](int parts) { return COMPACT_THREADS * COMPACT_UNROLL * parts; };
-  while (a.code_parts < codes && 2 * heads * a.code_parts < device_cu_count() &&
-         (int64_t)max_keep * codes > groups(a.code_parts))
-    a.code_parts = 2 * a.code_parts < codes ? 2 * a.code_parts : codes;
-  while (a.scale_parts < scales && 2 * heads * a.scale_parts < device_cu_count() &&
-         (int64_t)max_keep * scales > groups(a.scale_parts))
-    a.scale_parts = 2 * a.scale_parts < scales ? 2 * a.scale_parts : scales;
-  k_compact<<<dim3((unsigned)heads, (unsigned)(2 * (a.code_parts + a.scale_parts))), COMPACT_THREADS, 0, stream>>>(a);
+  if ((int64_t)max_keep * codes <= 4 * SMALL_THREADS * SMALL_UNROLL) {
+    k_compact<SMALL_THREADS, SMALL_UNROLL><<<dim3((unsigned)heads, 4), SMALL_THREADS, 0, stream>>>(a);
+    return hipGetLastError();
+  }
+  // long lists of few heads are shared by the pieces of a token, down to one each, until every CU has a workgroup
+  const auto parts = [&](int pieces) {
+    int n = 1;
+    while (n < pieces && 2 * heads * n < device_cu_count() && (int64_t)max_keep * pieces > LARGE_THREADS * LARGE_UNROLL * n)
+      n = 2 * n < pieces ? 2 * n : pieces;
+    return n;
+  };
+  a.code_parts = parts(codes);
+  a.scale_parts = parts(scales);
+  k_compact<LARGE_THREADS, LARGE_UNROLL>
+      <<<dim3((unsigned)heads, (unsigned)(2 * (a.code_parts + a.scale_parts))), LARGE_THREADS, 0, stream>>>(a);
   return hipGetLastError();
 }
 
