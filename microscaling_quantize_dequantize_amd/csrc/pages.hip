@@ -88,7 +88,7 @@ __global__ __launch_bounds__(256) void k_page_rows(BookArgs a) {
 }
 
 constexpr int TAKE_THREADS = 1024, TAKE_ITEMS = 4;  // entries of a table that a step of the workgroup looks at: 4096
-constexpr int SCAN_ITEMS = 8;                       // counts of holders: 8192
+constexpr int SCAN_ITEMS = 8, SKIP_ITEMS = 32;      // counts of holders: 8192, and 32768 where none is free
 constexpr int queue_of(int items) { return TAKE_THREADS * (items + SCAN_ITEMS); }  // pages, for steps of so many items a thread
 
 // The sum of v over the threads before this one, and over all of them (total).
@@ -120,8 +120,21 @@ struct FreePages {
   int *queue;                          // in LDS
   int head = 0, size = 0, cursor = 0;  // of the queue; the first page that was not looked at
 
+  // How many holders a page has: atomic, as the changes of this kernel are, which a barrier has put before it.
+  static __device__ __forceinline__ int holders(const BookArgs &a, unsigned page) {
+    return __hip_atomic_load(a.refs + page, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  }
+
   // At least `wanted`, if there are so many.
   __device__ __forceinline__ void find(const BookArgs &a, int wanted, int *waves) {
+    // the pool's low pages are taken as a rule: runs of them are passed over in large steps
+    while (size == 0 && wanted > 0 && a.pages - cursor >= TAKE_THREADS * SKIP_ITEMS) {
+      bool any = false;
+#pragma unroll
+      for (int k = 0; k < SKIP_ITEMS; ++k) any |= holders(a, (unsigned)cursor + k * TAKE_THREADS + threadIdx.x) == 0;
+      if (__syncthreads_or(any)) break;
+      cursor += TAKE_THREADS * SKIP_ITEMS;
+    }
     while (size < wanted && cursor < a.pages) {
       int found = 0;
       unsigned free = 0;
@@ -129,9 +142,7 @@ struct FreePages {
 #pragma unroll
       for (int k = 0; k < SCAN_ITEMS; ++k) {
         const unsigned p = p0 + k;
-        // atomic, as the changes of this kernel are, which a barrier has put before it
-        const bool is = p < (unsigned)a.pages &&
-                        __hip_atomic_load(a.refs + p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == 0;
+        const bool is = p < (unsigned)a.pages && holders(a, p) == 0;
         free |= (unsigned)is << k;
         found += is;
       }
@@ -153,8 +164,9 @@ struct FreePages {
   }
 };
 
-// Small tables: one workgroup sees to the rows and hands out pages.
-constexpr int SMALL_ROWS = 1024, SMALL_ITEMS = 16;  // rows; entries of a thread
+// Small tables: one workgroup sees to the rows and hands out pages.  (64 rows of 256 entries take it 10 us where nothing
+// is to be done, and two kernels 5; 64 rows of 63 entries 6 us.)
+constexpr int SMALL_ROWS = 1024, SMALL_ITEMS = 4;  // rows; entries of a thread
 
 template <bool FORK>
 __global__ __launch_bounds__(TAKE_THREADS) void k_pages_small(BookArgs a) {
@@ -169,22 +181,18 @@ __global__ __launch_bounds__(TAKE_THREADS) void k_pages_small(BookArgs a) {
   if (t == 0) any = 0u;
   __syncthreads();
   unsigned wants = 0;  // bit k: this thread's entry k lacks a page
+  int was[SMALL_ITEMS];
 #pragma unroll
-  for (int k0 = 0; k0 < SMALL_ITEMS; k0 += 4) {
-    if (k0 * TAKE_THREADS >= entries) break;
-    int was[4];
+  for (int k = 0; k < SMALL_ITEMS; ++k) {
+    const int e = k * TAKE_THREADS + t, r = e < entries ? e / a.cols : 0;
+    was[k] = e < entries ? entry_of<FORK>(a, rows[r], e - r * a.cols) : -1;
+  }
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const int e = (k0 + k) * TAKE_THREADS + t, r = e / a.cols;
-      was[k] = e < entries ? entry_of<FORK>(a, rows[r], e - r * a.cols) : -1;
-    }
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const int e = (k0 + k) * TAKE_THREADS + t, r = e / a.cols, j = e - r * a.cols;
-      if (e >= entries || !settle<FORK>(a, rows[r], r, j, was[k])) continue;
-      atomicAdd(lacks + r, 1);
-      wants |= 1u << (k0 + k);
-    }
+  for (int k = 0; k < SMALL_ITEMS; ++k) {
+    const int e = k * TAKE_THREADS + t, r = e < entries ? e / a.cols : 0;
+    if (e >= entries || !settle<FORK>(a, rows[r], r, e - r * a.cols, was[k])) continue;
+    atomicAdd(lacks + r, 1);
+    wants |= 1u << k;
   }
   FreePages<1> free{queue};
   if (FORK) {  // a page each for the rows whose last one is not full
@@ -221,33 +229,95 @@ __global__ __launch_bounds__(TAKE_THREADS) void k_pages_small(BookArgs a) {
   if (t < a.out_rows) a.missing[t] = lacks[t] + beyond(a, rows[t]);
 }
 
-// One workgroup hands out pages: it goes over the entries that lack one in their order, and over refs for free ones.
+// One workgroup hands out pages, to the entries that lack one in the order of rows and columns.  Of rows of a fork that is
+// the one behind the full pages; of others as a rule the last ones that the row needs, which is looked at first.
 template <bool FORK>
 __global__ __launch_bounds__(TAKE_THREADS) void k_page_take(BookArgs a) {
   __shared__ int waves[TAKE_THREADS / 64], queue[queue_of(TAKE_ITEMS)];
-  int lack = 0, total;
-  for (int r = threadIdx.x; r < a.out_rows; r += TAKE_THREADS) lack |= a.missing[r];
-  block_prefix(lack != 0, waves, total);
-  if (total == 0) return;
-
+  __shared__ int before[TAKE_THREADS + 1], end[TAKE_THREADS];  // of a step's rows: entries that lack a page, in sum; ends
+  const int t = threadIdx.x;
   FreePages<TAKE_ITEMS> free{queue};
-  const int64_t cols = FORK ? 1 : a.cols, entries = a.out_rows * cols;
+
+  // rows row0 .. row0 + TAKE_THREADS: what they lack within their columns; the sum
+  auto look = [&](int row0) {
+    const int r = row0 + t;
+    int lack = 0;
+    if (r < a.out_rows && (lack = a.missing[r]) != 0) {
+      const Row row = row_of<FORK>(a, r);
+      const int need = row.need < a.cols ? row.need : a.cols;
+      end[t] = need;
+      if (FORK) lack = row.keep < need;  // (its parent's holes are not filled)
+      else lack -= beyond(a, row);
+    }
+    int total;
+    const int rank = block_prefix(lack, waves, total);
+    before[t] = rank;
+    if (t == 0) before[TAKE_THREADS] = total;
+    __syncthreads();
+    return total;
+  };
+  // the entry of this rank, of rows that lack their last ones
+  auto entry = [&](int row0, int rank, int &r) {
+    int lo = 0, hi = TAKE_THREADS;  // before[lo] <= rank < before[hi]
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) / 2;
+      if (before[mid] <= rank) lo = mid;
+      else hi = mid;
+    }
+    r = row0 + lo;
+    return a.out + (int64_t)r * a.out_stride + (end[lo] - (before[lo + 1] - rank));
+  };
+  bool tails = true, none = true;
+  for (int row0 = 0; row0 < a.out_rows && tails; row0 += TAKE_THREADS) {
+    const int total = look(row0);
+    none = none && total == 0;
+    bool other = false;
+    if (!FORK)
+      for (int rank = t; rank < total; rank += TAKE_THREADS) {
+        int r;
+        other |= *entry(row0, rank, r) != -1;
+      }
+    tails = !__syncthreads_or(other);
+  }
+  if (tails) {
+    if (none) return;
+    for (int row0 = 0; row0 < a.out_rows; row0 += TAKE_THREADS) {
+      const int total = look(row0);
+      for (int base = 0; base < total; base += TAKE_THREADS * TAKE_ITEMS) {
+        const int some = total - base < TAKE_THREADS * TAKE_ITEMS ? total - base : TAKE_THREADS * TAKE_ITEMS;
+        free.find(a, some, waves);
+        for (int rank = t; rank < some; rank += TAKE_THREADS) {
+          const int page = free[rank];
+          if (page < 0) continue;
+          int r;
+          *entry(row0, base + rank, r) = page;
+          a.refs[page] = 1;
+          atomicSub(a.missing + r, 1);
+        }
+        free.drop(some);
+      }
+      __syncthreads();  // before[] and end[] have been read
+    }
+    return;
+  }
+
+  // some row has a page behind one that it lacks: all entries are gone over
+  const int64_t entries = (int64_t)a.out_rows * a.cols;
   for (int64_t base = 0; base < entries; base += TAKE_THREADS * TAKE_ITEMS) {
     int *place[TAKE_ITEMS], *miss[TAKE_ITEMS];
-    int wants = 0;
+    int wants = 0, total;
 #pragma unroll
     for (int k = 0; k < TAKE_ITEMS; ++k) {
-      const int64_t e = base + threadIdx.x * TAKE_ITEMS + k;
+      const int64_t e = base + t * TAKE_ITEMS + k;
       place[k] = nullptr;
       if (e >= entries) continue;
-      const int r = FORK ? (int)e : entries >> 32 ? (int)(e / cols) : (int)((unsigned)e / (unsigned)cols);
+      const int r = entries >> 32 ? (int)(e / a.cols) : (int)((unsigned)e / (unsigned)a.cols);
       miss[k] = a.missing + r;
       if (a.missing[r] == 0) continue;
       const Row row = row_of<FORK>(a, r);
-      const int j = FORK ? row.keep : (int)(e - r * cols);
-      if (j >= row.need || j >= a.cols) continue;
+      const int64_t j = e - (int64_t)r * a.cols;
       int *at = a.out + (int64_t)r * a.out_stride + j;
-      if (*at != -1) continue;
+      if (j >= row.need || *at != -1) continue;
       place[k] = at;
       ++wants;
     }

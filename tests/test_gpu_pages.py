@@ -222,6 +222,26 @@ def test_resize_of_odd_tables(mx):
     assert refs[:2] == [-1, -1] and refs[12] == 0
 
 
+@pytest.mark.parametrize("rows,cols", [(60, 100), (1030, 7), (3, 5000)])
+def test_resize_of_large_odd_tables(mx, rows, cols):
+    """More entries than one workgroup sees to, with holes before held pages, and a pool whose low pages are taken."""
+    pages, low = 90000, 70001
+    cache = mx.MXCache.allocate(0, pages, 1, 16, 32)
+    rng = random.Random(cols)
+    refs = [1] * low + [0] * (pages - low)
+    refs[40000] = refs[33] = 0
+    table = [[-1] * cols for _ in range(rows)]
+    check_resize(mx, cache, refs, table, [rng.randint(0, 16 * cols) for _ in range(rows)])
+    for _ in range(3):  # holes; what is taken out is given back by hand
+        for row in rng.sample(table, rows // 3 + 1):
+            for j in rng.sample(range(cols), min(cols, 40)):
+                if row[j] >= 0:
+                    refs[row[j]] -= 1
+                    row[j] = rng.choice([-1, -7, pages, 1 << 30])
+        check_resize(mx, cache, refs, table, [rng.randint(0, 16 * cols) for _ in range(rows)])
+    check_resize(mx, cache, refs, table, [16 * cols + 40] * rows)
+
+
 # ---- forks ------------------------------------------------------------------------------
 
 
