@@ -4,14 +4,17 @@
 //   pair p of rot/2:  a' = a c - b s,  b' = b c + a s,
 //   c, s = scale cos, scale sin of position * inv_freq[p];  the inverse takes
 //   -s, which is the transposed rotation, so it gives the gradient of x from
-//   that of y.
+//   that of y.  With axes the position is that of the pair's axis.
 //
 // Bound: HBM, one read and one write of x (3 flops a rotated element).  The
 // angles are formed once for each (token, pair) in fp64, rounded once to fp32
 // and kept in LDS for all heads of the token, whose pairs are rotated in fp32
 // whatever the type of x.  Measured on MI355X: 8192 x 64 heads of 128 in bf16
-// 43 us, 6.3 TB/s; in fp32 104 us, 5.2 TB/s; 4111 x 16 heads of 96 in fp32 9.4 us,
-// 5.4 TB/s; 8 tokens 3.4 us.
+// 43-45 us, 6.1 TB/s; in fp32 104 us, 5.2 TB/s; 8192 x 28 heads of 128 with three
+// axes in bf16 21.5 us, 5.5 TB/s; 4111 x 16 heads of 96 in fp32 10.3 us, 4.9 TB/s; 8
+// tokens 3.5 us.  Asking for positions and frequencies before the rows took 6% off
+// (48.4 to 45.4 and 23.3 to 22.0 us a call): loads come back in order, so an angle
+// behind the rows waited for them.
 //
 // Split: a workgroup owns whole tokens (one, or several while their heads are
 // few), a thread VEC neighbouring pairs of one head, so that both elements of
