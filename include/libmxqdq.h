@@ -427,8 +427,8 @@ MX_API int mx_cache_cross_attention(const mx_cache *cache, const void *q,
  * The cache's pages.  block_table is [rows x table_stride] int32, of which the
  * first table_pages of a row are used; an entry outside 0 .. pages - 1 is no
  * page.  refs [cache->pages] int32 counts the rows that hold each page; a page
- * is free where it is zero (one that is never to be handed out has another
- * value there).  Free pages are handed out lowest first, in the order of rows
+ * is free where it is zero (one that is kept from being handed out starts with a
+ * count of its own).  Free pages are handed out lowest first, in the order of rows
  * and columns, so that the same tables give the same pages.  The calls change
  * refs without a lock: those that share it follow one another on a stream.
  */
@@ -459,9 +459,10 @@ MX_API int mx_cache_resize(const mx_cache *cache, int32_t *refs,
  * meaning as block_table, no overlap with it) gets the full pages of row
  * parents[c], which both hold from then on, and, where the last page is not
  * full, a free page into which that page's tokens are copied (rows behind them
- * keep what they held).  The rest of the row is -1; so is all of it for a parent
- * outside 0 .. rows - 1.  missing [children] int32: the pages that a child needs
- * and does not hold.  children * cache->heads is below 2^23 (MX_ESHAPE).
+ * keep what they held, and so do all where the parent has no page there).  The
+ * rest of the row is -1; so is all of it for a parent outside 0 .. rows - 1.
+ * missing [children] int32: the pages that a child needs and does not hold.
+ * children * cache->heads is below 2^23 (MX_ESHAPE).
  */
 MX_API int mx_cache_fork(const mx_cache *cache, int32_t *refs,
                          const int32_t *block_table, int64_t table_stride,

@@ -372,6 +372,70 @@ def test_compact_nothing(mx):
     assert none.tolist() == [9]
 
 
+# ---- far pages and two calls at once -----------------------------------------------------------
+
+
+def test_pages_behind_4_gib(mx):
+    """Every call on pages whose bytes lie beyond 2^32 of each tensor."""
+    page, heads, dim, pages = 64, 8, 128, 70000  # 64 KiB a page
+    cache = mx.MXCache.allocate(1, pages, heads, page, dim)
+    refs = torch.ones(pages, dtype=I32, device="cuda")
+    refs[66000:66003] = 0
+    refs[69990:69994] = 0
+    table = torch.full((2, 4), -1, dtype=I32, device="cuda")
+    missing = mx.mx_cache_resize(cache, refs, table, i32([200, 0]))
+    assert table.tolist() == [[66000, 66001, 66002, 69990], [-1] * 4] and not bool(missing.any())
+    g = torch.Generator(device="cuda").manual_seed(1)
+    rows = [66000, 66001, 66002, 69990]
+    for n in NAMES:
+        t = getattr(cache, n)
+        for p in rows:
+            t[p] = torch.randint(0, 256, t[p].shape, generator=g, device="cuda", dtype=torch.uint8)
+    old = {n: getattr(cache, n)[rows].clone() for n in NAMES}
+    child, missing = mx.mx_cache_fork(cache, refs, table, i32([200, 0]), i32([0]))
+    assert child.tolist() == [[66000, 66001, 66002, 69991]] and missing.tolist() == [0]
+    mx.mx_cache_copy(cache, i32([66001, 69990]), i32([69992, 69993]))
+    keep = i32([[0, 70, 191, 199]])
+    assert mx.mx_cache_compact(cache, i32([0]), keep, i32([4]), table[:1]).tolist() == [4]
+    for n in NAMES:
+        t = getattr(cache, n)
+        assert torch.equal(t[[69992, 69993]], old[n][[1, 3]])
+        for r in range(64):
+            last = token(t, n, 69991, r)
+            assert torch.equal(last, token(old[n], n, 3, r)) if r < 8 else not bool(last.any())
+        for i, k in enumerate([0, 70, 191, 199]):
+            assert torch.equal(token(t, n, 66000, i), token(old[n], n, k // 64, k % 64))
+        assert torch.equal(token(t, n, 66000, 4), token(old[n], n, 0, 4)) and torch.equal(t[69990], old[n][3])
+
+
+def test_two_caches_on_two_streams(mx):
+    """Calls on caches and counts of their own may be under way together."""
+    both = []
+    for k in range(2):
+        cache = cache_of(mx, k, 300, 2, 16, 64, seed=k)
+        refs, table, lens = [0] * 300, [[-1] * 9 for _ in range(5)], [100, 33, 64, 7, 144]
+        resize(refs, table, lens, 16)
+        both.append((cache, refs, table, lens, snapshot(cache), torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    got = []
+    for turn in range(4):
+        for cache, refs, table, lens, data, s in both:
+            with torch.cuda.stream(s):
+                if turn == 0:
+                    got.append((i32(refs), grid(table), i32(lens), i32([4, 4, 0, 1, 2, 2]), i32([0] * 6)))
+                r, t, n, p, none = got[0 if cache is both[0][0] else 1]
+                child, _ = mx.mx_cache_fork(cache, r, t, n, p)
+                if turn < 3:
+                    mx.mx_cache_resize(cache, r, child, none)
+                else:
+                    got.append(child)
+    torch.cuda.synchronize()
+    for k, (cache, refs, table, lens, data, s) in enumerate(both):
+        want, _ = fork(refs, table, lens, [4, 4, 0, 1, 2, 2], 16, data)
+        assert got[2 + k].tolist() == want and got[k][0].tolist() == refs
+        same(cache, data)
+
+
 # ---- graphs ---------------------------------------------------------------------------------
 
 

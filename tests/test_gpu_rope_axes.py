@@ -92,6 +92,19 @@ def test_gradient_against_differences(mx):
     assert abs(float(diff - want)) <= 1920 * 8 * 2.0 ** -24 * 20
 
 
+def test_gradient_of_a_shared_head(mx):
+    """A head that several read, by a stride of zero: its gradient is the sum of theirs.  Four terms are added in fp32."""
+    x, pos, axes, f = inputs(13, 1, 64, (16, 16), torch.float32, 4)
+    leaf = x.requires_grad_()
+    w = torch.randn((13, 4, 64), device="cuda")
+    y = mx.mx_rope(leaf.expand(13, 4, 64), pos, f, axes=axes)
+    y.backward(w)
+    want, mag = rotate(w, pos, axes, f, 1.0, 0, True)
+    want, mag = want.sum(1, keepdim=True), mag.sum(1, keepdim=True)
+    # each term as above, and three additions of at most the sum of magnitudes
+    assert bool(((leaf.grad.double().cpu() - want).abs() <= (5 + 3) * 2.0 ** -24 * mag * (1 + 2.0 ** -20)).all())
+
+
 def test_second_gradient_and_sums(mx):
     """The gradient of the gradient is the rotation again; the gradient of a sum has no strides."""
     x, pos, axes, f = inputs(5, 2, 64, (16, 16), torch.float32, 3)

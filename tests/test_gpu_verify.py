@@ -282,6 +282,37 @@ def test_streams_and_replays(mx):
         c.check(held)
 
 
+def test_rows_behind_4_gib(mx):
+    """Rows 2^31 elements apart: strides and offsets are of 64 bits."""
+    c = Case([3], 500, torch.bfloat16, seed=2)
+    far = 1 << 31
+    for name in ("target", "draft"):
+        big = torch.empty(2 * far + 1000, dtype=torch.bfloat16, device="cuda")
+        rows = big.as_strided((3, 500), (far, 1), 3)
+        rows.copy_(getattr(c, name))
+        setattr(c, name, rows)
+    got = c.run(mx)
+    c.target, c.draft = c.target.clone(), c.draft.clone()
+    c.check(got)
+
+
+def test_two_streams_at_once(mx):
+    """Every call has a workspace of its own."""
+    cases = [Case([30] * 6, 40001, torch.bfloat16, True, True, seed=k) for k in range(2)]
+    want = [c.run(mx) for c in cases]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    got = [[], []]
+    for _ in range(10):
+        for k, c in enumerate(cases):
+            with torch.cuda.stream(streams[k]):
+                got[k].append(c.run(mx))
+    torch.cuda.synchronize()
+    for k in range(2):
+        for g in got[k]:
+            assert all(torch.equal(a, b) for a, b in zip(g, want[k]))
+
+
 def test_results_repeat(mx):
     c = Case([40] * 8, 50001, torch.bfloat16, True, True, seed=12)
     first = c.run(mx)
