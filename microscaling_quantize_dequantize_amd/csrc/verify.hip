@@ -50,33 +50,42 @@ template <typename T> struct Chunk {
   static constexpr int N = 16 / sizeof(T);
   T v[N];
 } __attribute__((aligned(16)));
+template <typename T> struct Loose {  // the same at any element
+  T v[16 / sizeof(T)];
+} __attribute__((packed, aligned(sizeof(T))));
 
-// A node's rows, cut at 16-byte boundaries: chunk k holds the entries k N - off ..., of which those outside 0 .. vocab
-// are zero; the chunks whole0 .. whole1 have none of these.  DRAFT: there is a row q, which is cut like p; wide says that
-// it lies to the boundaries as p does.
+// A node's rows, cut where the target's has 16-byte boundaries: chunk k holds the entries k N - off ..., of which those
+// outside 0 .. vocab are zero; the chunks whole0 .. whole1 have none of these.  DRAFT: there is a row q, whose chunks may
+// lie across boundaries (one load all the same).
 template <typename T, bool DRAFT> struct Rows {
   static constexpr int N = Chunk<T>::N;
   const T *p, *q;
   int vocab, off, chunks, whole0, whole1;
-  bool wide;
 
   __device__ __forceinline__ Rows(const VerifyArgs &a, int64_t row) {
     p = (const T *)a.target + row * a.target_stride;
-    q = DRAFT ? (const T *)a.draft + row * a.draft_stride : nullptr;
+    q = DRAFT ? (const T *)a.draft + row * a.draft_stride : p;
     vocab = a.vocab;
     off = (int)((uintptr_t)p % 16 / sizeof(T));
-    wide = !DRAFT || (uintptr_t)q % 16 / sizeof(T) == (unsigned)off;
     chunks = (vocab + off + N - 1) / N;
     whole0 = off > 0;
     whole1 = (vocab + off) / N;
   }
-  __device__ __forceinline__ Chunk<T> read(const T *x, int k, bool whole) const {
-    Chunk<T> c;
+  // A chunk that is whole.
+  __device__ __forceinline__ void read_whole(int64_t k, Chunk<T> &cp, Chunk<T> &cq) const {
+    const int64_t e = k * N - off;
+    cp = *(const Chunk<T> *)(p + e);
+    if (DRAFT) cq = __builtin_bit_cast(Chunk<T>, *(const Loose<T> *)(q + e));
+  }
+  __device__ __forceinline__ void read(int k, Chunk<T> &cp, Chunk<T> &cq) const {
+    if (k >= whole0 && k < whole1) return read_whole(k, cp, cq);
     const int64_t e = (int64_t)k * N - off;
-    if (whole && k >= whole0 && k < whole1) return *(const Chunk<T> *)(x + e);
 #pragma unroll
-    for (int i = 0; i < N; ++i) c.v[i] = e + i >= 0 && e + i < vocab ? x[e + i] : T(0);
-    return c;
+    for (int i = 0; i < N; ++i) {
+      const bool in = e + i >= 0 && e + i < vocab;
+      cp.v[i] = in ? p[e + i] : T(0);
+      if (DRAFT) cq.v[i] = in ? q[e + i] : T(0);
+    }
   }
 };
 
@@ -163,32 +172,25 @@ __device__ __forceinline__ double add_weights(const Rows<T, DRAFT> &rows, const 
 #pragma unroll
     for (int i = 0; i < N; ++i) sum += w[i];
   };
-  auto add_any = [&](int k) {
-    const Chunk<T> p = rows.read(rows.p, k, true);
-    add(k, p, DRAFT ? rows.read(rows.q, k, rows.wide) : p);
+  auto add_cut = [&](int k) {
+    Chunk<T> p, q;
+    rows.read(k, p, q);
+    add(k, p, q);
   };
-  if (rows.wide) {
-    const int k0 = from > rows.whole0 ? from : rows.whole0, k1 = to < rows.whole1 ? to : rows.whole1;
-    const Chunk<T> *ps = (const Chunk<T> *)(rows.p - rows.off), *qs = (const Chunk<T> *)(rows.q - rows.off);
-    for (int64_t k = k0 + (int64_t)lane; k < k1; k += UNROLL * lanes) {
-      Chunk<T> p[UNROLL], q[UNROLL];
+  const int k0 = from > rows.whole0 ? from : rows.whole0, k1 = to < rows.whole1 ? to : rows.whole1;
+  for (int64_t k = k0 + (int64_t)lane; k < k1; k += UNROLL * lanes) {
+    Chunk<T> p[UNROLL], q[UNROLL];
 #pragma unroll
-      for (int u = 0; u < UNROLL; ++u) {
-        // behind the end the last chunk, which is not added: no load waits for a branch
-        const int64_t at = k + u * lanes < k1 ? k + u * lanes : k1 - 1;
-        p[u] = ps[at];
-        if (DRAFT) q[u] = qs[at];
-      }
+    for (int u = 0; u < UNROLL; ++u)
+      // behind the end the last chunk, which is not added: no load waits for a branch
+      rows.read_whole(k + u * lanes < k1 ? k + u * lanes : k1 - 1, p[u], q[u]);
 #pragma unroll
-      for (int u = 0; u < UNROLL; ++u)
-        if (k + u * lanes < k1) add((int)k + u * lanes, p[u], q[u]);
-    }
-    // the ends, if they are cut (one lane each)
-    if (lane == 0 && from < rows.whole0 && to > 0) add_any(0);
-    if (lane == lanes - 1 && to > rows.whole1 && to > rows.whole0 && from <= rows.whole1) add_any(rows.whole1);
-  } else {
-    for (int64_t k = from + (int64_t)lane; k < to; k += lanes) add_any((int)k);
+    for (int u = 0; u < UNROLL; ++u)
+      if (k + u * lanes < k1) add((int)k + u * lanes, p[u], q[u]);
   }
+  // the ends, if they are cut (one lane each)
+  if (lane == 0 && from < rows.whole0 && to > 0) add_cut(0);
+  if (lane == lanes - 1 && to > rows.whole1 && to > rows.whole0 && from <= rows.whole1) add_cut(rows.whole1);
   return sum;
 }
 
@@ -539,9 +541,7 @@ __device__ __forceinline__ void pick(const VerifyArgs &a, const Space &space, in
     Chunk<T> p[HELD], q[HELD];
 #pragma unroll
     for (int h = 0; h < HELD; ++h) {
-      const int at = k + h < l ? k + h : l - 1;
-      p[h] = rows.read(rows.p, at, true);
-      if (DRAFT) q[h] = rows.read(rows.q, at, rows.wide);
+      rows.read(k + h < l ? k + h : l - 1, p[h], q[h]);
     }
 #pragma unroll
     for (int h = 0; h < HELD; ++h) {
@@ -558,8 +558,9 @@ __device__ __forceinline__ void pick(const VerifyArgs &a, const Space &space, in
   bool done = false;
   for (int k = f; k < l && !done; ++k) {
     double w[N];
-    const Chunk<T> p = rows.read(rows.p, k, true);
-    weigh<T, DRAFT>(rows, taken, k, p, DRAFT ? rows.read(rows.q, k, rows.wide) : p, w);
+    Chunk<T> p, q;
+    rows.read(k, p, q);
+    weigh<T, DRAFT>(rows, taken, k, p, q, w);
 #pragma unroll
     for (int i = 0; i < N; ++i) {
       sum += w[i];

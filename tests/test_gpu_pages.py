@@ -415,24 +415,20 @@ def test_two_caches_on_two_streams(mx):
         cache = cache_of(mx, k, 300, 2, 16, 64, seed=k)
         refs, table, lens = [0] * 300, [[-1] * 9 for _ in range(5)], [100, 33, 64, 7, 144]
         resize(refs, table, lens, 16)
-        both.append((cache, refs, table, lens, snapshot(cache), torch.cuda.Stream()))
+        args = i32(refs), grid(table), i32(lens), i32([4, 4, 0, 1, 2, 2])
+        both.append((cache, refs, table, lens, snapshot(cache), args, i32([0] * 6), torch.cuda.Stream()))
     torch.cuda.synchronize()
-    got = []
+    last = [None, None]
     for turn in range(4):
-        for cache, refs, table, lens, data, s in both:
-            with torch.cuda.stream(s):
-                if turn == 0:
-                    got.append((i32(refs), grid(table), i32(lens), i32([4, 4, 0, 1, 2, 2]), i32([0] * 6)))
-                r, t, n, p, none = got[0 if cache is both[0][0] else 1]
-                child, _ = mx.mx_cache_fork(cache, r, t, n, p)
+        for k, (cache, _, _, _, _, args, none, stream) in enumerate(both):
+            with torch.cuda.stream(stream):
+                last[k], _ = mx.mx_cache_fork(cache, *args)
                 if turn < 3:
-                    mx.mx_cache_resize(cache, r, child, none)
-                else:
-                    got.append(child)
+                    mx.mx_cache_resize(cache, args[0], last[k], none)
     torch.cuda.synchronize()
-    for k, (cache, refs, table, lens, data, s) in enumerate(both):
-        want, _ = fork(refs, table, lens, [4, 4, 0, 1, 2, 2], 16, data)
-        assert got[2 + k].tolist() == want and got[k][0].tolist() == refs
+    for k, (cache, refs, table, lens, data, args, _, _) in enumerate(both):
+        want, _ = fork(refs, table, lens, args[3].tolist(), 16, data)
+        assert last[k].tolist() == want and args[0].tolist() == refs
         same(cache, data)
 
 
