@@ -27,8 +27,8 @@
 // the weights at its end in shares of 1024 entries; k_pick finds the token in one
 // of them, with one wave.  Short rows are one workgroup's, which does both.
 //
-// Bound: HBM for large batches (64 rows of p and q of 128001 entries in fp32: 13 us
-// of k_sums, 5 TB/s, and 6 of k_pick on MI355X); else the chain of dependent loads
+// Bound: HBM for large batches (64 rows of p and q of 128001 entries in fp32: 12.7 us
+// of k_sums, 5.2 TB/s, and 4.9 of k_pick on MI355X); else the chain of dependent loads
 // (starts, tokens, points of rows, rows, sums: 6 us for small rows); of a node with
 // several refused children the vector units of its one CU: 7 fp64 instructions an
 // entry, 5 us a refusal for 50001 entries and 10 for 128000, whatever their type.
