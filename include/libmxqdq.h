@@ -409,9 +409,15 @@ MX_API int mx_cache_attention(const mx_cache *cache, const void *q,
 /*
  * Attention to another sequence's tokens (an encoder's states, the tokens of
  * images): as mx_cache_attention, but every query of sequence b sees all of its
- * kv_lens[b] tokens, whatever the number of its queries.  The workspace is that
- * of mx_cache_attention_workspace.
+ * kv_lens[b] tokens, whatever the number of its queries.  It has a workspace size
+ * of its own.
  */
+MX_API int64_t mx_cache_cross_attention_workspace(const mx_cache *cache,
+                                                  int64_t q_heads,
+                                                  int64_t batch,
+                                                  int64_t total_q,
+                                                  int64_t max_q,
+                                                  int64_t max_kv);
 MX_API int mx_cache_cross_attention(const mx_cache *cache, const void *q,
                                     int64_t q_token_stride,
                                     int64_t q_head_stride, int64_t q_heads,

@@ -63,6 +63,8 @@ _lib.mx_cache_write_axes.argtypes = [_vp, _vp, _i64, _i64, _vp, _i64, _i64, _vp,
                                      _int, _dbl]
 _lib.mx_cache_cross_attention.argtypes = [_vp, _vp, _i64, _i64, _i64, _vp, _vp, _i64, _vp, _i64, _i64, _i64, _i64, _i64,
                                           ctypes.c_float, _vp, _vp, _i64]
+_lib.mx_cache_cross_attention_workspace.argtypes = [_vp, _i64, _i64, _i64, _i64, _i64]
+_lib.mx_cache_cross_attention_workspace.restype = _i64
 _lib.mx_cache_copy.argtypes = [_vp, _vp, _vp, _i64]
 _lib.mx_cache_fork.argtypes = [_vp, _vp, _vp, _i64, _i64, _vp, _i64, _vp, _i64, _vp, _i64, _vp]
 _lib.mx_cache_resize.argtypes = [_vp, _vp, _vp, _i64, _i64, _vp, _i64, _vp]
@@ -677,7 +679,8 @@ def _attend(cache, q, q_starts, kv_lens, block_table, max_q, max_kv, tree, every
         _want(out, "out", torch.bfloat16, (total, heads, dim))
         _dev(out, "out")
     po = out.data_ptr()
-    need = _lib.mx_cache_attention_workspace(pc, heads, batch, total, max_q, max_kv)
+    need = (_lib.mx_cache_cross_attention_workspace if everything else _lib.mx_cache_attention_workspace)(
+        pc, heads, batch, total, max_q, max_kv)
     if need < 0:
         raise MXError(need)
     space = kv_lens.new_empty(need // 4) if need else None  # int32: 4 bytes each

@@ -362,13 +362,27 @@ MX_API int mx_cache_read(const mx_cache *cache, const int64_t *slots, int64_t to
   return launched(mx::launch_cache_read(view(cache), slots, tokens, k, v, tl_stream));
 }
 
-MX_API int64_t mx_cache_attention_workspace(const mx_cache *cache, int64_t q_heads, int64_t batch, int64_t total_q,
-                                            int64_t max_q, int64_t max_kv) {
+namespace {
+
+int64_t attention_space(const mx_cache *cache, int64_t q_heads, int64_t batch, int64_t total_q, int64_t max_q,
+                        int64_t max_kv, bool all) {
   const int st = check_attention(cache, q_heads, batch, total_q, max_q, max_kv);
   if (st) return st;
   if (max_q > total_q) max_q = total_q;
   return mx::attention_workspace(cache->fmt, cache->dim, cache->heads, (int)(q_heads / cache->heads), (int)batch,
-                                 total_q, max_q, max_kv, false);
+                                 total_q, max_q, max_kv, all);
+}
+
+}  // namespace
+
+MX_API int64_t mx_cache_attention_workspace(const mx_cache *cache, int64_t q_heads, int64_t batch, int64_t total_q,
+                                            int64_t max_q, int64_t max_kv) {
+  return attention_space(cache, q_heads, batch, total_q, max_q, max_kv, false);
+}
+
+MX_API int64_t mx_cache_cross_attention_workspace(const mx_cache *cache, int64_t q_heads, int64_t batch, int64_t total_q,
+                                                  int64_t max_q, int64_t max_kv) {
+  return attention_space(cache, q_heads, batch, total_q, max_q, max_kv, true);
 }
 
 namespace {

@@ -71,7 +71,14 @@ def test_cross_attention_refusals(b):
     for name in ("q", "starts", "lens", "table", "out"):
         assert attend(**{name: None}) == ENULL
     assert attend(q=A + 8) == EALIGN
-    assert attend(max_kv=100000, pages=8000, stride=8000, size=4) == EARG
+    space = b.raw().mx_cache_cross_attention_workspace
+    need = space(ctypes.addressof(keep), 4, 2, 2, 1, 100000)
+    assert need > 0
+    assert attend(max_kv=100000, pages=8000, stride=8000, size=need - 1) == EARG
+    assert attend(max_kv=100000, pages=8000, stride=8000, space=None) == ENULL
+    assert attend(max_kv=100000, pages=8000, stride=8000, space=A + 8) == EALIGN
+    assert space(ctypes.addressof(keep), 4, 0, 0, 0, 1000) == 0
+    assert space(ctypes.addressof(struct(b, dim=32)), 4, 2, 2, 1, 64) == EARG
     assert attend(total=0, q=None, out=None) == OK
 
 
@@ -186,7 +193,10 @@ def test_binding_axes(mx):
         mx.mx_cache_write(cache, x, x, ints(5), positions=ints(5), inv_freq=f, axes=ints(32, dtype=I32))
 
 
-def test_binding_cross_attention(mx):
+def test_binding_cross_attention(mx, monkeypatch):
+    real = mx._lib.real
+    monkeypatch.setattr(NoCompute, "mx_cache_cross_attention_workspace",
+                        property(lambda self: real.mx_cache_cross_attention_workspace), raising=False)
     cache = mx.MXCache.allocate(1, 2, 3, 16, 64, device="cpu")
     good = dict(q=bf(4, 6, 64), q_starts=ints(3, dtype=I32), kv_lens=ints(2, dtype=I32),
                 block_table=ints(2, 2, dtype=I32), max_q=2, max_kv=20)

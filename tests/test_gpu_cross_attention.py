@@ -56,6 +56,15 @@ def test_splits_and_ragged(mx, fmt, dim, group, nq):
     assert not bool(out[nq + 2:nq + 5].any())
 
 
+@pytest.mark.parametrize("fmt,dim,group,nq,kv", [(1, 64, 1, 200, 3000), (0, 128, 4, 60, 2000), (1, 96, 1, 300, 4096),
+                                                 (1, 64, 2, 1, 4000), (0, 256, 2, 70, 2500)])
+def test_few_sequences_of_some_thousand_tokens(mx, fmt, dim, group, nq, kv):
+    """Divided calls below the length from which all calls are divided: their blocks, and so their workspace, are not
+    those of the causal calls."""
+    c = Case(mx, fmt, 2, group, dim, 64, [kv, kv // 3], [nq, nq], seed=kv)
+    check(c, run(mx, c))
+
+
 def test_bounds_scale_and_padding(mx):
     c = Case(mx, 1, 2, 2, 64, 16, [400, 70, 9], [20, 3, 1], seed=2)
     check(c, run(mx, c, scale=0.3), scale=0.3)
