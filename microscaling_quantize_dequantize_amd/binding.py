@@ -495,20 +495,7 @@ class _Rope(torch.autograd.Function):
         if grad.stride(2) != 1:  # that of a sum, say, is one value for all
             grad = grad.contiguous()
         positions, inv_freq, axes = ctx.saved_tensors
-        if torch.is_grad_enabled():  # the gradient is recorded in its turn
-            return (mx_rope(grad, positions, inv_freq, layout, scale, not inverse, axes=axes),) + (None,) * 6
-        # what forward has checked is not checked again: in autograd's thread Python takes three times as long
-        ps, st, sh = _heads(grad, "the gradient", (grad.dtype,))
-        tokens, heads, dim = grad.shape
-        dst = _like(grad)
-        at = (positions.data_ptr(),)
-        if axes is not None:
-            at += positions.stride(0), positions.shape[0], axes.data_ptr()
-        _stream()
-        call = _lib.mx_rope if axes is None else _lib.mx_rope_axes
-        _call(call(ps, st, sh, _DTYPE[grad.dtype], tokens, heads, dim, *at, inv_freq.data_ptr(), 2 * inv_freq.shape[0],
-                   layout, scale, 0 if inverse else 1, dst.data_ptr(), heads * dim, dim))
-        return dst, None, None, None, None, None, None
+        return (mx_rope(grad, positions, inv_freq, layout, scale, not inverse, axes=axes),) + (None,) * 6
 
 
 class _CacheStruct(ctypes.Structure):
