@@ -111,7 +111,7 @@ __device__ __forceinline__ u32x4 rotate8(const unsigned short *x, u32x4 w, u32x4
 constexpr int WRITE_ROWS = 4;
 
 // VEC: 16-byte loads (strides and pointers allow them).  ALIGNED: half layout whose partners are whole pieces.
-template <int FMT, int LAYOUT, bool VEC, bool ALIGNED>
+template <int FMT, int LAYOUT, bool VEC, bool ALIGNED, bool AXES>
 __global__ __launch_bounds__(WRITE_THREADS) void k_cache_write(WriteArgs a) {
   __shared__ double tc[WRITE_TABLE], ts[WRITE_TABLE];
   const CacheView &cv = a.cache;
@@ -124,7 +124,7 @@ __global__ __launch_bounds__(WRITE_THREADS) void k_cache_write(WriteArgs a) {
   for (int i = threadIdx.x; i < nt * half; i += WRITE_THREADS) {
     const int t = i / half, p = i - t * half;
     double s, c;
-    sine_cosine(position_of(a.positions, t0 + t, p) * a.inv_freq[p], s, c);
+    sine_cosine(position_of<AXES>(a.positions, t0 + t, p) * a.inv_freq[p], s, c);
     tc[i] = c * a.scale;
     ts[i] = s * a.scale;
   }
@@ -184,6 +184,12 @@ __global__ __launch_bounds__(WRITE_THREADS) void k_cache_write(WriteArgs a) {
   }
 }
 
+template <int FMT, int LAYOUT, bool VEC, bool ALIGNED>
+static void write_start(dim3 grid, const WriteArgs &a, hipStream_t stream) {
+  if (a.positions.axes) k_cache_write<FMT, LAYOUT, VEC, ALIGNED, true><<<grid, WRITE_THREADS, 0, stream>>>(a);
+  else k_cache_write<FMT, LAYOUT, VEC, ALIGNED, false><<<grid, WRITE_THREADS, 0, stream>>>(a);
+}
+
 hipError_t launch_cache_write(const CacheView &cache, const void *k, const int64_t k_strides[2], const void *v,
                               const int64_t v_strides[2], const int64_t *slots, int64_t tokens,
                               const Positions &positions, const double *inv_freq, int64_t rot, int layout, double scale,
@@ -199,7 +205,7 @@ hipError_t launch_cache_write(const CacheView &cache, const void *k, const int64
   const dim3 grid((unsigned)tiles, (unsigned)((cache.heads + a.heads_per_wg - 1) / a.heads_per_wg), 2);
   bool vec = ((uintptr_t)k | (uintptr_t)v) % 16 == 0;
   for (int i = 0; i < 2; ++i) vec = vec && k_strides[i] % 8 == 0 && v_strides[i] % 8 == 0;
-#define MX_WRITE(F, L, V, A) k_cache_write<F, L, V, A><<<grid, WRITE_THREADS, 0, stream>>>(a)
+#define MX_WRITE(F, L, V, A) write_start<F, L, V, A>(grid, a, stream)
 #define MX_FORMAT(F)                                                        \
   if (layout == ROTARY_INTERLEAVED) {                                       \
     if (vec) MX_WRITE(F, ROTARY_INTERLEAVED, true, false);                  \

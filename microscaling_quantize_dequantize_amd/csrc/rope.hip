@@ -10,11 +10,9 @@
 // angles are formed once for each (token, pair) in fp64, rounded once to fp32
 // and kept in LDS for all heads of the token, whose pairs are rotated in fp32
 // whatever the type of x.  Measured on MI355X: 8192 x 64 heads of 128 in bf16
-// 43-45 us, 6.1 TB/s; in fp32 104 us, 5.2 TB/s; 8192 x 28 heads of 128 with three
-// axes in bf16 21.5 us, 5.5 TB/s; 4111 x 16 heads of 96 in fp32 10.3 us, 4.9 TB/s; 8
-// tokens 3.5 us.  Asking for positions and frequencies before the rows took 6% off
-// (48.4 to 45.4 and 23.3 to 22.0 us a call): loads come back in order, so an angle
-// behind the rows waited for them.
+// 43.5 us, 6.2 TB/s (44.5 on inputs that change from call to call); in fp32 104 us,
+// 5.2 TB/s; 8192 x 28 heads of 128 with three axes in bf16 21.5 us (24 where inputs
+// change), 5.5 TB/s; 4111 x 16 heads of 96 in fp32 9.7 us, 5.2 TB/s; 8 tokens 3.4 us.
 //
 // Split: a workgroup owns whole tokens (one, or several while their heads are
 // few), a thread VEC neighbouring pairs of one head, so that both elements of
@@ -46,7 +44,9 @@ __device__ __forceinline__ void from_f32(float &d, float f) { d = f; }
 constexpr int ROPE_ROWS = 2;  // rows whose loads a thread has under way together, the first ones before the angles
 
 // src and dst may be one tensor (no __restrict__): a thread reads all of a piece's pairs before it writes them.
-template <typename T, int VEC, int LAYOUT>
+// AXES is a template argument, as a branch in every angle made calls without axes 2 to 5% slower (k_rope_staged 68.4 us
+// for 65.7, k_cache_write of 64 tokens 4.4 for 4.1).
+template <typename T, int VEC, int LAYOUT, bool AXES>
 __global__ __launch_bounds__(ROPE_THREADS) void k_rope(const T *src, T *dst, RopeArgs a) {
   __shared__ float tc[ROPE_TABLE], ts[ROPE_TABLE];
   // items of a head: pieces of VEC pairs (HALF and single pairs) or of VEC elements, then the pieces that are copied
@@ -119,19 +119,21 @@ __global__ __launch_bounds__(ROPE_THREADS) void k_rope(const T *src, T *dst, Rop
     }
   };
 
-  // what the first angle takes is asked for before the rows: loads come back in their order, and the angle is formed
-  // while the rows are on their way
+  // With axes a position is a load behind a load, and loads come back in their order: what the first angle takes is asked
+  // for before the rows, and the angle is formed while these are on their way (8192 x 28 heads of 128 in bf16 23.6 us
+  // against 25.1).  Without, the rows are better first (8192 x 64 heads 44.5 against 47.5, 4111 x 16 of 96 in fp32 9.6
+  // and 10.0).
   double at = 0.0, per = 0.0;
   auto ask = [&](int i) {
     const int t = i / a.half, p = i - t * a.half;
-    at = position_of(a.positions, t0 + t, p);
+    at = position_of<AXES>(a.positions, t0 + t, p);
     per = a.inv_freq[p];
   };
   const int angles = nt * a.half;
-  if ((int)threadIdx.x < angles) ask(threadIdx.x);
+  if (AXES && (int)threadIdx.x < angles) ask(threadIdx.x);
   if (active) load(item0, first);
   for (int i = threadIdx.x; i < angles; i += ROPE_THREADS) {
-    if (i != (int)threadIdx.x) ask(i);
+    if (!AXES || i != (int)threadIdx.x) ask(i);
     double s, c;
     sine_cosine(at * per, s, c);
     tc[i] = (float)(c * a.scale);
@@ -150,7 +152,7 @@ __global__ __launch_bounds__(ROPE_THREADS) void k_rope(const T *src, T *dst, Rop
 // partners of its elements out of LDS, where the workgroup has put the rows' pieces.  (62 of 128 dimensions of 8192 x
 // 64 heads in bf16: 66-69 us; 140 in pieces of single pairs; 43 with whole pieces.)  Every row is in LDS before any of
 // it is written, so dst may be src.
-template <typename T, int VEC>
+template <typename T, int VEC, bool AXES>
 __global__ __launch_bounds__(ROPE_THREADS) void k_rope_staged(const T *src, T *dst, RopeArgs a) {
   __shared__ float tc[ROPE_TABLE], ts[ROPE_TABLE];
   __shared__ Piece<T, VEC> rows[2][ROPE_THREADS];
@@ -159,7 +161,7 @@ __global__ __launch_bounds__(ROPE_THREADS) void k_rope_staged(const T *src, T *d
   for (int i = threadIdx.x; i < nt * a.half; i += ROPE_THREADS) {
     const int t = i / a.half, p = i - t * a.half;
     double s, c;
-    sine_cosine(position_of(a.positions, t0 + t, p) * a.inv_freq[p], s, c);
+    sine_cosine(position_of<AXES>(a.positions, t0 + t, p) * a.inv_freq[p], s, c);
     tc[i] = (float)(c * a.scale);
     ts[i] = (float)(a.inverse ? -s * a.scale : s * a.scale);
   }
@@ -199,13 +201,15 @@ __global__ __launch_bounds__(ROPE_THREADS) void k_rope_staged(const T *src, T *d
 template <typename T, int VEC, int LAYOUT>
 static void rope_start(const void *src, void *dst, const RopeArgs &a, hipStream_t stream) {
   const unsigned grid = (unsigned)((a.tokens + a.per_wg - 1) / a.per_wg);
-  k_rope<T, VEC, LAYOUT><<<grid, ROPE_THREADS, 0, stream>>>((const T *)src, (T *)dst, a);
+  if (a.positions.axes) k_rope<T, VEC, LAYOUT, true><<<grid, ROPE_THREADS, 0, stream>>>((const T *)src, (T *)dst, a);
+  else k_rope<T, VEC, LAYOUT, false><<<grid, ROPE_THREADS, 0, stream>>>((const T *)src, (T *)dst, a);
 }
 
 template <typename T, int VEC>
 static void rope_staged(const void *src, void *dst, const RopeArgs &a, hipStream_t stream) {
   const unsigned grid = (unsigned)((a.tokens + a.per_wg - 1) / a.per_wg);
-  k_rope_staged<T, VEC><<<grid, ROPE_THREADS, 0, stream>>>((const T *)src, (T *)dst, a);
+  if (a.positions.axes) k_rope_staged<T, VEC, true><<<grid, ROPE_THREADS, 0, stream>>>((const T *)src, (T *)dst, a);
+  else k_rope_staged<T, VEC, false><<<grid, ROPE_THREADS, 0, stream>>>((const T *)src, (T *)dst, a);
 }
 
 template <typename T, int LAYOUT>

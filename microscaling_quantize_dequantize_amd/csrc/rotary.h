@@ -7,9 +7,10 @@ namespace mx {
 
 enum RotaryLayout { ROTARY_HALF = 0, ROTARY_INTERLEAVED = 1 };
 
-// The position that turns a pair of a token; zero on an axis that there is not.
+// The position that turns a pair of a token; zero on an axis that there is not.  AXES: the pairs have axes.
+template <bool AXES>
 __device__ __forceinline__ double position_of(const Positions &p, int64_t token, int pair) {
-  if (p.axes == nullptr) return (double)p.at[token];
+  if constexpr (!AXES) return (double)p.at[token];
   const int axis = p.axes[pair];
   return (unsigned)axis < (unsigned)p.count ? (double)p.at[axis * p.stride + token] : 0.0;
 }
