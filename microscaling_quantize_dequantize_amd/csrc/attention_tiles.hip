@@ -76,9 +76,13 @@ __device__ __forceinline__ u32x4 read_v(const lds_u8 *p, int far) {
   return u32x4{a.x, a.y, b.x, b.y};
 }
 
-template <int FMT, int D, int WAVES>
+// ALL: with heads of more than 128 dimensions, what a.all is.  Asked at run time it takes registers that these have not
+// left (causal, 2 chunks of 1000 over 12000, heads of 256: a call 398 us, and 393 so); smaller heads are no quicker so
+// (of 96, 2 chunks of 500 over 5000: 81.6 us asked, 83.0 otherwise).
+template <int FMT, int D, int WAVES, bool ALL>
 __global__ __launch_bounds__(64 * WAVES, D <= 128 ? 2 : 1) void k_attention_tiles(AttentionArgs a, Division dv) {
   using T = Tiled<FMT, D, WAVES>;
+  if (D > 128) a.all = ALL;
   extern __shared__ __align__(16) uint8_t lds[];
   const CacheView &cv = a.cache;
   const int wave = uniform((int)threadIdx.x / 64), lane = threadIdx.x % 64, n32 = lane % 32, h = lane / 32;
@@ -360,21 +364,23 @@ __global__ __launch_bounds__(64 * WAVES, D <= 128 ? 2 : 1) void k_attention_tile
   zero_padding(a);
 }
 
-template <int FMT, int D, int WAVES>
+template <int FMT, int D, int WAVES, bool ALL>
 static hipError_t start(const AttentionArgs &a, const Division &d, hipStream_t stream) {
   using T = Tiled<FMT, D, WAVES>;
   const int64_t grid = d.workers ? d.workers : (int64_t)a.batch * a.cache.heads * d.blocks;
   static std::atomic<uint64_t> done{0};
-  const hipError_t e = allow_lds((const void *)k_attention_tiles<FMT, D, WAVES>, T::LDS, done);
+  const hipError_t e = allow_lds((const void *)k_attention_tiles<FMT, D, WAVES, ALL>, T::LDS, done);
   if (e != hipSuccess) return e;
-  k_attention_tiles<FMT, D, WAVES><<<(unsigned)grid, T::THREADS, T::LDS, stream>>>(a, d);
+  k_attention_tiles<FMT, D, WAVES, ALL><<<(unsigned)grid, T::THREADS, T::LDS, stream>>>(a, d);
   return hipGetLastError();
 }
 
 template <int FMT, int D>
 static hipError_t by_rows(const AttentionArgs &a, const Division &d, hipStream_t stream) {
-  if (d.rows == 128) return start<FMT, D, 4>(a, d, stream);
-  if constexpr (D <= 128) return start<FMT, D, 8>(a, d, stream);
+  if constexpr (D > 128)
+    if (d.rows == 128 && a.all) return start<FMT, D, 4, true>(a, d, stream);
+  if (d.rows == 128) return start<FMT, D, 4, false>(a, d, stream);
+  if constexpr (D <= 128) return start<FMT, D, 8, false>(a, d, stream);
   return hipErrorInvalidValue;
 }
 
