@@ -7,17 +7,17 @@ namespace mx {
 // Joins the pieces of items: out = sum_s 2^(m_s - m) o_s / sum_s 2^(m_s - m) l_s, in the order of the workers.
 //
 // A lane has four dimensions of a row, so that its pieces come in loads of 16 bytes, and a wave several rows side by side;
-// a workgroup of four waves has join_rows() rows of an item, all of whose first loads are under way together.  (A wave
-// with one row at a time, its lanes two dimensions apart: 29 us against 14 for 248 items of 256 rows, heads of 128, in two or three pieces.)
-constexpr int JOIN_PASSES = 2;  // four: 29.6 us against 28.4 for 16 small trees, whose rows are few
+// a workgroup of four waves has join_rows() rows of an item, P of them for each lane, all of whose first loads are under
+// way together.  (A wave with one row at a time, its lanes two dimensions apart: 29 us against 14 for 248 items of 256
+// rows, heads of 128, in two or three pieces.)
 constexpr int join_side(int dim) { return 64 / (dim / 4); }  // rows of a wave's pass
-constexpr int join_rows(int dim) { return 4 * JOIN_PASSES * join_side(dim); }
+constexpr int join_rows(int dim, int passes) { return 4 * passes * join_side(dim); }
 
-template <int D, bool BY_WORKER>
+template <int D, bool BY_WORKER, int P>
 __global__ __launch_bounds__(256) void k_join(AttentionArgs a, Division dv, int row_groups) {
-  constexpr int LANES = D / 4, SIDE = join_side(D), P = JOIN_PASSES;
+  constexpr int LANES = D / 4, SIDE = join_side(D);
   const int wave = uniform((int)threadIdx.x / 64), lane = threadIdx.x % 64;
-  const int at = blockIdx.x / row_groups, row0 = (blockIdx.x - at * row_groups) * join_rows(D);
+  const int at = blockIdx.x / row_groups, row0 = (blockIdx.x - at * row_groups) * join_rows(D, P);
   const Record rec = records_of(a, dv)[at];
   // the item's record is where it belongs, so its sequence is read without waiting for it
   const int item = BY_WORKER ? uniform(rec.part) : at;
@@ -49,7 +49,7 @@ __global__ __launch_bounds__(256) void k_join(AttentionArgs a, Division dv, int 
 #pragma unroll
     for (int p = 0; p < P; ++p) m[p] = fmaxf(m[p], ml[2 * r[p]]);
   }
-#pragma unroll 2
+#pragma unroll 4 / P
   for (int w = w0; w <= w1; ++w) {
     const float *ml = part_stats(a, dv, slot(w), D), *o = part_sums(a, dv, slot(w), D) + d;
 #pragma unroll
@@ -149,9 +149,18 @@ static hipError_t join(const AttentionArgs &a, const Division &d, hipStream_t st
   if (d.workers / d.records >= 8 && d.records * most <= 2 * device_cu_count()) {
     k_join_wide<D><<<d.records * most, 1024, 0, stream>>>(a, d, most);
   } else {
-    const int groups = (most + join_rows(D) - 1) / join_rows(D);
-    if (d.by_worker) k_join<D, true><<<d.records * groups, 256, 0, stream>>>(a, d, groups);
-    else k_join<D, false><<<d.records * groups, 256, 0, stream>>>(a, d, groups);
+    // Two passes of rows a wave, but one for the few rows of single tokens and small trees, whose loads are spread over more
+    // workgroups so (heads of 128: 64 sequences of one token, 4 rows each, 6.0 us and 6.7 with two; blocks of 256 rows 11.6
+    // and 10.6).
+    const int passes = most <= 32 ? 1 : 2;
+    const int groups = (most + join_rows(D, passes) - 1) / join_rows(D, passes), grid = d.records * groups;
+    if (passes == 1) {
+      if (d.by_worker) k_join<D, true, 1><<<grid, 256, 0, stream>>>(a, d, groups);
+      else k_join<D, false, 1><<<grid, 256, 0, stream>>>(a, d, groups);
+    } else {
+      if (d.by_worker) k_join<D, true, 2><<<grid, 256, 0, stream>>>(a, d, groups);
+      else k_join<D, false, 2><<<grid, 256, 0, stream>>>(a, d, groups);
+    }
   }
   return hipGetLastError();
 }
