@@ -229,6 +229,43 @@ __global__ __launch_bounds__(TAKE_THREADS) void k_pages_small(BookArgs a) {
   if (t < a.out_rows) a.missing[t] = lacks[t] + beyond(a, rows[t]);
 }
 
+// Some row has a page behind one that it lacks: all entries are gone over.
+__device__ __forceinline__ void take_holes(const BookArgs &a, FreePages<TAKE_ITEMS> &free, int *waves) {
+  const int t = threadIdx.x;
+  const int64_t entries = (int64_t)a.out_rows * a.cols;
+  for (int64_t base = 0; base < entries; base += TAKE_THREADS * TAKE_ITEMS) {
+    int *place[TAKE_ITEMS], *miss[TAKE_ITEMS];
+    int wants = 0, total;
+#pragma unroll
+    for (int k = 0; k < TAKE_ITEMS; ++k) {
+      const int64_t e = base + t * TAKE_ITEMS + k;
+      place[k] = nullptr;
+      if (e >= entries) continue;
+      const int r = entries >> 32 ? (int)(e / a.cols) : (int)((unsigned)e / (unsigned)a.cols);
+      miss[k] = a.missing + r;
+      if (a.missing[r] == 0) continue;
+      const Row row = row_of<false>(a, r);
+      const int64_t j = e - (int64_t)r * a.cols;
+      int *at = a.out + (int64_t)r * a.out_stride + j;
+      if (j >= row.need || *at != -1) continue;
+      place[k] = at;
+      ++wants;
+    }
+    int rank = block_prefix(wants, waves, total);
+    free.find(a, total, waves);
+#pragma unroll
+    for (int k = 0; k < TAKE_ITEMS; ++k) {
+      if (place[k] == nullptr) continue;
+      const int page = free[rank++];
+      if (page < 0) continue;
+      *place[k] = page;
+      a.refs[page] = 1;
+      atomicSub(miss[k], 1);
+    }
+    free.drop(total);
+  }
+}
+
 // One workgroup hands out pages, to the entries that lack one in the order of rows and columns.  Of rows of a fork that is
 // the one behind the full pages; of others as a rule the last ones that the row needs, which is looked at first.
 template <bool FORK>
@@ -267,72 +304,37 @@ __global__ __launch_bounds__(TAKE_THREADS) void k_page_take(BookArgs a) {
     r = row0 + lo;
     return a.out + (int64_t)r * a.out_stride + (end[lo] - (before[lo + 1] - rank));
   };
-  bool tails = true, none = true;
-  for (int row0 = 0; row0 < a.out_rows && tails; row0 += TAKE_THREADS) {
-    const int total = look(row0);
-    none = none && total == 0;
-    bool other = false;
-    if (!FORK)
+  if constexpr (!FORK) {
+    bool tails = true, none = true;
+    for (int row0 = 0; row0 < a.out_rows && tails; row0 += TAKE_THREADS) {
+      const int total = look(row0);
+      none = none && total == 0;
+      bool other = false;
       for (int rank = t; rank < total; rank += TAKE_THREADS) {
         int r;
         other |= *entry(row0, rank, r) != -1;
       }
-    tails = !__syncthreads_or(other);
-  }
-  if (tails) {
+      tails = !__syncthreads_or(other);
+    }
+    if (!tails) return take_holes(a, free, waves);
     if (none) return;
-    for (int row0 = 0; row0 < a.out_rows; row0 += TAKE_THREADS) {
-      const int total = look(row0);
-      for (int base = 0; base < total; base += TAKE_THREADS * TAKE_ITEMS) {
-        const int some = total - base < TAKE_THREADS * TAKE_ITEMS ? total - base : TAKE_THREADS * TAKE_ITEMS;
-        free.find(a, some, waves);
-        for (int rank = t; rank < some; rank += TAKE_THREADS) {
-          const int page = free[rank];
-          if (page < 0) continue;
-          int r;
-          *entry(row0, base + rank, r) = page;
-          a.refs[page] = 1;
-          atomicSub(a.missing + r, 1);
-        }
-        free.drop(some);
-      }
-      __syncthreads();  // before[] and end[] have been read
-    }
-    return;
   }
-
-  // some row has a page behind one that it lacks: all entries are gone over
-  const int64_t entries = (int64_t)a.out_rows * a.cols;
-  for (int64_t base = 0; base < entries; base += TAKE_THREADS * TAKE_ITEMS) {
-    int *place[TAKE_ITEMS], *miss[TAKE_ITEMS];
-    int wants = 0, total;
-#pragma unroll
-    for (int k = 0; k < TAKE_ITEMS; ++k) {
-      const int64_t e = base + t * TAKE_ITEMS + k;
-      place[k] = nullptr;
-      if (e >= entries) continue;
-      const int r = entries >> 32 ? (int)(e / a.cols) : (int)((unsigned)e / (unsigned)a.cols);
-      miss[k] = a.missing + r;
-      if (a.missing[r] == 0) continue;
-      const Row row = row_of<FORK>(a, r);
-      const int64_t j = e - (int64_t)r * a.cols;
-      int *at = a.out + (int64_t)r * a.out_stride + j;
-      if (j >= row.need || *at != -1) continue;
-      place[k] = at;
-      ++wants;
+  for (int row0 = 0; row0 < a.out_rows; row0 += TAKE_THREADS) {
+    const int total = look(row0);
+    for (int base = 0; base < total; base += TAKE_THREADS * TAKE_ITEMS) {
+      const int some = total - base < TAKE_THREADS * TAKE_ITEMS ? total - base : TAKE_THREADS * TAKE_ITEMS;
+      free.find(a, some, waves);
+      for (int rank = t; rank < some; rank += TAKE_THREADS) {
+        const int page = free[rank];
+        if (page < 0) continue;
+        int r;
+        *entry(row0, base + rank, r) = page;
+        a.refs[page] = 1;
+        atomicSub(a.missing + r, 1);
+      }
+      free.drop(some);
     }
-    int rank = block_prefix(wants, waves, total);
-    free.find(a, total, waves);
-#pragma unroll
-    for (int k = 0; k < TAKE_ITEMS; ++k) {
-      if (place[k] == nullptr) continue;
-      const int page = free[rank++];
-      if (page < 0) continue;
-      *place[k] = page;
-      a.refs[page] = 1;
-      atomicSub(miss[k], 1);
-    }
-    free.drop(total);
+    __syncthreads();  // before[] and end[] have been read
   }
 }
 
