@@ -453,7 +453,8 @@ MX_API int mx_cache_copy(const mx_cache *cache, const int32_t *src,
  * pages behind them are released first, in all rows, and their entries become
  * -1; then entries without a page get free ones.  missing [rows] int32: the
  * pages that a row needs and did not get, because none was free or the row is
- * too short.  rows up to 2^24 (MX_ESHAPE).
+ * too short.  rows up to 2^24; 1024 of them (or all, if fewer) have less than
+ * 2^31 entries (MX_ESHAPE).
  */
 MX_API int mx_cache_resize(const mx_cache *cache, int32_t *refs,
                            int32_t *block_table, int64_t table_stride,

@@ -457,6 +457,7 @@ MX_API int mx_cache_resize(const mx_cache *cache, int32_t *refs, int32_t *block_
                            int64_t table_pages, const int32_t *kv_lens, int64_t rows, int32_t *missing) {
   int st;
   if ((st = check_table(cache, rows, table_stride, table_pages))) return st;
+  if ((rows < mx::TAKE_ROWS ? rows : mx::TAKE_ROWS) * table_pages > INT32_MAX) return MX_ESHAPE;
   if (rows == 0) return MX_OK;
   if (!kv_lens || !missing || (table_pages > 0 && !block_table) || (cache->pages > 0 && !refs)) return MX_ENULL;
   if (!aligned(refs, 4) || !aligned(block_table, 4) || !aligned(kv_lens, 4) || !aligned(missing, 4)) return MX_EALIGN;

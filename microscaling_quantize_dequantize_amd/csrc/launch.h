@@ -105,6 +105,7 @@ hipError_t launch_cache_attention(const AttentionArgs &a, hipStream_t stream);
 
 // The cache's pages: tables [rows][pages] with rows `stride` apart, refs[page] holders of each page.
 constexpr int64_t MAX_FORKS = ((int64_t)1 << 23) - 1;    // heads of children: two workgroups of 256 threads each
+constexpr int64_t TAKE_ROWS = 1024;                      // rows whose missing pages are counted together, in 32 bits
 constexpr int64_t MAX_COPIES = MAX_GROUPS_256;           // a workgroup each at least
 constexpr int64_t MAX_COMPACT = ((int64_t)1 << 20) - 1;  // heads of sequences: four workgroups of 1024 threads each
 

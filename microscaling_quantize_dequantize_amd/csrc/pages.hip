@@ -87,7 +87,7 @@ __global__ __launch_bounds__(256) void k_page_rows(BookArgs a) {
   if (lane == 0) a.missing[r] = lack + beyond(a, row);
 }
 
-constexpr int TAKE_THREADS = 1024, TAKE_ITEMS = 4;  // entries of a table that a step of the workgroup looks at: 4096
+constexpr int TAKE_THREADS = (int)TAKE_ROWS, TAKE_ITEMS = 4;  // entries of a table that a step of the workgroup looks at: 4096
 constexpr int SCAN_ITEMS = 8, SKIP_ITEMS = 32;      // counts of holders: 8192, and 32768 where none is free
 constexpr int queue_of(int items) { return TAKE_THREADS * (items + SCAN_ITEMS); }  // pages, for steps of so many items a thread
 
