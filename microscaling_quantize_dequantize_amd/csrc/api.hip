@@ -524,7 +524,7 @@ int check_verify(int64_t batch, int64_t total_q, int64_t max_q, int64_t vocab) {
 MX_API int64_t mx_verify_workspace(int64_t batch, int64_t total_q, int64_t max_q, int64_t vocab) {
   const int st = check_verify(batch, total_q, max_q, vocab);
   if (st) return st;
-  return mx::verify_workspace((int)batch, (int)max_q, (int)vocab);
+  return mx::verify_workspace((int)batch, total_q, (int)vocab);
 }
 
 MX_API int mx_verify(const void *target, int64_t target_stride, const void *draft, int64_t draft_stride, int dtype,
@@ -541,7 +541,7 @@ MX_API int mx_verify(const void *target, int64_t target_stride, const void *draf
   if (!aligned(target, size) || !aligned(draft, size) || !aligned(tokens, 8) || !aligned(uniforms, 8) ||
       !aligned(q_starts, 4) || !aligned(parents, 4) || !aligned(counts, 4) || !aligned(path, 4) || !aligned(out, 8))
     return MX_EALIGN;
-  const int64_t need = mx::verify_workspace((int)batch, (int)max_q, (int)vocab);
+  const int64_t need = mx::verify_workspace((int)batch, total_q, (int)vocab);
   if (need > 0 && !workspace) return MX_ENULL;
   if (workspace_bytes < need) return MX_EARG;
   if (need > 0 && !aligned(workspace, 16)) return MX_EALIGN;

@@ -135,7 +135,7 @@ struct VerifyArgs {
   int batch, total_q, max_q, vocab;
 };
 
-int64_t verify_workspace(int batch, int max_q, int vocab);
+int64_t verify_workspace(int batch, int64_t total_q, int vocab);
 hipError_t launch_verify(int dtype, const VerifyArgs &a, hipStream_t stream);
 
 }  // namespace mx

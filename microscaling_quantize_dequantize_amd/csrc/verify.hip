@@ -217,14 +217,14 @@ struct Follow {
 };
 struct Space {
   End *ends;        // [batch]
-  Follow *follow;   // [batch][max_q], trees
-  int *gone;        // [batch][max_q], trees without a draft's rows: the node's token was taken from its parent's weights
+  Follow *follow;   // [total_q], trees
+  int *gone;        // [total_q], trees without a draft's rows: the node's token was taken from its parent's weights
   double *sums;     // [batch][shares]
 };
 
 int64_t ends_bytes(int batch) { return (int64_t)batch * (int64_t)sizeof(End); }
-int64_t follow_bytes(int batch, int max_q) { return (int64_t)batch * max_q * (int64_t)sizeof(Follow); }
-int64_t gone_bytes(int batch, int max_q) { return ((int64_t)batch * max_q * 4 + 7) / 8 * 8; }
+int64_t follow_bytes(int64_t total_q) { return total_q * (int64_t)sizeof(Follow); }
+int64_t gone_bytes(int64_t total_q) { return (total_q * 4 + 7) / 8 * 8; }
 
 // Whether the test of a point passes, with the weights as they are at first (what k_sums and k_branch ask alike).
 __device__ __forceinline__ bool passes(double u, double W, double q, double w) { return u * W * q < w; }
@@ -266,8 +266,8 @@ __global__ __launch_bounds__(BRANCH_THREADS) void k_branch(VerifyArgs a, Space s
   const int b = blockIdx.x / groups, group = blockIdx.x - b * groups, t = threadIdx.x;
   const Nodes nodes = nodes_of(a, b);
   if (nodes.count == 0) return;
-  Follow *follow = space.follow + (int64_t)b * a.max_q;
-  int *gone = space.gone + (int64_t)b * a.max_q;
+  Follow *follow = space.follow + nodes.first;
+  int *gone = space.gone + nodes.first;
 
   bool asked = false;  // this thread's node has a parent that may ask it
   first[t] = VERIFY_NODES;
@@ -399,7 +399,7 @@ __device__ __forceinline__ Taken taken_at(const VerifyArgs &a, const Space &spac
     if (lane == 0 && all) list[0] = (int)a.tokens[nodes.first + end.node + 1];
     taken.count = all;
   } else {
-    const int *gone = space.gone + (int64_t)b * a.max_q;
+    const int *gone = space.gone + nodes.first;
     for (int base = end.node + 1; base < nodes.count; base += 64) {
       const int i = base + lane;
       int64_t x = -1;
@@ -423,7 +423,7 @@ __device__ __forceinline__ End walk(const VerifyArgs &a, const Space &space, int
   int64_t *out = a.out + (int64_t)b * a.max_q;
   End end{0, 0, 0.0, 0.0};
   if (TREE) {
-    const Follow *follow = space.follow + (int64_t)b * a.max_q;
+    const Follow *follow = space.follow + nodes.first;
     for (int i = t; i < nodes.count; i += THREADS) next[i] = follow[i].next;
     __syncthreads();
     // what follows nodes that no walk reaches is not set, and not looked at
@@ -675,8 +675,8 @@ hipError_t verify(const VerifyArgs &a, const Space &space, hipStream_t stream) {
 
 }  // namespace
 
-int64_t verify_workspace(int batch, int max_q, int vocab) {
-  return ends_bytes(batch) + follow_bytes(batch, max_q) + gone_bytes(batch, max_q) +
+int64_t verify_workspace(int batch, int64_t total_q, int vocab) {
+  return ends_bytes(batch) + follow_bytes(total_q) + gone_bytes(total_q) +
          (int64_t)batch * cut_of(batch, vocab).shares * 8;
 }
 
@@ -685,8 +685,8 @@ hipError_t launch_verify(int dtype, const VerifyArgs &a, hipStream_t stream) {
   Space space;
   space.ends = (End *)at;
   space.follow = (Follow *)(at += ends_bytes(a.batch));
-  space.gone = (int *)(at += follow_bytes(a.batch, a.max_q));
-  space.sums = (double *)(at += gone_bytes(a.batch, a.max_q));
+  space.gone = (int *)(at += follow_bytes(a.total_q));
+  space.sums = (double *)(at += gone_bytes(a.total_q));
   return dtype == 1 ? verify<float>(a, space, stream) : verify<unsigned short>(a, space, stream);
 }
 
