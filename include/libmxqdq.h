@@ -441,9 +441,9 @@ MX_API int mx_cache_cross_attention(const mx_cache *cache, const void *q,
 
 /*
  * Copy whole pages, keys and values: page src[i] to page dst[i], i < count
- * (int32; count up to 2^24 - 1, MX_ESHAPE).  Pairs with a page outside the cache
- * are skipped.  The pages of dst are distinct and no other pair's source; the
- * bytes of one that is are undefined.
+ * (int32; count up to 2^24 - 1, MX_ESHAPE).  Pairs with a page outside the cache,
+ * or twice the same one, are skipped.  The pages of dst are distinct and no other
+ * pair's source; the bytes of one that is are undefined.
  */
 MX_API int mx_cache_copy(const mx_cache *cache, const int32_t *src,
                          const int32_t *dst, int64_t count);
@@ -469,7 +469,10 @@ MX_API int mx_cache_resize(const mx_cache *cache, int32_t *refs,
  * keep what they held, and so do all where the parent has no page there).  The
  * rest of the row is -1; so is all of it for a parent outside 0 .. rows - 1.
  * missing [children] int32: the pages that a child needs and does not hold.
- * children * cache->heads is below 2^23 (MX_ESHAPE).
+ * children * cache->heads is below 2^23 (MX_ESHAPE).  Caches that share a table
+ * and refs (the layers of a model) are forked in one call, with one of them; the
+ * others copy the last pages with mx_cache_copy, from the parents' rows to the
+ * children's.
  */
 MX_API int mx_cache_fork(const mx_cache *cache, int32_t *refs,
                          const int32_t *block_table, int64_t table_stride,

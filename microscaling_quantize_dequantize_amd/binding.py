@@ -696,7 +696,7 @@ def _rows(t, name: str) -> int:
 def mx_cache_copy(cache: MXCache, src: torch.Tensor, dst: torch.Tensor) -> None:
     """Copy whole pages, keys and values, from src to dst (int32 page numbers [pages]).  A page may be the source of
     several; those of dst are distinct and no sources (the bytes of one that is are not defined).  Pairs with a page
-    outside the cache are skipped."""
+    outside the cache, or twice the same one, are skipped."""
     pc = _cache(cache)
     n = _rows(src, "src")
     ps, pd = _vector(src, "src", torch.int32, n), _vector(dst, "dst", torch.int32, n)
@@ -732,7 +732,13 @@ def mx_cache_fork(cache: MXCache, refs: torch.Tensor, block_table: torch.Tensor,
 
     Returns the children's rows (int32 [children, pages], -1 where there is none; out if given, which is not
     block_table) and int32 [children], the pages that each child needs and does not hold.  A parent that there is not
-    gives an empty row."""
+    gives an empty row.
+
+    Layers whose caches share a table and refs are forked once, with the first one's cache; the others copy the last
+    pages that are not full, by the two tables:
+        last = (kv_lens[parents] // cache.page).clamp(max=pages - 1).long()[:, None]
+        src, dst = (t.gather(1, last)[:, 0] for t in (block_table[parents], rows))
+        mx_cache_copy(other, src, dst)  # a page that is shared, or that there is not, is passed over"""
     pc = _cache(cache)
     rows, children = _rows(kv_lens, "kv_lens"), _rows(parents, "parents")
     pl, pp = _vector(kv_lens, "kv_lens", torch.int32, rows), _vector(parents, "parents", torch.int32, children)
