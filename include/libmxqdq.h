@@ -513,7 +513,8 @@ MX_API int mx_cache_compact(const mx_cache *cache, const int32_t *kv_starts,
  * with tokens outside the vocabulary are passed over.
  *   target, draft  [total_q x vocab] in dtype, strides in elements: row c holds
  *              the probabilities after node c, and those that its children were
- *              drawn from.  vocab 1 to 2^30 (MX_ESHAPE).
+ *              drawn from, independently (siblings may have the same token).
+ *              vocab 1 to 2^30 (MX_ESHAPE).
  *   tokens     [total_q] int64; uniforms [total_q] fp64 in [0, 1).
  *   batch      up to 2^22 - 1 (MX_ESHAPE).
  *   parents    [total_q] int32: a node's parent by its place in the sequence

@@ -803,7 +803,8 @@ def mx_verify(target: torch.Tensor, tokens: torch.Tensor, uniforms: torch.Tensor
     Sequence b has the nodes q_starts[b] .. q_starts[b + 1] (int32 [batch + 1]): the first is its last settled token, the
     others are drafted (up to 1024 nodes in all).  tokens int64 [nodes] (the first one's is not read); target [nodes,
     vocabulary] (bf16 or fp32, any row stride): the target's probabilities after each node; draft, the same: the
-    distribution that the children of each node were drawn from, one by one; without it they count as certain.
+    distribution that the children of each node were drawn from, independently (siblings may be equal: drawn without
+    replacement they would give tokens that are not the target's); without it they count as certain.
     parents int32 [nodes]: each node's parent as its place in the sequence, below its own; without it each follows the
     one before (a chain).  uniforms float64 [nodes], in [0, 1): of a drafted node for its own test, of the first one for
     the token that is sampled.
