@@ -205,7 +205,17 @@ static Division divide(int rows, int64_t workers, int min_tiles, int heads, int 
   // Where all of a sequence's tokens are seen (states of an encoder, a few thousand as a rule) items are alike, and what a
   // division costs, `cost` tiles of a workgroup, is often more than the rounds of whole items lose.  (256 items of 224
   // rows, heads of 64: 44 us undivided and 58 divided for 1500 tokens, 80 and 91 for 3000; 64 such items 41 and 34, 73
-  // and 47; 512 items of one row 22 and 40, 35 and 58.)  Up to 4096 tokens: one long sequence may be among short ones.
+  // and 47.)  Up to 4096 tokens: one long sequence may be among short ones.
+  //
+  // Items of few rows are so never divided up to 2048 tokens, whatever the heads.  Single tokens in MXFP8, us a call whole
+  // and divided (all are whole up to 2048):
+  //   tokens                                512       1024       1500       2048
+  //   512 items of 1 row, heads of 64    11 / 18    16 / 29    21 / 29    25 / 38
+  //   512 items of 4, 128                17 / 25    26 / 35    36 / 46    45 / 54
+  //   512 items of 4, 256                36 / 37    56 / 57    93 / 93   110 / 110
+  //   64 items of 4, 128                 10 / 14    14 / 14    20 / 17    25 / 15
+  //   8 items of 4, 256                  14 / 16    21 / 16    30 / 20    33 / 16
+  // Few items with large heads lose by it: a tile's time grows with the head, the cost here does not.
   const int64_t rounds = (items + held - 1) / held;
   const bool whole = all && d.tiles <= WHOLE_TILES && (rounds * held - items) * d.tiles <= cost * held;
   d.workers = (d.tiles <= min_tiles || whole) && items < ((int64_t)1 << 32) / 512
@@ -230,7 +240,9 @@ Division attention_division_tiles(int dim, int heads, int group, int batch, int6
   // 128), for which heads of more than 128 dimensions have no registers.  One workgroup for every CU, or two of the
   // small ones (64 rows over 32768 tokens: 201 us against 309 with one), in runs of eight tiles at least: a piece costs
   // as much as seven of them (512 tokens 30 us against 45 in runs of two tiles).
-  // Whole items are better smaller: 320 of up to 224 rows, heads of 64, 1500 tokens 63 us and 84 in blocks of 256.
+  // Whole items are better smaller: 320 of up to 224 rows, heads of 64, 1500 tokens 63 us and 84 in blocks of 256; 96 of
+  // 800, 128, 1500 tokens 95 and 112.  So are most of those that are divided after all, but not all (32 of 2800, 128, 4000
+  // tokens 226 and 214).
   const bool small = all && max_kv <= WHOLE_TILES * TILE;
   const int rows = max_q * group <= 128 || dim > 128 || small ? 128 : 256;
   const int two = rows == 128 && dim <= 128;

@@ -539,8 +539,9 @@ hipError_t launch_cache_fork(const CacheView &cache, int *refs, const int *table
   return hipGetLastError();
 }
 
-// Copies of so many bytes are written past the caches, which they would empty: 94 MB take 32 us so and 41 otherwise, but
-// 18 MB that are compacted afterwards 33 with the compaction, and 26 out of the caches.
+// Copies of so many bytes are written past the caches, which they would empty: 94 MB (keys and values, read) take 32 us so
+// and 41 otherwise, 67 MB 20 and 30, 53 MB 16 and 22, 27 MB 9 either way.  What reads the copies at once has them from
+// memory then: with a compaction behind it a copy of 94 MB takes 105 us so and 82 otherwise, one of 27 MB 31 and 26.
 constexpr int64_t PAST_BYTES = (int64_t)64 << 20;
 
 hipError_t launch_cache_copy(const CacheView &cache, const int *src, const int *dst, int64_t count, hipStream_t stream) {

@@ -27,11 +27,13 @@
 // the weights at its end in shares of 1024 entries; k_pick finds the token in one
 // of them, with one wave.  Short rows are one workgroup's, which does both.
 //
-// Bound: HBM for large batches (64 rows of p and q of 128001 entries in fp32: 12.7 us
-// of k_sums, 5.2 TB/s, and 4.9 of k_pick on MI355X); else the chain of dependent loads
-// (starts, tokens, points of rows, rows, sums: 6 us for small rows); of a node with
-// several refused children the vector units of its one CU: 7 fp64 instructions an
-// entry, 5 us a refusal for 50001 entries and 10 for 128000, whatever their type.
+// Bound: HBM for large batches (64 rows of p and q of 128001 entries in fp32 on MI355X:
+// k_sums 14.4 us, 4.5 TB/s, on inputs that change from call to call, and 12.4, 5.3
+// TB/s, out of the last-level cache, which holds them; k_pick 4.9); else the chain of
+// dependent loads (starts, tokens, points of rows, rows, sums: 6 us for small rows); of
+// a node with several refused children the vector units of its one CU: 7 instructions
+// an entry (two medians, two conversions, three of fp64 arithmetic), 5 us a refusal
+// for 50001 entries and 10 for 128000, whatever their type.
 // (A refusal's sum in fp32 would be quicker, but its error would move every border
 // of the sample: one token in some thousand would be another.)
 #include "launch.h"
