@@ -428,8 +428,9 @@ __device__ __forceinline__ End walk(const VerifyArgs &a, const Space &space, int
     const Follow *follow = space.follow + nodes.first;
     for (int i = t; i < nodes.count; i += THREADS) next[i] = follow[i].next;
     __syncthreads();
-    // what follows nodes that no walk reaches is not set, and not looked at
-    for (int i = nodes.count > 0 ? next[0] : -1; i >= 0; i = next[i]) {
+    // what follows nodes that no walk reaches is not set, and not looked at.  A node's next one is behind it, unless
+    // starts that do not ascend give it to several sequences: then the walk ends.
+    for (int i = nodes.count > 0 ? next[0] : -1; i > end.node && i < nodes.count; i = next[i]) {
       end.node = i;
       ++end.kept;
       if (write && t == 0) {

@@ -171,3 +171,24 @@ def test_bushy_trees_of_many_sequences(mx, draft, batch):
     assert max(need) > 8 and sum(n > 4 for n in need) > batch // 2, need
     want = c.check(c.run(mx))
     assert int(want[0].max()) > 2  # and walks go on behind refused children
+
+
+@pytest.mark.parametrize("draft", [False, True])
+@pytest.mark.parametrize("vocab", [24, WIDE])
+def test_starts_that_do_not_ascend(mx, draft, vocab):
+    """Sequences that share nodes: what comes out is not defined, but it is a walk through places of the sequence."""
+    c = Case([40, 30, 50], vocab, tree=True, draft=draft, seed=5, noise=1.0)
+    c.q_starts = torch.tensor([0, 60, 20, 110, 7, 200, -5, 120], dtype=torch.int32, device="cuda")
+    counts, path, out = (t.cpu() for t in c.run(mx, max_q=64))
+    starts = c.q_starts.tolist()
+    for b in range(7):
+        first = max(starts[b], 0)
+        n = min(max(min(starts[b + 1], 120) - first, 0), 64)
+        k = int(counts[b])
+        assert (1 if n else 0) <= k <= n
+        places = path[b].tolist()
+        assert places[k:] == [-1] * (64 - k) and places[:k] == sorted(set(places[:k]))
+        if n:
+            assert places[0] == 0 and max(places) < n
+            assert out[b, :k - 1].tolist() == [int(c.tokens[first + i]) for i in places[1:k]]
+            assert -1 <= int(out[b, k - 1]) < vocab
